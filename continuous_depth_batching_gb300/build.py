@@ -34,6 +34,8 @@ SOURCES = [
     "gemm_tc.cu",
     "attention_noalloc.cu",
     "tmap.cu",
+    "sample.cu",
+    "ops.cu",
 ]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
