@@ -35,6 +35,7 @@ SOURCES = [
     "attention_noalloc.cu",
     "tmap.cu",
     "sample.cu",
+    "cache_ops.cu",
     "ops.cu",
 ]
 

@@ -1,0 +1,797 @@
+// The paged-cache operators of include/cdb_ops.h: the cache write (query / key
+// norm, rotation, e4m3 or bf16 store) and decode attention over the cache with
+// grouped heads.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "../../include/cdb.h"
+#include "cache_ops.h"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "tmap.h"
+
+namespace cdb {
+
+__device__ __forceinline__ void report(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// ---------------------------------------------------------------------------
+// Cache write.
+//
+// A streaming kernel: every element of qkv is read once and written once, so
+// HBM bounds it.  One CTA per row; groups of GW lanes take one head at a time,
+// 8 elements per lane (16-byte loads for bf16, two for fp32; the rotation's
+// partner elements sit rot_dim / 16 lanes away), so the sums of the norm and
+// the maximum of the quantisation are shuffles inside the group and a head is
+// never staged in memory.  Each lane keeps the (cos, sin) of its 8 elements in
+// registers over all heads of the row.
+// ---------------------------------------------------------------------------
+namespace cw {
+
+constexpr int kThreads = 256;
+
+template <int HD>
+struct Geo {
+  static constexpr int GW = HD / 8 <= 4 ? 4 : HD / 8 <= 8 ? 8 : 16;  // lanes of a group (hd 96: 12 of 16 work)
+  static constexpr int NG = kThreads / GW;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float* v) {
+  Chunk<float>::load(p, v);
+  Chunk<float>::load(p + 4, v + 4);
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
+  Chunk<__nv_bfloat16>::load(p, v);
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint4 u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return u;
+}
+
+template <typename T, int HD, bool Q8>
+__global__ void __launch_bounds__(kThreads) k_cache_write(cdb_cache_write_args a) {
+  using G = Geo<HD>;
+  pdl_wait();
+  pdl_trigger();
+  const int row = blockIdx.x;
+  const int g = threadIdx.x / G::GW, l = threadIdx.x % G::GW;
+  const int seq = a.seq[row];
+  if (seq < 0) return;  // padding
+  const cdb_paged_cache& c = a.cache;
+  const int pos = a.pos[row];
+  if (seq >= c.n_seqs || pos < 0 || pos >= c.max_blocks * 16 || (a.rope && pos >= a.rope_positions)) {
+    if (threadIdx.x == 0) report(a.status, CDB_OPS_BAD_ROW);
+    return;
+  }
+  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
+  const int blk = c.block_table[(size_t)seq * c.max_blocks + (pos >> 4)];
+  if (slot < 0 || slot >= c.n_kv_slots || blk < 0 || blk >= c.kv_blocks) {
+    if (threadIdx.x == 0) report(a.status, blk < 0 || blk >= c.kv_blocks ? CDB_OPS_BAD_BLOCK : CDB_OPS_BAD_SLOT);
+    return;
+  }
+  const bool on = l * 8 < HD;
+  // Groups of a warp may be at different kinds of heads: shuffles name their group's lanes only.
+  const uint32_t peers = (0xffffffffu >> (32 - G::GW)) << ((threadIdx.x & 31) / G::GW * G::GW);
+  const int H = a.n_heads, Hk = c.n_kv_heads, total = H + 2 * Hk;
+  // Rotation of this lane's 8 elements: low half (own index) or high half (index - rot/2).
+  const int rl = a.rope ? a.rot_dim / 16 : 0;  // lanes of one half
+  const bool low = l < rl, high = !low && l < 2 * rl;
+  float cs[8], sn[8];
+  if (low || high) {
+    const float4* t = reinterpret_cast<const float4*>(a.rope + ((size_t)pos * (a.rot_dim / 2) + (low ? l : l - rl) * 8) * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = t[i];
+      cs[2 * i] = v.x, sn[2 * i] = v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = v.w;
+    }
+  }
+  const T* src = reinterpret_cast<const T*>(a.qkv) + (size_t)row * a.ldqkv + l * 8;
+  // Cached element (kv half, head j) of this position starts at ((cell + kv Hk + j) 16 + pos % 16).
+  const size_t cell = ((size_t)blk * c.n_kv_slots + slot) * 2 * Hk;
+  const int peer = low ? l + rl : l - rl;  // lane holding the rotation's other element
+#pragma unroll 3
+  for (int h = g; h < total; h += G::NG) {
+    float v[8] = {};
+    if (on) load8<T>(src + (size_t)h * HD, v);
+    if (h < H + Hk) {
+      if (a.q_gain) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+        for (int o = G::GW / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o, G::GW);
+        const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+        if (on) {
+          float w[8];
+          load8<float>((h < H ? a.q_gain : a.k_gain) + l * 8, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
+        }
+      }
+      if (rl) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_sync(peers, v[e], peer & (G::GW - 1), G::GW);
+          float x, y;
+          if (low) {
+            rope_pair(v[e], o, make_float2(cs[e], sn[e]), x, y);
+            v[e] = x;
+          } else if (high) {
+            rope_pair(o, v[e], make_float2(cs[e], sn[e]), x, y);
+            v[e] = y;
+          }
+        }
+      }
+    }
+    if (h < H) {
+      if (on)
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)h * HD + l * 8) =
+            pack8(v);
+      continue;
+    }
+    const size_t at = (cell + (h - H)) * 16 + (pos & 15);  // K heads, then V heads
+    if constexpr (Q8) {
+      // Scale of this (position, head): the largest magnitude maps to 448; the
+      // floor keeps the scale and its reciprocal normal numbers.
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+#pragma unroll
+      for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
+      const float s = fmaxf(m / 448.f, 0x1p-126f);
+      const float inv = 1.f / s;
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv), __NV_SATFINITE,
+                                                     __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
+      }
+      if (on) *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(c.pool) + at * HD + l * 8) = make_uint2(w[0], w[1]);
+      if (l == 0) c.scales[at] = s;
+    } else if (on) {
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.pool) + at * HD + l * 8) = pack8(v);
+    }
+  }
+}
+
+template <typename T, int HD>
+cudaError_t launch(cudaStream_t s, const cdb_cache_write_args& a) {
+  count_launch();
+  if (a.cache.dtype == CDB_E4M3)
+    return launch_pdl(k_cache_write<T, HD, true>, dim3(a.rows), dim3(kThreads), 0, s, a);
+  return launch_pdl(k_cache_write<T, HD, false>, dim3(a.rows), dim3(kThreads), 0, s, a);
+}
+
+}  // namespace cw
+
+cudaError_t launch_cache_write(cudaStream_t s, const cdb_cache_write_args& a) {
+  if (a.rows <= 0) return cudaSuccess;
+  const bool f = a.dtype == CDB_FP32;
+  switch (a.cache.head_dim) {
+    case 32: return f ? cw::launch<float, 32>(s, a) : cw::launch<__nv_bfloat16, 32>(s, a);
+    case 64: return f ? cw::launch<float, 64>(s, a) : cw::launch<__nv_bfloat16, 64>(s, a);
+    case 96: return f ? cw::launch<float, 96>(s, a) : cw::launch<__nv_bfloat16, 96>(s, a);
+    case 128: return f ? cw::launch<float, 128>(s, a) : cw::launch<__nv_bfloat16, 128>(s, a);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Decode attention, grouped heads, bf16 or e4m3 cache.
+//
+// One query token per row: every cached key of a row is read once per KV head,
+// so HBM bounds it.  A CTA takes `split` keys of one row and up to four KV
+// heads: a producer warp moves 16-key pages of those heads (16 * heads rows of
+// one rectangular tile for K, one for V, and the scales) with TMA into a ring,
+// four consumer warps each take one (KV head, run of keys).  A warp holds the
+// up to 8 query heads of its KV head as the rows of an m16n8k16 MMA: scores
+// S = Q K^T come out with the row's keys spread over the four lanes that share
+// it, which is the A layout of the second product O = P V, so the weights never
+// leave their lanes.  The rows 8..15 of that product carry the low parts of the
+// weights (P as a sum of two 16-bit numbers), which costs nothing extra.
+// K and V fragments are read as whole 16-byte pieces of the page rows (any
+// order of the summed index is fine as long as both operands use it; any order
+// of the output columns is undone at the end); the pairs of keys that the MMA
+// wants side by side are made with byte permutes, for e4m3 before the codes are
+// widened to fp16 (exactly).  Codes are not scaled: a key's scale multiplies
+// its score, a value's scale its weight, relative to the largest value scale
+// seen so far so that weights stay within fp16's range.
+// Partials (maximum, sum, unnormalised output) of the splits are joined in
+// split order by k_join; a row that fits one split is written directly.
+// ---------------------------------------------------------------------------
+namespace da {
+
+constexpr int kWarps = 4;  // consumer warps
+
+template <int HD, bool Q8>
+struct Geo {
+  static constexpr int ES = Q8 ? 1 : 2;
+  static constexpr int RB = HD * ES;                                             // bytes of a key row
+  static constexpr int SB = RB % 128 == 0 ? 128 : RB % 64 == 0 ? 64 : RB;        // bytes of a tile row (slice)
+  static constexpr int SW = SB == 128 ? 128 : SB == 64 ? 64 : 0;                 // swizzle span
+  static constexpr int NX = RB / SB;                                             // slices of a key row
+  static constexpr int KB = Q8 ? 32 : 16;                                        // keys of a warp per stage
+  static constexpr int PG = kWarps * KB / 16;                                    // (page, head) cells of a stage
+  static constexpr int CELL = 16 * RB;                                           // K (or V) bytes of a cell
+  static constexpr int KREG = PG * CELL;                                         // K (or V) bytes of a stage
+  static constexpr int SCALES = Q8 ? 2 * PG * 64 : 0;
+  static constexpr int STAGE = (2 * KREG + SCALES + 1023) / 1024 * 1024;
+  static constexpr int NS = 72 * 1024 / STAGE < 4 ? 72 * 1024 / STAGE : 4;       // stages: three CTAs per SM
+  static constexpr size_t SMEM = 1024 + (size_t)NS * STAGE + NS * 2 * 8 + NS * 4;
+  static constexpr int NT = HD / 8;                                              // 8-column tiles of the output
+  static constexpr int KS = HD / 16;                                             // 16-element steps of q . k
+  static constexpr int TE = SB / (4 * ES);    // elements of a slice row that one of 4 lanes takes from K
+  static constexpr int VE = SB / (8 * ES);    // elements of a slice row that one of 8 lanes takes from V
+  // First of the 4 elements that lane t takes in step s.
+  __host__ __device__ static constexpr int k_elem(int t, int s) {
+    return (4 * s / TE) * (SB / ES) + t * TE + (4 * s) % TE;
+  }
+  // Element that column g of output tile j stands for; four tiles j, j+1, j+2, j+3 (j a multiple of 4) are
+  // adjacent elements.
+  __host__ __device__ static constexpr int v_elem(int g, int j) { return (j / VE) * (SB / ES) + g * VE + j % VE; }
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count));
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
+}
+// Wait for the phase of the given parity; false after ~2 s of global time.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = su32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 63) == 0) {
+      uint64_t t;
+      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > 2000000000ull) return false;
+    }
+  }
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
+                                       uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(map), "r"(su32(bar)), "r"(x), "r"(y), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_1d(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(su32(bar))
+               : "memory");
+}
+// 2^x (ex2.approx: within a few ulp; below 2^-126 it is 0, no weight beside the maximum's 1).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two e4m3 codes (low byte first) as two fp16 numbers, exactly.
+__device__ __forceinline__ uint32_t widen(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(two));
+  return r;
+}
+template <bool Q8>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (Q8) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <bool Q8>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  if constexpr (Q8) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+// D[16x8] += A[16x16] . B[16x8], fp32 accumulate; operands fp16 (Q8) or bf16.
+template <bool Q8>
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (Q8)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// N bytes (4, 8, 12 or 16) of shared memory into words.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+  if constexpr (N == 16)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (N == 8)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
+  }
+}
+
+struct Args {
+  cdb_attention_args a;
+  int hpc, wph, split, qblocks, group, own_parts, nhg;
+  float* part_o;   // [row][query head][own_parts][HD]
+  float2* part_ml; // [row][query head][own_parts]
+};
+
+// Shared offset of byte b of tile row r.
+template <int SB, int SW>
+__device__ __forceinline__ uint32_t swz(int r, int b) {
+  if constexpr (SW == 128) return (uint32_t)(r * 128 + (b ^ ((r & 7) << 4)));
+  else if constexpr (SW == 64) return (uint32_t)(r * 64 + (b ^ (((r >> 1) & 3) << 4)));
+  else return (uint32_t)(r * SB + b);
+}
+
+template <int HD, bool Q8>
+__global__ void __launch_bounds__((kWarps + 1) * 32, 3)
+    k_decode(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Args A) {
+  using G = Geo<HD, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)G::NS * G::STAGE);
+  uint64_t* empty = full + G::NS;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(empty + G::NS);  // which pages of the stage arrived
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const cdb_attention_args& a = A.a;
+  const cdb_paged_cache& c = a.cache;
+  const int row = blockIdx.x / A.nhg, hg = blockIdx.x % A.nhg, sp = blockIdx.y;
+  const int qb = hg % A.qblocks, k0 = hg / A.qblocks * A.hpc;  // first KV head
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
+    for (int i = 0; i < G::NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int seq = a.seq[row];
+  if (seq < 0) return;  // padding
+  const int pos = a.pos[row];
+  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
+  if (seq >= c.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= c.n_kv_slots) {
+    if (threadIdx.x == 0 && sp == 0 && hg == 0)
+      report(a.status, slot < 0 || slot >= c.n_kv_slots ? CDB_OPS_BAD_SLOT : CDB_OPS_BAD_ROW);
+    return;
+  }
+  const int L = pos + 1;
+  const int lo = sp * A.split, hi = min(L, lo + A.split);
+  if (lo >= L && !(sp == 0 && L <= 0)) return;
+  const int pps = A.wph * (G::KB / 16);  // pages of one stage (per head)
+  const int npg = max(0, (hi - lo + 15) >> 4), nst = (npg + pps - 1) / pps;
+
+  if (warp == kWarps) {
+    // ---------------- producer ----------------
+    const int* bt = c.block_table + (size_t)seq * c.max_blocks + (lo >> 4);
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    const int heads = min(A.hpc, c.n_kv_heads - k0);
+    bool fail = false;
+    int issued = 0;
+    for (int st = 0; st < nst; ++st) {
+      const int s = st % G::NS;
+      const int pg = st * pps + lane;
+      const int blk = lane < pps && pg < npg ? bt[pg] : -1;
+      const bool ok = blk >= 0 && blk < c.kv_blocks;
+      if (lane < pps && pg < npg && !ok) report(a.status, CDB_OPS_BAD_BLOCK);
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (st >= G::NS && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((st / G::NS) - 1) & 1))) {
+        fail = true;
+        break;
+      }
+      const uint32_t cell = (uint32_t)A.hpc * G::CELL;  // one page of the CTA's heads, K or V
+      if (lane == 0) {
+        masks[s] = mask;
+        mbar_arrive_tx(&full[s], (uint32_t)__popc(mask) * (2 * cell + (Q8 ? 2u * heads * 64 : 0u)));
+      }
+      __syncwarp();
+      if (ok) {
+        // Rows of head k0's page at this block and slot; V follows n_kv_heads pages later.
+        const long long head0 = ((long long)blk * c.n_kv_slots + slot) * 2 * c.n_kv_heads + k0;
+        const uint32_t base = su32(smem + (size_t)s * G::STAGE) + lane * cell;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int y = (int)((head0 + kv * c.n_kv_heads) * 16);
+#pragma unroll
+          for (int x = 0; x < G::NX; ++x)
+            tma_2d(base + kv * G::KREG + x * (A.hpc * 16 * G::SB), &tm, &full[s], x * G::SB, y, pol);
+          if constexpr (Q8)
+            bulk_1d(su32(smem + (size_t)s * G::STAGE) + 2 * G::KREG + (kv * G::PG + lane * A.hpc) * 64,
+                    c.scales + (head0 + kv * c.n_kv_heads) * 16, (uint32_t)heads * 64, &full[s]);
+        }
+      }
+      issued = st + 1;
+    }
+    if (fail && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    // Copies in flight land before the CTA may leave (at once when the consumers took every stage).
+    for (int st = max(0, issued - G::NS); st < issued; ++st) mbar_wait(&full[st % G::NS], (st / G::NS) & 1);
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int hh = warp % A.hpc, sub = warp / A.hpc;  // KV head of the CTA, run of keys of the stage
+  const int g = lane >> 2, t = lane & 3;
+  const int kh = k0 + hh;
+  const int nq = min(8, A.group - qb * 8);
+  const bool live = kh < c.n_kv_heads;
+  const int qh = kh * A.group + qb * 8 + g;  // this lane group's query head
+  // q as A fragments (rows 8..15 are zero).
+  uint32_t qf[G::KS][2];
+  float mul = a.scale * 1.4426950408889634f;  // scores in the log2 domain
+  {
+    uint2 raw[G::KS];
+    const bool have = live && g < nq;
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)qh * HD;
+#pragma unroll
+    for (int s = 0; s < G::KS; ++s)
+      raw[s] = have ? *reinterpret_cast<const uint2*>(q + G::k_elem(t, s)) : make_uint2(0u, 0u);
+    if constexpr (Q8) {
+      // fp16 copy of q, scaled by a power of two so that its largest element is in [1, 2).
+      float mx = 0.f;
+#pragma unroll
+      for (int s = 0; s < G::KS; ++s) {
+        const float2 x = unpack<false>(raw[s].x), y = unpack<false>(raw[s].y);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^-e and 2^e for mx = 2^e f; 1 for zero, tiny, infinite or NaN maxima.
+      const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
+      const bool norm = eb > 0x00800000u && eb < 0x7E000000u;
+      const float down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f, up = norm ? __uint_as_float(eb) : 1.f;
+#pragma unroll
+      for (int s = 0; s < G::KS; ++s) {
+        const float2 x = unpack<false>(raw[s].x), y = unpack<false>(raw[s].y);
+        qf[s][0] = pack<true>(x.x * down, x.y * down);
+        qf[s][1] = pack<true>(y.x * down, y.y * down);
+      }
+      mul *= up;
+    } else {
+#pragma unroll
+      for (int s = 0; s < G::KS; ++s) qf[s][0] = raw[s].x, qf[s][1] = raw[s].y;
+    }
+  }
+  float o[G::NT][4];
+#pragma unroll
+  for (int j = 0; j < G::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  float m = -INFINITY, l = 0.f;  // reference maximum (log2), this lane's share of the sum
+  float ref = 0x1p-126f, iref = 0x1p126f;  // value scale the weights are relative to (e4m3), its reciprocal
+  constexpr int PW = G::KB / 16;  // pages of a warp per stage
+  bool ok = true;
+  for (int st = 0; st < nst; ++st) {
+    const int s = st % G::NS;
+    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (st / G::NS) & 1)))) break;
+    const uint32_t base = su32(smem + (size_t)s * G::STAGE);
+    const uint32_t arrived = masks[s];
+    const int key0 = lo + (st * pps + sub * PW) * 16;  // this warp's first key of the stage
+    // Bit per key: within the split and in a page that arrived.
+    uint32_t valid = key0 >= hi ? 0u : hi - key0 >= 32 ? 0xffffffffu : (1u << (hi - key0)) - 1u;
+#pragma unroll
+    for (int p = 0; p < PW; ++p)
+      if (!((arrived >> (sub * PW + p)) & 1u)) valid &= ~(0xFFFFu << (16 * p));
+    if constexpr (PW == 1) valid &= 0xFFFFu;
+    constexpr uint32_t kAll = PW == 1 ? 0xFFFFu : 0xffffffffu;
+    if (valid) {
+      float sc[2 * PW][4];
+#pragma unroll
+      for (int p = 0; p < PW; ++p) {
+        const uint32_t page = base + (uint32_t)((sub * PW + p) * A.hpc) * G::CELL;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float* d = sc[2 * p + n];
+          d[0] = d[1] = d[2] = d[3] = 0.f;
+          const int r = hh * 16 + n * 8 + g;
+#pragma unroll
+          for (int x = 0; x < G::NX; ++x) {
+            constexpr int TB = G::SB / 4;  // bytes of a slice row this lane takes
+            uint32_t w[TB / 4];
+#pragma unroll
+            for (int i = 0; i < TB; i += 16 <= TB && TB % 16 == 0 ? 16 : 8)
+              lds<(TB % 16 == 0 ? 16 : 8)>(page + x * (A.hpc * 16 * G::SB) + swz<G::SB, G::SW>(r, t * TB + i), w + i / 4);
+            if constexpr (Q8) {
+#pragma unroll
+              for (int i = 0; i < TB / 4; ++i) {
+                const int s2 = x * (TB / 4) + i;
+                mma<true>(d, qf[s2][0], 0u, qf[s2][1], 0u, widen(w[i]), widen(w[i] >> 16));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < TB / 8; ++i) {
+                const int s2 = x * (TB / 8) + i;
+                mma<false>(d, qf[s2][0], 0u, qf[s2][1], 0u, w[2 * i], w[2 * i + 1]);
+              }
+            }
+          }
+        }
+      }
+      // Scores of keys 16p + 8n + 2t, +1 for query head g.
+      float vs[2 * PW][2];
+#pragma unroll
+      for (int i = 0; i < 2 * PW; ++i) {
+        float f0 = mul, f1 = mul;
+        if constexpr (Q8) {
+          const uint32_t sa = base + 2 * G::KREG + ((sub * PW + i / 2) * A.hpc + hh) * 64 + (i & 1) * 32 + t * 8;
+          uint32_t w[2];
+          lds<8>(sa, w);
+          f0 *= __uint_as_float(w[0]), f1 *= __uint_as_float(w[1]);
+          lds<8>(sa + G::PG * 64, w);
+          vs[i][0] = __uint_as_float(w[0]), vs[i][1] = __uint_as_float(w[1]);
+        }
+        sc[i][0] *= f0, sc[i][1] *= f1;
+      }
+      if (valid != kAll) {
+#pragma unroll
+        for (int i = 0; i < 2 * PW; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!((valid >> (8 * i + 2 * t + e)) & 1u)) sc[i][e] = -INFINITY, vs[i][e] = 0.f;
+      }
+      float mx = fmaxf(sc[0][0], sc[0][1]), vmax = 0.f;
+#pragma unroll
+      for (int i = 1; i < 2 * PW; ++i) mx = fmaxf(mx, fmaxf(sc[i][0], sc[i][1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if constexpr (Q8) {
+#pragma unroll
+        for (int i = 0; i < 2 * PW; ++i) vmax = fmaxf(vmax, fmaxf(vs[i][0], vs[i][1]));
+        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+      }
+      // The reference maximum moves only when a score passes it by 2^8 (weights
+      // then reach 2^8), the reference value scale when one passes it by 2^6:
+      // fp16 weights stay below 2^14, and most stages rescale nothing.
+      const float mnew = mx > m + 8.f ? mx : m;
+      const float rnew = Q8 && vmax > 64.f * ref ? vmax : ref;
+      if (__any_sync(0xffffffffu, mnew != m) || rnew != ref) {
+        const float f = m == -INFINITY ? 0.f : ex2(m - mnew);
+        l *= f;
+        const float fo = Q8 ? f * (ref / rnew) : f;
+#pragma unroll
+        for (int j = 0; j < G::NT; ++j) {
+          o[j][0] *= fo, o[j][1] *= fo;
+          o[j][2] *= fo, o[j][3] *= fo;
+        }
+        m = mnew;
+        if (rnew != ref) ref = rnew, iref = 1.f / rnew;
+      }
+      const float mm = m == -INFINITY ? 0.f : m;
+      uint32_t ph[2 * PW], pl[2 * PW];
+#pragma unroll
+      for (int i = 0; i < 2 * PW; ++i) {
+        float p0 = ex2(sc[i][0] - mm), p1 = ex2(sc[i][1] - mm);
+        l += p0 + p1;
+        if constexpr (Q8) p0 *= vs[i][0] * iref, p1 *= vs[i][1] * iref;
+        ph[i] = pack<Q8>(p0, p1);
+        const float2 back = unpack<Q8>(ph[i]);
+        pl[i] = pack<Q8>(p0 - back.x, p1 - back.y);
+      }
+      // O += P V: lanes (g, t) hold keys 2t, 2t+1, 2t+8, 2t+9 of columns v_elem(g, .).
+#pragma unroll
+      for (int p = 0; p < PW; ++p) {
+        const uint32_t page = base + G::KREG + (uint32_t)((sub * PW + p) * A.hpc) * G::CELL;
+        const uint32_t vb = valid >> (16 * p);
+#pragma unroll
+        for (int x = 0; x < G::NX; ++x) {
+          constexpr int VB = G::SB / 8;  // bytes of a slice row this lane takes
+          uint32_t w[4][VB / 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 2 * t + (i & 1) + (i >> 1) * 8;
+            lds<VB>(page + x * (A.hpc * 16 * G::SB) + swz<G::SB, G::SW>(hh * 16 + key, g * VB), w[i]);
+            if (valid != kAll && !((vb >> key) & 1u)) {  // no weight, but the row may hold NaN
+#pragma unroll
+              for (int e = 0; e < VB / 4; ++e) w[i][e] = 0u;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < VB / 4; ++e) {
+            if constexpr (Q8) {  // 4 elements per word
+              const uint32_t a01 = __byte_perm(w[0][e], w[1][e], 0x5140), a23 = __byte_perm(w[0][e], w[1][e], 0x7362);
+              const uint32_t b01 = __byte_perm(w[2][e], w[3][e], 0x5140), b23 = __byte_perm(w[2][e], w[3][e], 0x7362);
+              const int j = x * G::VE + e * 4;
+              mma<true>(o[j], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a01), widen(b01));
+              mma<true>(o[j + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a01 >> 16), widen(b01 >> 16));
+              mma<true>(o[j + 2], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a23), widen(b23));
+              mma<true>(o[j + 3], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a23 >> 16), widen(b23 >> 16));
+            } else {  // 2 elements per word
+              const int j = x * G::VE + e * 2;
+              mma<false>(o[j], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1],
+                         __byte_perm(w[0][e], w[1][e], 0x5410), __byte_perm(w[2][e], w[3][e], 0x5410));
+              mma<false>(o[j + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1],
+                         __byte_perm(w[0][e], w[1][e], 0x7632), __byte_perm(w[2][e], w[3][e], 0x7632));
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+  }
+  if (!ok) {
+    if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    return;
+  }
+  // This lane: columns v_elem(2t, j), v_elem(2t + 1, j) of query head g; high and low weight parts added.
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (!live || g >= nq) return;
+  const int parts = L <= 0 ? 0 : ((L + A.split - 1) / A.split) * A.wph;
+  const float fin = Q8 ? ref : 1.f;
+  if (parts <= 1) {
+    const float inv = l > 0.f ? fin / l : 0.f;  // no keys: zeros
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)qh * HD;
+#pragma unroll
+    for (int j = 0; j < G::NT; j += 4)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint2*>(dst + G::v_elem(2 * t + e, j)) =
+            make_uint2(pack<false>((o[j][e] + o[j][2 + e]) * inv, (o[j + 1][e] + o[j + 1][2 + e]) * inv),
+                       pack<false>((o[j + 2][e] + o[j + 2][2 + e]) * inv, (o[j + 3][e] + o[j + 3][2 + e]) * inv));
+    return;
+  }
+  const size_t pi = ((size_t)row * a.n_heads + qh) * A.own_parts + sp * A.wph + sub;
+  float* po = A.part_o + pi * HD;
+#pragma unroll
+  for (int j = 0; j < G::NT; j += 4)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float4*>(po + G::v_elem(2 * t + e, j)) =
+          make_float4((o[j][e] + o[j][2 + e]) * fin, (o[j + 1][e] + o[j + 1][2 + e]) * fin,
+                      (o[j + 2][e] + o[j + 2][2 + e]) * fin, (o[j + 3][e] + o[j + 3][2 + e]) * fin);
+  if (t == 0) A.part_ml[pi] = make_float2(m, l);
+}
+
+// Join a row's partials in split order: one warp per (row, query head), lane j
+// owns columns 4j..4j+3.
+template <int HD>
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
+  pdl_wait();
+  pdl_trigger();
+  const cdb_attention_args& a = A.a;
+  const int lane = threadIdx.x & 31;
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int row = item / a.n_heads, h = item % a.n_heads;
+  if (row >= a.rows) return;
+  const int seq = a.seq[row], pos = a.pos[row];
+  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
+  if (seq < 0 || seq >= a.cache.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= a.cache.n_kv_slots) return;
+  const int L = pos + 1;
+  const int parts = L <= 0 ? 0 : ((L + A.split - 1) / A.split) * A.wph;
+  if (parts <= 1) return;  // written by the attention kernel
+  const size_t pi = ((size_t)row * a.n_heads + h) * A.own_parts;
+  float m = -INFINITY;
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, A.part_ml[pi + s].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool cols = 4 * lane < HD;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    const int s = s0 + lane, n = min(32, parts - s0);
+    const float2 ml = s < parts ? A.part_ml[pi + s] : make_float2(-INFINITY, 0.f);
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m), ls = ml.y * w;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      l += __shfl_sync(0xffffffffu, ls, k);
+      if (cols) {
+        const float4 x = *reinterpret_cast<const float4*>(A.part_o + (pi + s0 + k) * HD + 4 * lane);
+        v.x = fmaf(x.x, wk, v.x), v.y = fmaf(x.y, wk, v.y), v.z = fmaf(x.z, wk, v.z), v.w = fmaf(x.w, wk, v.w);
+      }
+    }
+  }
+  if (!cols) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint2 r;
+  r.x = pack<false>(v.x * inv, v.y * inv);
+  r.y = pack<false>(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)h * HD + 4 * lane) = r;
+}
+
+template <int HD, bool Q8>
+cudaError_t launch(cudaStream_t s, const Args& A) {
+  using G = Geo<HD, Q8>;
+  const cdb_paged_cache& c = A.a.cache;
+  CUtensorMap tm;
+  const uint64_t rows = (uint64_t)c.kv_blocks * c.n_kv_slots * 2 * c.n_kv_heads * 16;
+  if (!tmap_u8_2d(&tm, c.pool, G::RB, rows, G::RB, G::SB, A.hpc * 16, G::SW)) return cudaErrorInvalidValue;
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (!set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_decode<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  const int splits = A.own_parts / A.wph;
+  count_launch();
+  cudaError_t e = launch_pdl(k_decode<HD, Q8>, dim3((unsigned)A.a.rows * A.nhg, splits), dim3((kWarps + 1) * 32), G::SMEM,
+                             s, tm, A);
+  if (e != cudaSuccess || A.own_parts <= 1) return e;
+  count_launch();
+  const long long items = (long long)A.a.rows * A.a.n_heads;
+  return launch_pdl(k_join<HD>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, s, A);
+}
+
+}  // namespace da
+
+// Keys of a CTA: 128 per warp and head, 256 from four query heads per KV head
+// on, whose partials would else weigh more than 3% of the keys read (a partial
+// is head_dim + 2 floats per query head).  Below four KV heads the CTA's warps
+// share a head and take runs of its keys.  Nothing here looks at the batch, so
+// a row's bits do not depend on it.
+AttnPlan attention_plan(int n_heads, int n_kv_heads, int head_dim, int max_ctx) {
+  (void)head_dim;
+  AttnPlan p;
+  const int group = n_heads / n_kv_heads;
+  p.hpc = n_kv_heads >= 4 ? 4 : n_kv_heads >= 2 ? 2 : 1;
+  p.warps_per_head = da::kWarps / p.hpc;
+  p.qblocks = (group + 7) / 8;
+  p.split = (group >= 4 ? 256 : 128) * p.warps_per_head;
+  p.own_parts = (max_ctx + p.split - 1) / p.split * p.warps_per_head;
+  return p;
+}
+
+cudaError_t launch_decode_attention(cudaStream_t s, const cdb_attention_args& a) {
+  if (a.rows <= 0) return cudaSuccess;
+  const AttnPlan p = attention_plan(a.n_heads, a.cache.n_kv_heads, a.cache.head_dim, a.max_ctx);
+  da::Args A;
+  A.a = a;
+  A.hpc = p.hpc;
+  A.wph = p.warps_per_head;
+  A.split = p.split;
+  A.qblocks = p.qblocks;
+  A.group = a.n_heads / a.cache.n_kv_heads;
+  A.own_parts = p.own_parts;
+  A.nhg = (a.cache.n_kv_heads + p.hpc - 1) / p.hpc * p.qblocks;
+  const size_t cells = (size_t)a.rows * a.n_heads * p.own_parts;
+  A.part_o = static_cast<float*>(a.workspace);
+  A.part_ml = reinterpret_cast<float2*>(A.part_o + cells * a.cache.head_dim);
+  const bool q8 = a.cache.dtype == CDB_E4M3;
+  switch (a.cache.head_dim) {
+    case 32: return q8 ? da::launch<32, true>(s, A) : da::launch<32, false>(s, A);
+    case 64: return q8 ? da::launch<64, true>(s, A) : da::launch<64, false>(s, A);
+    case 96: return q8 ? da::launch<96, true>(s, A) : da::launch<96, false>(s, A);
+    case 128: return q8 ? da::launch<128, true>(s, A) : da::launch<128, false>(s, A);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace cdb

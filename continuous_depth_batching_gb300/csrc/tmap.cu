@@ -77,4 +77,21 @@ const CUtensorMap* tmap_bf16_2d(const void* p, uint64_t inner, uint64_t outer, u
   return &cache.emplace(k, m).first->second;
 }
 
+bool tmap_u8_2d(CUtensorMap* out, const void* p, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+                uint32_t box_outer, int swizzle) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (swizzle == 64) sw = CU_TENSOR_MAP_SWIZZLE_64B;
+  else if (swizzle == 128) sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  else if (swizzle != 0) return false;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {stride};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace cdb

@@ -14,4 +14,9 @@ namespace cdb {
 const CUtensorMap* tmap_bf16_2d(const void* p, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
                                 uint32_t box_outer, int swizzle);
 
+// The same for bytes, encoded into *out on every call (nothing is cached, so
+// the map never outlives the memory it was made for); false as above.
+bool tmap_u8_2d(CUtensorMap* out, const void* p, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+                uint32_t box_outer, int swizzle);
+
 }  // namespace cdb

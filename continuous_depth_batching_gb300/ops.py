@@ -23,9 +23,38 @@ class SampleArgs(C.Structure):
                 ("top_p", C.c_void_p), ("min_p", C.c_void_p), ("token", C.c_void_p), ("logprob", C.c_void_p)]
 
 
+class Cache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("scales", C.c_void_p), ("block_table", C.c_void_p), ("dtype", C.c_int),
+                ("kv_blocks", C.c_int), ("n_kv_slots", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("n_seqs", C.c_int), ("max_blocks", C.c_int)]
+
+
+class CacheWriteArgs(C.Structure):
+    _fields_ = [("cache", Cache), ("rows", C.c_int), ("n_heads", C.c_int), ("qkv", C.c_void_p), ("dtype", C.c_int),
+                ("ldqkv", C.c_int64), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p), ("eps", C.c_float),
+                ("rope", C.c_void_p), ("rope_positions", C.c_int), ("rot_dim", C.c_int), ("seq", C.c_void_p),
+                ("pos", C.c_void_p), ("depth", C.c_void_p), ("slot_base", C.c_int), ("q", C.c_void_p),
+                ("ldq", C.c_int64), ("status", C.c_void_p)]
+
+
+class AttentionArgs(C.Structure):
+    _fields_ = [("cache", Cache), ("rows", C.c_int), ("n_heads", C.c_int), ("q", C.c_void_p), ("ldq", C.c_int64),
+                ("seq", C.c_void_p), ("pos", C.c_void_p), ("depth", C.c_void_p), ("slot_base", C.c_int),
+                ("scale", C.c_float), ("max_ctx", C.c_int), ("shared_len", C.c_int), ("out", C.c_void_p),
+                ("ldo", C.c_int64), ("status", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+STATUS = {1: "block table entry out of range", 2: "slot out of range", 8: "sequence or position out of range",
+          32: "bounded wait expired", 128: "rows do not share the prefix's blocks"}
+
+
 def _lib():
     L = lib()
     if L.cdb_sample.argtypes is None:
+        L.cdb_cache_write.argtypes = [C.c_void_p, C.c_void_p]
+        L.cdb_attention.argtypes = [C.c_void_p, C.c_void_p]
+        L.cdb_attention_workspace.restype = C.c_size_t
+        L.cdb_attention_workspace.argtypes = [C.c_int] * 6
         L.cdb_ops_last_error.restype = C.c_char_p
         L.cdb_ops_last_error.argtypes = []
         L.cdb_sample.argtypes = [C.c_void_p, C.c_void_p]
@@ -104,3 +133,151 @@ class Sampler(_Op):
         if rc != 0:
             _fail(self.L, rc, "cdb_sample")
         return self.token[:rows], self.logprob[:rows]
+
+
+class PagedCache:
+    """A paged KV cache in the engine's layout, over tensors the caller owns.
+
+    pool [kv_blocks, n_slots, 2, n_kv_heads, 16, head_dim], bfloat16 or float8_e4m3fn (then
+    scales float32 of the pool's shape without its last axis); block_table int32
+    [n_seqs, max_blocks].
+    """
+
+    def __init__(self, pool, block_table, scales=None):
+        import torch
+        if pool.dim() != 6 or pool.shape[2] != 2 or pool.shape[4] != 16 or not pool.is_contiguous():
+            raise ValueError(f"pool: expected contiguous [kv_blocks, n_slots, 2, n_kv_heads, 16, head_dim], got "
+                             f"{tuple(pool.shape)}")
+        if pool.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"pool: {pool.dtype}, expected bfloat16 or float8_e4m3fn")
+        e4m3 = pool.dtype == torch.float8_e4m3fn
+        if e4m3 != (scales is not None):
+            raise ValueError("an e4m3 pool needs scales, a bf16 pool has none")
+        if e4m3 and (scales.dtype != torch.float32 or scales.shape != pool.shape[:-1] or not scales.is_contiguous()):
+            raise ValueError(f"scales: expected contiguous float32 {tuple(pool.shape[:-1])}, got {tuple(scales.shape)}")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+            raise ValueError("block_table: expected contiguous int32 [n_seqs, max_blocks]")
+        for t in (block_table,) + ((scales,) if e4m3 else ()):
+            if t.device != pool.device:
+                raise ValueError(f"pool is on {pool.device}, block_table or scales on {t.device}")
+        if pool.device.type != "cuda":
+            raise ValueError(f"pool is on {pool.device}, expected a CUDA device")
+        self.pool, self.block_table, self.scales = pool, block_table, scales
+        nb, ns, _, hk, _, hd = pool.shape
+        self.n_kv_heads, self.head_dim, self.n_slots = hk, hd, ns
+        self.max_ctx = 16 * block_table.shape[1]
+        self.desc = Cache(pool.data_ptr(), scales.data_ptr() if e4m3 else None, block_table.data_ptr(),
+                          E4M3 if e4m3 else BF16, nb, ns, hk, hd, block_table.shape[0], block_table.shape[1])
+
+
+class _CacheOp(_Op):
+    def __init__(self, cache, n_heads):
+        super().__init__()
+        if cache.pool.device.index != self.dev:
+            raise ValueError(f"the cache is on {cache.pool.device}, the current device is cuda:{self.dev}")
+        self.cache, self.n_heads = cache, int(n_heads)
+        self.width = self.n_heads * cache.head_dim
+        self.status = self._t.zeros(1, dtype=self._t.int32, device=cache.pool.device)
+
+    def check(self):
+        """Wait for the device and raise if a call found an index out of range."""
+        st = int(self.status.item())
+        if st:
+            self.status.zero_()
+            raise CdbError(-5, "; ".join(v for k, v in STATUS.items() if st & k) or f"status {st}")
+
+
+class CacheWriter(_CacheOp):
+    """Query / key norm, rotation and the cache write of a step's rows, in one pass (cdb_cache_write).
+
+    qkv [rows, (n_heads + 2 n_kv_heads) head_dim] fp32 or bf16: query heads, key heads, value
+    heads.  rope: float32 [positions, rot_dim / 2, 2] (cos, sin), see rope_table, or None;
+    q_gain, k_gain: float32 [head_dim] norm weights, or None.  Returns the queries, bf16
+    [rows, n_heads head_dim]; rows with seq < 0 are padding and left alone.
+    """
+
+    def __init__(self, cache, n_heads, rope=None, q_gain=None, k_gain=None, eps=1e-6):
+        super().__init__(cache, n_heads)
+        t = self._t
+        a = self.args = CacheWriteArgs(cache=cache.desc, n_heads=self.n_heads, eps=eps)
+        hd = cache.head_dim
+        if (q_gain is None) != (k_gain is None):
+            raise ValueError("q_gain and k_gain come together")
+        a.q_gain, a.k_gain = self._vec("q_gain", q_gain, t.float32, hd), self._vec("k_gain", k_gain, t.float32, hd)
+        if rope is not None:
+            if (rope.dtype != t.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() or
+                    rope.device.index != self.dev):
+                raise ValueError(f"rope: expected contiguous float32 [positions, rot_dim / 2, 2], got {tuple(rope.shape)}")
+            a.rope, a.rope_positions, a.rot_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+        self._keep = (rope, q_gain, k_gain)
+        a.status = self.status.data_ptr()
+        self._ref = C.byref(a)
+
+    def __call__(self, qkv, seq, pos, depth=None, slot_base=0, q_out=None):
+        t, a = self._t, self.args
+        rows = qkv.shape[0]
+        if q_out is None:
+            q_out = t.zeros(rows, self.width, dtype=t.bfloat16, device=qkv.device)
+        a.rows, a.slot_base = rows, slot_base
+        a.qkv, a.ldqkv = self._mat("qkv", qkv, (t.float32, t.bfloat16), rows,
+                                   self.width + 2 * self.cache.n_kv_heads * self.cache.head_dim)
+        a.dtype = BF16 if qkv.dtype == t.bfloat16 else FP32
+        a.seq, a.pos = self._vec("seq", seq, t.int32, rows), self._vec("pos", pos, t.int32, rows)
+        a.depth = self._vec("depth", depth, t.int32, rows)
+        a.q, a.ldq = self._mat("q_out", q_out, (t.bfloat16,), rows, self.width)
+        rc = self.L.cdb_cache_write(self._ref, self._stream())
+        if rc != 0:
+            _fail(self.L, rc, "cdb_cache_write")
+        return q_out
+
+
+class DecodeAttention(_CacheOp):
+    """Attention of one query token per row over the paged cache (cdb_attention).
+
+    q bf16 [rows, n_heads head_dim]; row i attends to positions 0..pos[i] of sequence seq[i]
+    in slot slot_base + depth[i].  shared_len: positions that every row's sequence shares
+    (same blocks), read once for all rows.  Rows with seq < 0 are left alone.  max_ctx bounds
+    every position (+ 1); the workspace is sized for max_rows rows of it.
+    """
+
+    def __init__(self, cache, n_heads, max_rows, max_ctx=None, scale=None):
+        super().__init__(cache, n_heads)
+        self.max_rows, self.max_ctx = int(max_rows), int(max_ctx or cache.max_ctx)
+        hd = cache.head_dim
+        n = max(self.L.cdb_attention_workspace(self.max_rows, self.n_heads, cache.n_kv_heads, hd, self.max_ctx, s)
+                for s in (0, self.max_ctx // 16 * 16))
+        if n == 0:
+            raise ValueError(f"n_heads {n_heads}, max_rows {max_rows}, max_ctx {max_ctx}: not supported with "
+                             f"{cache.n_kv_heads} KV heads of {hd}")
+        t = self._t
+        self.workspace = t.empty(n + 256, dtype=t.uint8, device=cache.pool.device)
+        base = (self.workspace.data_ptr() + 255) // 256 * 256
+        self.args = AttentionArgs(cache=cache.desc, n_heads=self.n_heads, scale=hd ** -0.5 if scale is None else scale,
+                                  max_ctx=self.max_ctx, status=self.status.data_ptr(), workspace=base,
+                                  workspace_bytes=n)
+        self._ref = C.byref(self.args)
+
+    def __call__(self, q, seq, pos, depth=None, slot_base=0, shared_len=0, out=None):
+        t, a = self._t, self.args
+        rows = q.shape[0]
+        if rows > self.max_rows:
+            raise ValueError(f"{rows} rows, the workspace holds {self.max_rows}")
+        if out is None:
+            out = t.zeros(rows, self.width, dtype=t.bfloat16, device=q.device)
+        a.rows, a.slot_base, a.shared_len = rows, slot_base, shared_len
+        a.q, a.ldq = self._mat("q", q, (t.bfloat16,), rows, self.width)
+        a.seq, a.pos = self._vec("seq", seq, t.int32, rows), self._vec("pos", pos, t.int32, rows)
+        a.depth = self._vec("depth", depth, t.int32, rows)
+        a.out, a.ldo = self._mat("out", out, (t.bfloat16,), rows, self.width)
+        rc = self.L.cdb_attention(self._ref, self._stream())
+        if rc != 0:
+            _fail(self.L, rc, "cdb_attention")
+        return out
+
+
+def rope_table(positions, rot_dim, theta=10000.0, device="cuda"):
+    """(cos, sin) of pos * theta^(-2j / rot_dim), float32 [positions, rot_dim / 2, 2], angles in float64."""
+    import torch
+    inv = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.stack([a.cos(), a.sin()], -1).float().contiguous()

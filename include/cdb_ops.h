@@ -59,6 +59,97 @@ typedef struct {
 } cdb_sample_args;
 int cdb_sample(const cdb_sample_args *a, void *stream);
 
+/* ------------------------------------------------------------- paged cache
+ * A pool of 16-token pages, laid out as the engine's: per block and slot, K
+ * then V, each head's 16 positions contiguous.  A slot is one KV entry per
+ * token: looped models keep one per (layer, loop step).  Position p of sequence
+ * s lives in block block_table[s][p / 16].
+ * An e4m3 pool (CDB_E4M3) holds 8-bit codes and, per (position, head) of K and
+ * of V, a float32 scale; a cached value is scale * code. */
+#define CDB_E4M3 2
+typedef struct {
+  void *pool;                 /* [kv_blocks][n_kv_slots][2][n_kv_heads][16][head_dim] */
+  float *scales;              /* e4m3: [kv_blocks][n_kv_slots][2][n_kv_heads][16]; else NULL */
+  const int32_t *block_table; /* [n_seqs][max_blocks], entries behind a sequence's last page unused */
+  int dtype;                  /* CDB_BF16 or CDB_E4M3 */
+  int kv_blocks, n_kv_slots, n_kv_heads, head_dim; /* head_dim 32, 64, 96 or 128 */
+  int n_seqs, max_blocks;
+} cdb_paged_cache;
+
+/* Device status bits that the cache operators OR into *status (a device int32
+ * the caller zeroes; NULL: not reported).  The row concerned is skipped. */
+#define CDB_OPS_BAD_BLOCK 1   /* block table entry out of range */
+#define CDB_OPS_BAD_SLOT 2    /* slot_base + depth out of range */
+#define CDB_OPS_BAD_ROW 8     /* sequence or position out of range */
+#define CDB_OPS_TIMEOUT 32    /* a bounded wait inside a kernel expired */
+#define CDB_OPS_NOT_SHARED 128 /* rows name different blocks inside shared_len */
+
+/* ------------------------------------------------------------- cache write
+ * Row i of qkv holds n_heads query heads, n_kv_heads key heads and n_kv_heads
+ * value heads of head_dim elements.  In one pass, in fp32:
+ *   with gains, every query and key head is normalised, x / sqrt(mean x^2 +
+ *   eps) * gain;  with a table, queries and keys are rotated by the row's
+ *   position, element j < rot_dim / 2 with j + rot_dim / 2, by (cos, sin) =
+ *   rope[pos][j] (elements behind rot_dim are left);
+ *   queries are rounded to bf16 into q; keys and values go to position pos of
+ *   sequence seq, slot slot_base + depth: rounded to bf16, or as e4m3 with
+ *   scale = max(max|x| / 448, 2^-126) and code = e4m3(x / scale).
+ * A row with seq < 0 is padding: nothing of it is read or written.  Two rows
+ * of one call must not name the same position of the same sequence and slot. */
+typedef struct {
+  cdb_paged_cache cache;
+  int rows, n_heads;
+  const void *qkv;        /* [rows][ldqkv], ldqkv >= (n_heads + 2 n_kv_heads) head_dim; 16-byte aligned rows */
+  int dtype;              /* CDB_FP32 or CDB_BF16 */
+  int64_t ldqkv;
+  const float *q_gain, *k_gain; /* [head_dim] each, or both NULL: no norm */
+  float eps;
+  const float *rope;      /* [rope_positions][rot_dim / 2][2], or NULL: no rotation */
+  int rope_positions, rot_dim; /* rot_dim a multiple of 16, <= head_dim */
+  const int32_t *seq, *pos;    /* [rows] */
+  const int32_t *depth;   /* [rows], or NULL: all 0 */
+  int slot_base;
+  void *q;                /* bf16 [rows][ldq], ldq >= n_heads head_dim; 16-byte aligned rows */
+  int64_t ldq;
+  int32_t *status;
+} cdb_cache_write_args;
+int cdb_cache_write(const cdb_cache_write_args *a, void *stream);
+
+/* -------------------------------------------------------- decode attention
+ * One query token per row over the cached positions 0..pos of its sequence:
+ * o = sum_j softmax_j(scale * q . k_j) v_j per head, query head h reading KV
+ * head h / (n_heads / n_kv_heads).  Softmax statistics and sums are fp32.
+ * A row with seq < 0 is padding: its output is left as it was.  A row with
+ * pos < 0 has no keys: zeros.  Keys are taken `split` at a time and joined in
+ * order, so a row's bits do not depend on the other rows.
+ * shared_len > 0 (a multiple of 16) says that every row's sequence names the
+ * same blocks for positions 0..shared_len-1 (a common prompt): those keys are
+ * then read once for all rows.  The sequence of the first row with seq >= 0
+ * names the blocks that are read; a row that names others sets
+ * CDB_OPS_NOT_SHARED.  depth must be NULL then (all rows in one slot).
+ * workspace: cdb_attention_workspace() bytes, 256-byte aligned, any contents;
+ * used by one call at a time. */
+typedef struct {
+  cdb_paged_cache cache;
+  int rows, n_heads;
+  const void *q;          /* bf16 [rows][ldq]; 16-byte aligned rows */
+  int64_t ldq;
+  const int32_t *seq, *pos;
+  const int32_t *depth;
+  int slot_base;
+  float scale;
+  int max_ctx;            /* every pos < max_ctx (checked on the device), <= max_blocks * 16 */
+  int shared_len;
+  void *out;              /* bf16 [rows][ldo]; 16-byte aligned rows */
+  int64_t ldo;
+  int32_t *status;
+  void *workspace;
+  size_t workspace_bytes;
+} cdb_attention_args;
+int cdb_attention(const cdb_attention_args *a, void *stream);
+/* Workspace for a call of this many rows; 0 for arguments cdb_attention refuses. */
+size_t cdb_attention_workspace(int rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx, int shared_len);
+
 #ifdef __cplusplus
 }
 #endif

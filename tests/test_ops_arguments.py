@@ -37,3 +37,69 @@ def test_sample_refuses_no_arguments(L):
 def test_sample_takes_an_empty_batch(L):
     assert L.cdb_sample(C.byref(sample_args(rows=0)), None) == 0
     assert L.cdb_ops_last_error() == b""
+
+
+def cache_desc(**kw):
+    c = ops.Cache(pool=0x1000, scales=0x1000, block_table=0x1000, dtype=2, kv_blocks=8, n_kv_slots=1, n_kv_heads=4,
+                  head_dim=64, n_seqs=2, max_blocks=4)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+CACHE_BAD = [dict(dtype=0), dict(dtype=3), dict(head_dim=48), dict(head_dim=256), dict(kv_blocks=0), dict(n_kv_slots=0),
+             dict(n_kv_heads=0), dict(n_seqs=0), dict(max_blocks=0), dict(pool=None), dict(pool=0x1008),
+             dict(block_table=None), dict(scales=None), dict(scales=0x1004), dict(max_blocks=1 << 28)]
+
+
+def write_args(**kw):
+    p = 0x1000
+    a = ops.CacheWriteArgs(cache=cache_desc(), rows=3, n_heads=8, qkv=p, dtype=0, ldqkv=1024, q_gain=p, k_gain=p, eps=1e-6,
+                           rope=p, rope_positions=64, rot_dim=64, seq=p, pos=p, q=p, ldq=512)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("bad", [dict(cache=cache_desc(**b)) for b in CACHE_BAD] +
+                         [dict(rows=-1), dict(n_heads=0), dict(dtype=2), dict(ldqkv=1023), dict(ldqkv=1026), dict(qkv=None),
+                          dict(qkv=0x1004), dict(q=None), dict(q=0x1002), dict(ldq=504), dict(ldq=516), dict(q_gain=None),
+                          dict(k_gain=None), dict(q_gain=0x1004), dict(eps=-1.0), dict(eps=float("nan")), dict(rot_dim=8),
+                          dict(rot_dim=24), dict(rot_dim=80), dict(rot_dim=0), dict(rope_positions=0), dict(rope=0x1008),
+                          dict(seq=None), dict(pos=None)])
+def test_cache_write_refuses(L, bad):
+    assert L.cdb_cache_write(C.byref(write_args(**bad)), None) == ARG
+    assert L.cdb_ops_last_error()
+
+
+def attention_args(**kw):
+    p = 0x1000
+    a = ops.AttentionArgs(cache=cache_desc(), rows=3, n_heads=8, q=p, ldq=512, seq=p, pos=p, scale=0.125, max_ctx=64, out=p,
+                          ldo=512, workspace=p, workspace_bytes=1 << 30)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("bad", [dict(cache=cache_desc(**b)) for b in CACHE_BAD] +
+                         [dict(rows=-1), dict(rows=(1 << 31) - 1), dict(n_heads=0), dict(n_heads=6), dict(q=None), dict(q=0x1008),
+                          dict(ldq=504), dict(ldq=516), dict(out=None), dict(out=0x1002), dict(ldo=504), dict(ldo=518),
+                          dict(seq=None), dict(pos=None), dict(max_ctx=0), dict(max_ctx=65), dict(shared_len=8),
+                          dict(shared_len=-16), dict(shared_len=80), dict(shared_len=16, depth=0x1000),
+                          dict(workspace=None), dict(workspace=0x1010), dict(workspace_bytes=0),
+                          dict(cache=cache_desc(kv_blocks=1 << 25))])
+def test_attention_refuses(L, bad):
+    assert L.cdb_attention(C.byref(attention_args(**bad)), None) == ARG
+    assert L.cdb_ops_last_error()
+
+
+def test_empty_batches(L):
+    assert L.cdb_cache_write(C.byref(write_args(rows=0)), None) == 0
+    assert L.cdb_attention(C.byref(attention_args(rows=0)), None) == 0
+
+
+def test_attention_workspace_sizes(L):
+    assert L.cdb_attention_workspace(4, 8, 3, 64, 100, 0) == 0   # heads do not divide
+    assert L.cdb_attention_workspace(4, 8, 8, 64, 100, 8) == 0
+    one, two = (L.cdb_attention_workspace(r, 8, 8, 128, 4096, 0) for r in (1, 2))
+    assert 0 < one < two <= 2 * one
