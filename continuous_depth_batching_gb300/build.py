@@ -36,6 +36,7 @@ SOURCES = [
     "tmap.cu",
     "sample.cu",
     "cache_ops.cu",
+    "shared_prefix.cu",
     "ops.cu",
 ]
 

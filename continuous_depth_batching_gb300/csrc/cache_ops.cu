@@ -4,17 +4,16 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "../../include/cdb.h"
 #include "cache_ops.h"
 #include "common.cuh"
 #include "kernels.cuh"
+#include "tc.cuh"
 #include "tmap.h"
 
 namespace cdb {
-
-__device__ __forceinline__ void report(int* status, int bit) {
-  if (status) atomicOr(status, bit);
-}
 
 // ---------------------------------------------------------------------------
 // Cache write.
@@ -245,61 +244,8 @@ struct Geo {
   __host__ __device__ static constexpr int v_elem(int g, int j) { return (j / VE) * (SB / ES) + g * VE + j % VE; }
 };
 
-__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count));
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
-}
-// Wait for the phase of the given parity; false after ~2 s of global time.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = su32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((it & 63) == 0) {
-      uint64_t t;
-      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-      if (t0 == 0) t0 = t;
-      else if (t - t0 > 2000000000ull) return false;
-    }
-  }
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
-                                       uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(map), "r"(su32(bar)), "r"(x), "r"(y), "l"(pol)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_1d(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(su32(bar))
-               : "memory");
-}
-// 2^x (ex2.approx: within a few ulp; below 2^-126 it is 0, no weight beside the maximum's 1).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Two e4m3 codes (low byte first) as two fp16 numbers, exactly.
-__device__ __forceinline__ uint32_t widen(uint32_t two) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(two));
-  return r;
-}
+using namespace tc;
+
 template <bool Q8>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   if constexpr (Q8) {
@@ -343,11 +289,19 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
   }
 }
 
+// Partials of a row of L keys.
+__device__ __forceinline__ int row_parts(int L, int first, int split, int wph) {
+  return L <= first ? 0 : (L - first + split - 1) / split * wph;
+}
+
 struct Args {
   cdb_attention_args a;
-  int hpc, wph, split, qblocks, group, own_parts, nhg;
-  float* part_o;   // [row][query head][own_parts][HD]
-  float2* part_ml; // [row][query head][own_parts]
+  int hpc, wph, split, qblocks, group, nhg;
+  int first;        // keys below belong to the shared prefix
+  int chunks;       // partials of the shared prefix, before a row's own
+  int parts;        // partials a row can have
+  float* part_o;    // [row][query head][parts][HD]
+  float2* part_ml;  // [row][query head][parts]: maximum (log2), sum
 };
 
 // Shared offset of byte b of tile row r.
@@ -393,8 +347,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     return;
   }
   const int L = pos + 1;
-  const int lo = sp * A.split, hi = min(L, lo + A.split);
-  if (lo >= L && !(sp == 0 && L <= 0)) return;
+  const int lo = A.first + sp * A.split, hi = min(L, lo + A.split);
+  // A row without keys gets its zeros here, unless k_join writes every row.
+  if (lo >= L && (A.chunks > 0 || sp > 0 || L > 0)) return;
   const int pps = A.wph * (G::KB / 16);  // pages of one stage (per head)
   const int npg = max(0, (hi - lo + 15) >> 4), nst = (npg + pps - 1) / pps;
 
@@ -652,9 +607,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
   if (!live || g >= nq) return;
-  const int parts = L <= 0 ? 0 : ((L + A.split - 1) / A.split) * A.wph;
   const float fin = Q8 ? ref : 1.f;
-  if (parts <= 1) {
+  if (A.chunks == 0 && row_parts(L, A.first, A.split, A.wph) <= 1) {
     const float inv = l > 0.f ? fin / l : 0.f;  // no keys: zeros
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)qh * HD;
 #pragma unroll
@@ -666,7 +620,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
                        pack<false>((o[j + 2][e] + o[j + 2][2 + e]) * inv, (o[j + 3][e] + o[j + 3][2 + e]) * inv));
     return;
   }
-  const size_t pi = ((size_t)row * a.n_heads + qh) * A.own_parts + sp * A.wph + sub;
+  const size_t pi = ((size_t)row * a.n_heads + qh) * A.parts + A.chunks + sp * A.wph + sub;
   float* po = A.part_o + pi * HD;
 #pragma unroll
   for (int j = 0; j < G::NT; j += 4)
@@ -692,10 +646,23 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   const int seq = a.seq[row], pos = a.pos[row];
   const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
   if (seq < 0 || seq >= a.cache.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= a.cache.n_kv_slots) return;
+  if (A.chunks > 0 && h == 0) {  // does the row name the prefix's blocks?
+    int base = -1;
+    for (int r0 = 0; base < 0; r0 += 32) {  // ends: this row has a sequence
+      const int s = r0 + lane < a.rows ? a.seq[r0 + lane] : -1;
+      const uint32_t has = __ballot_sync(0xffffffffu, s >= 0 && s < a.cache.n_seqs);
+      if (has) base = __shfl_sync(0xffffffffu, s, __ffs(has) - 1);
+    }
+    const int* t0 = a.cache.block_table + (size_t)base * a.cache.max_blocks;
+    const int* t1 = a.cache.block_table + (size_t)seq * a.cache.max_blocks;
+    bool same = true;
+    for (int p = lane; p < min(A.first, pos + 1 + 15) / 16; p += 32) same = same && t0[p] == t1[p];
+    if (!same) report(a.status, CDB_OPS_NOT_SHARED);
+  }
   const int L = pos + 1;
-  const int parts = L <= 0 ? 0 : ((L + A.split - 1) / A.split) * A.wph;
-  if (parts <= 1) return;  // written by the attention kernel
-  const size_t pi = ((size_t)row * a.n_heads + h) * A.own_parts;
+  const int parts = A.chunks + row_parts(L, A.first, A.split, A.wph);
+  if (A.chunks == 0 && parts <= 1) return;  // written by the attention kernel
+  const size_t pi = ((size_t)row * a.n_heads + h) * A.parts;
   float m = -INFINITY;
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, A.part_ml[pi + s].x);
 #pragma unroll
@@ -711,7 +678,7 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
     for (int k = 0; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       l += __shfl_sync(0xffffffffu, ls, k);
-      if (cols) {
+      if (cols && wk > 0.f) {
         const float4 x = *reinterpret_cast<const float4*>(A.part_o + (pi + s0 + k) * HD + 4 * lane);
         v.x = fmaf(x.x, wk, v.x), v.y = fmaf(x.y, wk, v.y), v.z = fmaf(x.z, wk, v.z), v.w = fmaf(x.w, wk, v.w);
       }
@@ -740,11 +707,11 @@ cudaError_t launch(cudaStream_t s, const Args& A) {
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const int splits = A.own_parts / A.wph;
+  const int splits = max(1, (A.a.max_ctx - A.first + A.split - 1) / A.split);
   count_launch();
   cudaError_t e = launch_pdl(k_decode<HD, Q8>, dim3((unsigned)A.a.rows * A.nhg, splits), dim3((kWarps + 1) * 32), G::SMEM,
                              s, tm, A);
-  if (e != cudaSuccess || A.own_parts <= 1) return e;
+  if (e != cudaSuccess || (A.chunks == 0 && A.parts <= 1)) return e;
   count_launch();
   const long long items = (long long)A.a.rows * A.a.n_heads;
   return launch_pdl(k_join<HD>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, s, A);
@@ -757,21 +724,49 @@ cudaError_t launch(cudaStream_t s, const Args& A) {
 // is head_dim + 2 floats per query head).  Below four KV heads the CTA's warps
 // share a head and take runs of its keys.  Nothing here looks at the batch, so
 // a row's bits do not depend on it.
-AttnPlan attention_plan(int n_heads, int n_kv_heads, int head_dim, int max_ctx) {
-  (void)head_dim;
+static AttnPlan attention_plan(int n_heads, int n_kv_heads, int max_ctx, int first) {
   AttnPlan p;
   const int group = n_heads / n_kv_heads;
   p.hpc = n_kv_heads >= 4 ? 4 : n_kv_heads >= 2 ? 2 : 1;
   p.warps_per_head = da::kWarps / p.hpc;
   p.qblocks = (group + 7) / 8;
   p.split = (group >= 4 ? 256 : 128) * p.warps_per_head;
-  p.own_parts = (max_ctx + p.split - 1) / p.split * p.warps_per_head;
+  p.own_parts = (max_ctx - first + p.split - 1) / p.split * p.warps_per_head;
   return p;
+}
+
+// How a shared prefix is cut: tiles of up to 128 query rows, and as many chunks
+// of keys as give every SM one CTA (a chunk has at least four blocks of keys,
+// so that its setup and partials stay small beside it).
+constexpr int kSms = 152;
+static SharedPlan shared_plan(int rows, int n_heads, int n_kv_heads, int head_dim, int shared_len) {
+  SharedPlan p = {0, 0, 0};
+  const int group = n_heads / n_kv_heads;
+  if (shared_len <= 0 || rows < 2 || group > 128 || (head_dim != 64 && head_dim != 128)) return p;
+  p.tile_rows = 128 / group;
+  const long long tiles = (long long)n_kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows);
+  if (tiles > 65535) return SharedPlan{0, 0, 0};
+  const int blocks = (shared_len + 63) / 64;
+  const int want = (int)std::max(1ll, std::min((long long)(blocks + 3) / 4, kSms / std::min(tiles, (long long)kSms)));
+  p.chunk = (blocks + want - 1) / want * 64;
+  p.chunks = (shared_len + p.chunk - 1) / p.chunk;
+  return p;
+}
+
+size_t attention_workspace(int rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx, int shared_len) {
+  const SharedPlan sh = shared_plan(rows, n_heads, n_kv_heads, head_dim, shared_len);
+  const AttnPlan p = attention_plan(n_heads, n_kv_heads, max_ctx, sh.chunks ? shared_len : 0);
+  size_t cells = (size_t)rows * n_heads * (sh.chunks + p.own_parts);
+  // Any prefix, up to this many rows: chunks is 1, or chunks * tiles <= kSms with at most 128 query rows per tile.
+  if (shared_len < 0) cells += std::max((size_t)rows * n_heads, (size_t)kSms * 128);
+  return (cells * (head_dim + 2) * 4 + 511) / 256 * 256;
 }
 
 cudaError_t launch_decode_attention(cudaStream_t s, const cdb_attention_args& a) {
   if (a.rows <= 0) return cudaSuccess;
-  const AttnPlan p = attention_plan(a.n_heads, a.cache.n_kv_heads, a.cache.head_dim, a.max_ctx);
+  const SharedPlan sh = shared_plan(a.rows, a.n_heads, a.cache.n_kv_heads, a.cache.head_dim, a.shared_len);
+  const int first = sh.chunks ? a.shared_len : 0;
+  const AttnPlan p = attention_plan(a.n_heads, a.cache.n_kv_heads, a.max_ctx, first);
   da::Args A;
   A.a = a;
   A.hpc = p.hpc;
@@ -779,11 +774,17 @@ cudaError_t launch_decode_attention(cudaStream_t s, const cdb_attention_args& a)
   A.split = p.split;
   A.qblocks = p.qblocks;
   A.group = a.n_heads / a.cache.n_kv_heads;
-  A.own_parts = p.own_parts;
   A.nhg = (a.cache.n_kv_heads + p.hpc - 1) / p.hpc * p.qblocks;
-  const size_t cells = (size_t)a.rows * a.n_heads * p.own_parts;
+  A.first = first;
+  A.chunks = sh.chunks;
+  A.parts = sh.chunks + p.own_parts;
+  const size_t cells = (size_t)a.rows * a.n_heads * A.parts;
   A.part_o = static_cast<float*>(a.workspace);
   A.part_ml = reinterpret_cast<float2*>(A.part_o + cells * a.cache.head_dim);
+  if (sh.chunks) {
+    const cudaError_t e = launch_shared_prefix(s, a, sh, A.parts, A.part_o, A.part_ml);
+    if (e != cudaSuccess) return e;
+  }
   const bool q8 = a.cache.dtype == CDB_E4M3;
   switch (a.cache.head_dim) {
     case 32: return q8 ? da::launch<32, true>(s, A) : da::launch<32, false>(s, A);

@@ -119,9 +119,8 @@ static const char* bad_attention(int rows, int n_heads, int n_kv_heads, int head
 }
 
 size_t cdb_attention_workspace(int rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx, int shared_len) {
-  if (bad_attention(rows, n_heads, n_kv_heads, head_dim, max_ctx, shared_len)) return 0;
-  const cdb::AttnPlan p = cdb::attention_plan(n_heads, n_kv_heads, head_dim, max_ctx);
-  return ((size_t)rows * n_heads * p.own_parts * (head_dim + 2) * 4 + 511) / 256 * 256;
+  if (bad_attention(rows, n_heads, n_kv_heads, head_dim, max_ctx, shared_len < 0 ? 0 : shared_len)) return 0;
+  return cdb::attention_workspace(rows, n_heads, n_kv_heads, head_dim, max_ctx, shared_len);
 }
 
 int cdb_attention(const cdb_attention_args* a, void* stream) {
@@ -140,7 +139,8 @@ int cdb_attention(const cdb_attention_args* a, void* stream) {
   if (!a->out || !aligned(a->out, 16) || a->ldo % 8 || a->ldo < width)
     return refuse("out is missing, too narrow, or its rows are not 16-byte aligned");
   if (!a->seq || !a->pos) return refuse("seq and pos are needed");
-  if (a->shared_len && a->depth) return refuse("a shared prefix needs all rows in one slot (depth NULL)");
+  if (a->shared_len && (a->depth || a->slot_base < 0 || a->slot_base >= c.n_kv_slots))
+    return refuse("a shared prefix needs all rows in one slot (depth NULL, slot_base a slot of the cache)");
   if (!a->workspace || !aligned(a->workspace, 256) ||
       a->workspace_bytes < cdb_attention_workspace(a->rows, a->n_heads, c.n_kv_heads, c.head_dim, a->max_ctx, a->shared_len))
     return refuse("workspace is missing, too small or not 256-byte aligned");

@@ -19,4 +19,9 @@ const CUtensorMap* tmap_bf16_2d(const void* p, uint64_t inner, uint64_t outer, u
 bool tmap_u8_2d(CUtensorMap* out, const void* p, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
                 uint32_t box_outer, int swizzle);
 
+// bf16 tensor [d2][d1][d0], strides of d1 and d2 in bytes, box b0 x b1 x b2,
+// 128-byte swizzle; not cached.
+bool tmap_bf16_3d(CUtensorMap* out, const void* p, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1, uint64_t stride2,
+                  uint32_t b0, uint32_t b1, uint32_t b2);
+
 }  // namespace cdb

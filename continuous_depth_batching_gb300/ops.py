@@ -244,8 +244,7 @@ class DecodeAttention(_CacheOp):
         super().__init__(cache, n_heads)
         self.max_rows, self.max_ctx = int(max_rows), int(max_ctx or cache.max_ctx)
         hd = cache.head_dim
-        n = max(self.L.cdb_attention_workspace(self.max_rows, self.n_heads, cache.n_kv_heads, hd, self.max_ctx, s)
-                for s in (0, self.max_ctx // 16 * 16))
+        n = self.L.cdb_attention_workspace(self.max_rows, self.n_heads, cache.n_kv_heads, hd, self.max_ctx, -1)
         if n == 0:
             raise ValueError(f"n_heads {n_heads}, max_rows {max_rows}, max_ctx {max_ctx}: not supported with "
                              f"{cache.n_kv_heads} KV heads of {hd}")

@@ -120,13 +120,17 @@ int cdb_cache_write(const cdb_cache_write_args *a, void *stream);
  * o = sum_j softmax_j(scale * q . k_j) v_j per head, query head h reading KV
  * head h / (n_heads / n_kv_heads).  Softmax statistics and sums are fp32.
  * A row with seq < 0 is padding: its output is left as it was.  A row with
- * pos < 0 has no keys: zeros.  Keys are taken `split` at a time and joined in
- * order, so a row's bits do not depend on the other rows.
+ * pos < 0 has no keys: zeros.  Without a shared prefix, keys are taken a fixed
+ * number at a time and joined in order, so a row's bits do not depend on the
+ * other rows.
  * shared_len > 0 (a multiple of 16) says that every row's sequence names the
- * same blocks for positions 0..shared_len-1 (a common prompt): those keys are
- * then read once for all rows.  The sequence of the first row with seq >= 0
- * names the blocks that are read; a row that names others sets
- * CDB_OPS_NOT_SHARED.  depth must be NULL then (all rows in one slot).
+ * same blocks for positions 0..shared_len-1 (a common prompt, all of it
+ * written): those keys are then read once for all rows (head_dim 64 and 128,
+ * two rows or more, at most 128 query heads per KV head; else the prefix is
+ * read per row), and cut by the number of rows, which changes a row's roundings.
+ * The sequence of the first row with seq >= 0 names the blocks that are read; a
+ * row that names others sets CDB_OPS_NOT_SHARED where they are read once.  A row
+ * may end inside the prefix.  depth must be NULL then (all rows in one slot).
  * workspace: cdb_attention_workspace() bytes, 256-byte aligned, any contents;
  * used by one call at a time. */
 typedef struct {
@@ -147,7 +151,8 @@ typedef struct {
   size_t workspace_bytes;
 } cdb_attention_args;
 int cdb_attention(const cdb_attention_args *a, void *stream);
-/* Workspace for a call of this many rows; 0 for arguments cdb_attention refuses. */
+/* Workspace for a call of this many rows; shared_len < 0: for any shared_len
+ * and any number of rows up to this.  0 for arguments cdb_attention refuses. */
 size_t cdb_attention_workspace(int rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx, int shared_len);
 
 #ifdef __cplusplus

@@ -229,6 +229,91 @@ def test_pool_offsets_past_32_bits():
         assert float((out[i].double().view(16, hd) - o).norm() / o.norm()) < 2.0 ** -4
 
 
+SHARED_HEADS = [(16, 16), (8, 2), (9, 3), (5, 1), (24, 4)]
+
+
+def check_shared(cs, kw=None):
+    """A batch behind a common prefix.  The prefix's weights are bf16, each off by 2^-8 of itself: 2^-8 max |v|
+    beside what expected() allows.  Over a row those errors are independent: the norm stays within 2^-7."""
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    n = cs["q"].shape[0]
+    at = ops.DecodeAttention(cs["cache"], cs["H"], n + 3, min(cs["max_ctx"], cs["cache"].max_ctx))
+    out = at(cs["q"], cs["seq"], cs["pos"], shared_len=cs["shared"], **(kw or {}))
+    at.check()
+    total = [0.0, 0.0]
+    for i in range(n):
+        if int(cs["seq"][i]) < 0:
+            continue
+        o, tol = expected(cs, i, cs["hd"] ** -0.5)
+        err = (out[i].double().view(cs["H"], cs["hd"]) - o).abs()
+        tol = tol + 2.0 ** -8 * cs["vals"][:, :, 1].nan_to_num().abs().max()
+        assert bool((err <= tol).all()), (i, float((err / tol).max()), int(cs["pos"][i]))
+        total[0] += float(err.square().sum())
+        total[1] += float(o.square().sum())
+    assert total[0] ** 0.5 <= 2.0 ** -7 * total[1] ** 0.5
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [32, 64, 96, 128])
+@pytest.mark.parametrize("heads", SHARED_HEADS)
+def test_shared_prefix_shapes(dtype, hd, heads):
+    rng = np.random.default_rng(hd)
+    for shared, rows in ((16, 2), (64, 5), (112, 33), (336, 3), (1040, 20)):
+        lengths = [int(v) for v in rng.integers(1, 150, rows)]
+        check_shared(attention_case(dtype, *heads, hd, lengths, shared=shared, seed=shared))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,shared", [(1, 512), (129, 256), (300, 2064), (40, 9008)])
+def test_shared_prefix_large(dtype, rows, shared):
+    rng = np.random.default_rng(rows)
+    check_shared(attention_case(dtype, 8, 4, 128, [int(v) for v in rng.integers(1, 300, rows)], shared=shared, seed=rows))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_shared_prefix_rows_inside_it_and_padding(dtype):
+    # Rows that end inside the prefix, at its end, without keys, and padding before the first live row.
+    import torch
+    cs = attention_case(dtype, 8, 2, 64, [1, 20, 3, 90, 7, 16, 1, 2], shared=208, seed=3)
+    pos = cs["pos"]
+    pos[1], pos[2], pos[3] = 207, 100, 0
+    cs["seq"][0] = cs["seq"][5] = -1
+    out = torch.full((8, 8 * 64 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    check_shared(cs, dict(out=out[:, :512]))
+    assert bool((out[[0, 5]] == 7).all()) and bool((out[:, 512:] == 7).all())
+    pos[4] = -1
+    from continuous_depth_batching_gb300 import ops
+    at = ops.DecodeAttention(cs["cache"], 8, 8)
+    at(cs["q"], cs["seq"], pos, shared_len=208, out=out[:, :512])
+    at.check()
+    assert bool((out[4, :512] == 0).all())
+    cs["seq"].fill_(-1)
+    out.fill_(3.0)
+    at(cs["q"], cs["seq"], pos, shared_len=208, out=out[:, :512])
+    at.check()
+    assert bool((out == 3).all())
+
+
+def test_shared_prefix_exactly_the_context():
+    # No row has keys of its own.
+    cs = attention_case("bf16", 4, 4, 128, [1, 1, 1], shared=128, seed=2)
+    cs["pos"].fill_(127)
+    cs["max_ctx"] = 128
+    check_shared(cs)
+
+
+def test_shared_prefix_of_other_blocks_is_reported():
+    from continuous_depth_batching_gb300 import ops
+    cs = attention_case("bf16", 4, 4, 64, [5, 9, 3], shared=64, seed=4)
+    t = cs["cache"].block_table
+    t[int(cs["seq"][2]), 1] = t[int(cs["seq"][2]), 4]
+    at = ops.DecodeAttention(cs["cache"], 4, 3)
+    at(cs["q"], cs["seq"], cs["pos"], shared_len=64)
+    assert int(at.status.item()) == 128
+
+
 def write_reference(cs):
     """Float64 queries [rows, H, hd], keys and values [rows, 2, hk, hd]."""
     import torch

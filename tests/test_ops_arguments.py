@@ -103,3 +103,7 @@ def test_attention_workspace_sizes(L):
     assert L.cdb_attention_workspace(4, 8, 8, 64, 100, 8) == 0
     one, two = (L.cdb_attention_workspace(r, 8, 8, 128, 4096, 0) for r in (1, 2))
     assert 0 < one < two <= 2 * one
+    any_prefix = L.cdb_attention_workspace(64, 16, 4, 128, 4096, -1)
+    for rows in (1, 2, 3, 31, 32, 33, 64):
+        for shared in range(0, 4097, 16):
+            assert L.cdb_attention_workspace(rows, 16, 4, 128, 4096, shared) <= any_prefix
