@@ -36,16 +36,9 @@ struct Geo {
   static constexpr int NG = kThreads / GW;
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
+__device__ __forceinline__ void load8(const float* p, float* v) {
   Chunk<float>::load(p, v);
   Chunk<float>::load(p + 4, v + 4);
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  Chunk<__nv_bfloat16>::load(p, v);
 }
 __device__ __forceinline__ uint4 pack8(const float* v) {
   uint4 u;
@@ -58,111 +51,150 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return u;
 }
 
+// Heads of a group whose elements are loaded together: their bytes are in
+// flight while the row's sequence, position and block are looked up.
+constexpr int kAhead = 3;
+
+// 8 elements as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+
 template <typename T, int HD, bool Q8>
-__global__ void __launch_bounds__(kThreads) k_cache_write(cdb_cache_write_args a) {
+__global__ void __launch_bounds__(kThreads, 4) k_cache_write(const __grid_constant__ cdb_cache_write_args a) {
   using G = Geo<HD>;
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x;
   const int g = threadIdx.x / G::GW, l = threadIdx.x % G::GW;
-  const int seq = a.seq[row];
-  if (seq < 0) return;  // padding
   const cdb_paged_cache& c = a.cache;
-  const int pos = a.pos[row];
+  const int seq = a.seq[row], pos = a.pos[row], dep = a.depth ? a.depth[row] : 0;
+  const bool on = l * 8 < HD;
+  const int H = a.n_heads, Hk = c.n_kv_heads, total = H + 2 * Hk;
+  const T* src = reinterpret_cast<const T*>(a.qkv) + (size_t)row * a.ldqkv + l * 8;
+  Raw<T> raw[kAhead] = {};
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (on && g + i * G::NG < total) raw[i].load(src + (size_t)(g + i * G::NG) * HD);
+  if (seq < 0) return;  // padding
   if (seq >= c.n_seqs || pos < 0 || pos >= c.max_blocks * 16 || (a.rope && pos >= a.rope_positions)) {
     if (threadIdx.x == 0) report(a.status, CDB_OPS_BAD_ROW);
     return;
   }
-  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
+  const int slot = a.slot_base + dep;
   const int blk = c.block_table[(size_t)seq * c.max_blocks + (pos >> 4)];
-  if (slot < 0 || slot >= c.n_kv_slots || blk < 0 || blk >= c.kv_blocks) {
-    if (threadIdx.x == 0) report(a.status, blk < 0 || blk >= c.kv_blocks ? CDB_OPS_BAD_BLOCK : CDB_OPS_BAD_SLOT);
-    return;
-  }
-  const bool on = l * 8 < HD;
   // Groups of a warp may be at different kinds of heads: shuffles name their group's lanes only.
   const uint32_t peers = (0xffffffffu >> (32 - G::GW)) << ((threadIdx.x & 31) / G::GW * G::GW);
-  const int H = a.n_heads, Hk = c.n_kv_heads, total = H + 2 * Hk;
-  // Rotation of this lane's 8 elements: low half (own index) or high half (index - rot/2).
+  // Rotation: x' = x cos + y sn, y the element rot_dim / 2 away, sn = -sin in the lower half and sin in
+  // the upper one.
   const int rl = a.rope ? a.rot_dim / 16 : 0;  // lanes of one half
-  const bool low = l < rl, high = !low && l < 2 * rl;
+  const bool low = l < rl, turned = l < 2 * rl;
   float cs[8], sn[8];
-  if (low || high) {
+  if (turned) {
     const float4* t = reinterpret_cast<const float4*>(a.rope + ((size_t)pos * (a.rot_dim / 2) + (low ? l : l - rl) * 8) * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = t[i];
-      cs[2 * i] = v.x, sn[2 * i] = v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = v.w;
+      cs[2 * i] = v.x, sn[2 * i] = low ? -v.y : v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = low ? -v.w : v.w;
     }
   }
-  const T* src = reinterpret_cast<const T*>(a.qkv) + (size_t)row * a.ldqkv + l * 8;
+  const int peer = (low ? l + rl : l - rl) & (G::GW - 1);  // lane holding the rotation's other element
+  if (slot < 0 || slot >= c.n_kv_slots || blk < 0 || blk >= c.kv_blocks) {
+    if (threadIdx.x == 0) report(a.status, blk < 0 || blk >= c.kv_blocks ? CDB_OPS_BAD_BLOCK : CDB_OPS_BAD_SLOT);
+    return;
+  }
   // Cached element (kv half, head j) of this position starts at ((cell + kv Hk + j) 16 + pos % 16).
   const size_t cell = ((size_t)blk * c.n_kv_slots + slot) * 2 * Hk;
-  const int peer = low ? l + rl : l - rl;  // lane holding the rotation's other element
-#pragma unroll 3
-  for (int h = g; h < total; h += G::NG) {
-    float v[8] = {};
-    if (on) load8<T>(src + (size_t)h * HD, v);
-    if (h < H + Hk) {
-      if (a.q_gain) {
-        float ss = 0.f;
+
+  for (int h0 = g; h0 < total; h0 += kAhead * G::NG) {
+    if (h0 != g) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+      for (int i = 0; i < kAhead; ++i)
+        if (on && h0 + i * G::NG < total) raw[i].load(src + (size_t)(h0 + i * G::NG) * HD);
+    }
 #pragma unroll
-        for (int o = G::GW / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o, G::GW);
-        const float r = rsqrtf(ss * (1.f / HD) + a.eps);
-        if (on) {
-          float w[8];
-          load8<float>((h < H ? a.q_gain : a.k_gain) + l * 8, w);
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * G::NG;
+      if (h >= total) break;
+      float v[8];
+      raw[i].get(v);  // zeros in the idle lanes of a 96-element head
+      if (h < H + Hk) {
+        if (a.q_gain) {
+          float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
+          for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+          for (int o = G::GW / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o, G::GW);
+          const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+          if (on) {
+            float w[8];
+            load8((h < H ? a.q_gain : a.k_gain) + l * 8, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
+          }
         }
-      }
-      if (rl) {
+        if (rl) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(peers, v[e], peer & (G::GW - 1), G::GW);
-          float x, y;
-          if (low) {
-            rope_pair(v[e], o, make_float2(cs[e], sn[e]), x, y);
-            v[e] = x;
-          } else if (high) {
-            rope_pair(o, v[e], make_float2(cs[e], sn[e]), x, y);
-            v[e] = y;
+          for (int e = 0; e < 8; ++e) {
+            const float o = __shfl_sync(peers, v[e], peer, G::GW);
+            if (turned) v[e] = __fadd_rn(__fmul_rn(v[e], cs[e]), __fmul_rn(o, sn[e]));
           }
         }
       }
-    }
-    if (h < H) {
-      if (on)
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)h * HD + l * 8) =
-            pack8(v);
-      continue;
-    }
-    const size_t at = (cell + (h - H)) * 16 + (pos & 15);  // K heads, then V heads
-    if constexpr (Q8) {
-      // Scale of this (position, head): the largest magnitude maps to 448; the
-      // floor keeps the scale and its reciprocal normal numbers.
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-#pragma unroll
-      for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
-      const float s = fmaxf(m / 448.f, 0x1p-126f);
-      const float inv = 1.f / s;
-      uint32_t w[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv), __NV_SATFINITE,
-                                                     __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
+      if (h < H) {
+        if (on)
+          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)h * HD + l * 8) =
+              pack8(v);
+        continue;
       }
-      if (on) *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(c.pool) + at * HD + l * 8) = make_uint2(w[0], w[1]);
-      if (l == 0) c.scales[at] = s;
-    } else if (on) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.pool) + at * HD + l * 8) = pack8(v);
+      const size_t at = (cell + (h - H)) * 16 + (pos & 15);  // K heads, then V heads
+      if constexpr (Q8) {
+        // Scale of this (position, head): the largest magnitude maps to 448; the
+        // floor keeps the scale and its reciprocal normal numbers.
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+#pragma unroll
+        for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
+        const float s = fmaxf(m * (1.f / 448.f), 0x1p-126f);
+        const float inv = __frcp_rn(s);
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j] * inv, v[4 * j + 1] * inv), __NV_SATFINITE,
+                                                       __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2] * inv, v[4 * j + 3] * inv),
+                                                       __NV_SATFINITE, __NV_E4M3);
+          w[j] = lo | (hi << 16);
+        }
+        if (on) *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(c.pool) + at * HD + l * 8) = make_uint2(w[0], w[1]);
+        if (l == 0) c.scales[at] = s;
+      } else if (on) {
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.pool) + at * HD + l * 8) = pack8(v);
+      }
     }
   }
 }
@@ -196,14 +228,16 @@ cudaError_t launch_cache_write(cudaStream_t s, const cdb_cache_write_args& a) {
 // so HBM bounds it.  A CTA takes `split` keys of one row and up to four KV
 // heads: a producer warp moves 16-key pages of those heads (16 * heads rows of
 // one rectangular tile for K, one for V, and the scales) with TMA into a ring,
-// four consumer warps each take one (KV head, run of keys).  A warp holds the
-// up to 8 query heads of its KV head as the rows of an m16n8k16 MMA: scores
-// S = Q K^T come out with the row's keys spread over the four lanes that share
-// it, which is the A layout of the second product O = P V, so the weights never
-// leave their lanes.  The rows 8..15 of that product carry the low parts of the
-// weights (P as a sum of two 16-bit numbers), which costs nothing extra.
+// four consumer warps each take one (KV head, run of keys).  A warp computes
+// S^T = K Q^T and O^T = V^T P^T with m16n8k16 MMAs: keys (then output columns)
+// fill the 16 rows, the up to 8 query heads of the KV head the 8 columns, so no
+// row of the larger operand is padding; P^T is turned into the second product's
+// layout by one 8x8 transpose (movmatrix) per 8 keys.
+// Weights enter as 16-bit numbers, high and low part: with up to four query
+// heads the low parts sit in the columns 4..7, which costs nothing, else they
+// take a second product.
 // K and V fragments are read as whole 16-byte pieces of the page rows (any
-// order of the summed index is fine as long as both operands use it; any order
+// order of the summed index is fine as long as both operands use it; the order
 // of the output columns is undone at the end); the pairs of keys that the MMA
 // wants side by side are made with byte permutes, for e4m3 before the codes are
 // widened to fp16 (exactly).  Codes are not scaled: a key's scale multiplies
@@ -231,7 +265,7 @@ struct Geo {
   static constexpr int STAGE = (2 * KREG + SCALES + 1023) / 1024 * 1024;
   static constexpr int NS = 72 * 1024 / STAGE < 4 ? 72 * 1024 / STAGE : 4;       // stages: three CTAs per SM
   static constexpr size_t SMEM = 1024 + (size_t)NS * STAGE + NS * 2 * 8 + NS * 4;
-  static constexpr int NT = HD / 8;                                              // 8-column tiles of the output
+  static constexpr int NT = HD / 16;                                             // 16-element tiles of the output
   static constexpr int KS = HD / 16;                                             // 16-element steps of q . k
   static constexpr int TE = SB / (4 * ES);    // elements of a slice row that one of 4 lanes takes from K
   static constexpr int VE = SB / (8 * ES);    // elements of a slice row that one of 8 lanes takes from V
@@ -239,9 +273,9 @@ struct Geo {
   __host__ __device__ static constexpr int k_elem(int t, int s) {
     return (4 * s / TE) * (SB / ES) + t * TE + (4 * s) % TE;
   }
-  // Element that column g of output tile j stands for; four tiles j, j+1, j+2, j+3 (j a multiple of 4) are
-  // adjacent elements.
-  __host__ __device__ static constexpr int v_elem(int g, int j) { return (j / VE) * (SB / ES) + g * VE + j % VE; }
+  // The i-th of the HD / 8 elements that lane group g takes from V; row g of output tile j is element
+  // 2j, row g + 8 element 2j + 1.  Four elements i..i+3 (i a multiple of 4) are adjacent.
+  __host__ __device__ static constexpr int v_elem(int g, int i) { return (i / VE) * (SB / ES) + g * VE + i % VE; }
 };
 
 using namespace tc;
@@ -312,7 +346,15 @@ __device__ __forceinline__ uint32_t swz(int r, int b) {
   else return (uint32_t)(r * SB + b);
 }
 
-template <int HD, bool Q8>
+// 8x8 transpose of 16-bit elements across the warp (lane 4r + t holds row r, columns 2t, 2t + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// WIDE: more than four query heads per KV head (up to 8 here).
+template <int HD, bool Q8, bool WIDE>
 __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     k_decode(const __grid_constant__ CUtensorMap tm, const __grid_constant__ Args A) {
   using G = Geo<HD, Q8>;
@@ -407,17 +449,19 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   const int kh = k0 + hh;
   const int nq = min(8, A.group - qb * 8);
   const bool live = kh < c.n_kv_heads;
-  const int qh = kh * A.group + qb * 8 + g;  // this lane group's query head
-  // q as A fragments (rows 8..15 are zero).
+  const int q0 = kh * A.group + qb * 8;  // first query head
+  // q as B fragments: column g is query head q0 + g (narrow: columns 4..7 repeat 0..3).
   uint32_t qf[G::KS][2];
-  float mul = a.scale * 1.4426950408889634f;  // scores in the log2 domain
+  float mul[2];  // factor of the scores of columns 2t, 2t + 1 (log2 domain)
   {
     uint2 raw[G::KS];
-    const bool have = live && g < nq;
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)qh * HD;
+    const int qi = WIDE ? g : g & 3;
+    const bool have = live && qi < nq;
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)(q0 + qi) * HD;
 #pragma unroll
     for (int s = 0; s < G::KS; ++s)
       raw[s] = have ? *reinterpret_cast<const uint2*>(q + G::k_elem(t, s)) : make_uint2(0u, 0u);
+    float f = a.scale * 1.4426950408889634f;
     if constexpr (Q8) {
       // fp16 copy of q, scaled by a power of two so that its largest element is in [1, 2).
       float mx = 0.f;
@@ -438,18 +482,22 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         qf[s][0] = pack<true>(x.x * down, x.y * down);
         qf[s][1] = pack<true>(y.x * down, y.y * down);
       }
-      mul *= up;
+      f *= up;
     } else {
 #pragma unroll
       for (int s = 0; s < G::KS; ++s) qf[s][0] = raw[s].x, qf[s][1] = raw[s].y;
     }
+    mul[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+    mul[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
   }
   float o[G::NT][4];
 #pragma unroll
   for (int j = 0; j < G::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m = -INFINITY, l = 0.f;  // reference maximum (log2), this lane's share of the sum
+  // Columns 2t, 2t + 1: reference maximum (log2, the same in the 8 lanes of a column), this lane's share of the sum.
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float ref = 0x1p-126f, iref = 0x1p126f;  // value scale the weights are relative to (e4m3), its reciprocal
-  constexpr int PW = G::KB / 16;  // pages of a warp per stage
+  constexpr int PW = G::KB / 16;           // pages of a warp per stage
+  constexpr uint32_t kAll = PW == 1 ? 0xFFFFu : 0xffffffffu;
   bool ok = true;
   for (int st = 0; st < nst; ++st) {
     const int s = st % G::NS;
@@ -462,106 +510,122 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 #pragma unroll
     for (int p = 0; p < PW; ++p)
       if (!((arrived >> (sub * PW + p)) & 1u)) valid &= ~(0xFFFFu << (16 * p));
-    if constexpr (PW == 1) valid &= 0xFFFFu;
-    constexpr uint32_t kAll = PW == 1 ? 0xFFFFu : 0xffffffffu;
+    valid &= kAll;
     if (valid) {
-      float sc[2 * PW][4];
+      float sc[PW][4], vs[PW][2];  // keys g (0, 1), g + 8 (2, 3) of columns 2t, 2t + 1; value scales of g, g + 8
 #pragma unroll
       for (int p = 0; p < PW; ++p) {
         const uint32_t page = base + (uint32_t)((sub * PW + p) * A.hpc) * G::CELL;
+        sc[p][0] = sc[p][1] = sc[p][2] = sc[p][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float* d = sc[2 * p + n];
-          d[0] = d[1] = d[2] = d[3] = 0.f;
-          const int r = hh * 16 + n * 8 + g;
+        for (int x = 0; x < G::NX; ++x) {
+          constexpr int TB = G::SB / 4;  // bytes of a slice row this lane takes
+          constexpr int LD = TB % 16 == 0 ? 16 : 8;
+          uint32_t w0[TB / 4], w1[TB / 4];
 #pragma unroll
-          for (int x = 0; x < G::NX; ++x) {
-            constexpr int TB = G::SB / 4;  // bytes of a slice row this lane takes
-            uint32_t w[TB / 4];
+          for (int i = 0; i < TB; i += LD) {
+            lds<LD>(page + x * (A.hpc * 16 * G::SB) + swz<G::SB, G::SW>(hh * 16 + g, t * TB + i), w0 + i / 4);
+            lds<LD>(page + x * (A.hpc * 16 * G::SB) + swz<G::SB, G::SW>(hh * 16 + 8 + g, t * TB + i), w1 + i / 4);
+          }
+          if constexpr (Q8) {
 #pragma unroll
-            for (int i = 0; i < TB; i += 16 <= TB && TB % 16 == 0 ? 16 : 8)
-              lds<(TB % 16 == 0 ? 16 : 8)>(page + x * (A.hpc * 16 * G::SB) + swz<G::SB, G::SW>(r, t * TB + i), w + i / 4);
-            if constexpr (Q8) {
+            for (int i = 0; i < TB / 4; ++i) {
+              const int s2 = x * (TB / 4) + i;
+              mma<true>(sc[p], widen(w0[i]), widen(w1[i]), widen_hi(w0[i]), widen_hi(w1[i]), qf[s2][0], qf[s2][1]);
+            }
+          } else {
 #pragma unroll
-              for (int i = 0; i < TB / 4; ++i) {
-                const int s2 = x * (TB / 4) + i;
-                mma<true>(d, qf[s2][0], 0u, qf[s2][1], 0u, widen(w[i]), widen(w[i] >> 16));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < TB / 8; ++i) {
-                const int s2 = x * (TB / 8) + i;
-                mma<false>(d, qf[s2][0], 0u, qf[s2][1], 0u, w[2 * i], w[2 * i + 1]);
-              }
+            for (int i = 0; i < TB / 8; ++i) {
+              const int s2 = x * (TB / 8) + i;
+              mma<false>(sc[p], w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1], qf[s2][0], qf[s2][1]);
             }
           }
         }
-      }
-      // Scores of keys 16p + 8n + 2t, +1 for query head g.
-      float vs[2 * PW][2];
-#pragma unroll
-      for (int i = 0; i < 2 * PW; ++i) {
-        float f0 = mul, f1 = mul;
         if constexpr (Q8) {
-          const uint32_t sa = base + 2 * G::KREG + ((sub * PW + i / 2) * A.hpc + hh) * 64 + (i & 1) * 32 + t * 8;
-          uint32_t w[2];
-          lds<8>(sa, w);
-          f0 *= __uint_as_float(w[0]), f1 *= __uint_as_float(w[1]);
-          lds<8>(sa + G::PG * 64, w);
-          vs[i][0] = __uint_as_float(w[0]), vs[i][1] = __uint_as_float(w[1]);
+          const uint32_t sa = base + 2 * G::KREG + ((sub * PW + p) * A.hpc + hh) * 64 + g * 4;
+          uint32_t w[4];
+          lds<4>(sa, w);
+          lds<4>(sa + 32, w + 1);
+          lds<4>(sa + G::PG * 64, w + 2);
+          lds<4>(sa + G::PG * 64 + 32, w + 3);
+          vs[p][0] = __uint_as_float(w[2]), vs[p][1] = __uint_as_float(w[3]);
+          sc[p][0] *= __uint_as_float(w[0]), sc[p][1] *= __uint_as_float(w[0]);
+          sc[p][2] *= __uint_as_float(w[1]), sc[p][3] *= __uint_as_float(w[1]);
         }
-        sc[i][0] *= f0, sc[i][1] *= f1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[p][e] *= mul[e & 1];
       }
       if (valid != kAll) {
 #pragma unroll
-        for (int i = 0; i < 2 * PW; ++i)
+        for (int p = 0; p < PW; ++p)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (!((valid >> (8 * i + 2 * t + e)) & 1u)) sc[i][e] = -INFINITY, vs[i][e] = 0.f;
+            if (!((valid >> (16 * p + 8 * e + g)) & 1u)) sc[p][2 * e] = sc[p][2 * e + 1] = -INFINITY, vs[p][e] = 0.f;
       }
-      float mx = fmaxf(sc[0][0], sc[0][1]), vmax = 0.f;
+      float mx[2] = {fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[0][1], sc[0][3])}, vmax = 0.f;
 #pragma unroll
-      for (int i = 1; i < 2 * PW; ++i) mx = fmaxf(mx, fmaxf(sc[i][0], sc[i][1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      for (int p = 1; p < PW; ++p) {
+        mx[0] = max3(mx[0], sc[p][0], sc[p][2]);
+        mx[1] = max3(mx[1], sc[p][1], sc[p][3]);
+      }
       if constexpr (Q8) {
 #pragma unroll
-        for (int i = 0; i < 2 * PW; ++i) vmax = fmaxf(vmax, fmaxf(vs[i][0], vs[i][1]));
-        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+        for (int p = 0; p < PW; ++p) vmax = max3(vmax, vs[p][0], vs[p][1]);
       }
       // The reference maximum moves only when a score passes it by 2^8 (weights
       // then reach 2^8), the reference value scale when one passes it by 2^6:
       // fp16 weights stay below 2^14, and most stages rescale nothing.
-      const float mnew = mx > m + 8.f ? mx : m;
-      const float rnew = Q8 && vmax > 64.f * ref ? vmax : ref;
-      if (__any_sync(0xffffffffu, mnew != m) || rnew != ref) {
-        const float f = m == -INFINITY ? 0.f : ex2(m - mnew);
-        l *= f;
-        const float fo = Q8 ? f * (ref / rnew) : f;
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || (Q8 && vmax > 64.f * ref))) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+          const float mnew = mx[e] > m[e] + 8.f ? mx[e] : m[e];
+          f[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - mnew);
+          l[e] *= f[e];
+          m[e] = mnew;
+        }
+        if constexpr (Q8) {
+          vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+          const float rnew = vmax > 64.f * ref ? vmax : ref;
+          f[0] *= ref / rnew, f[1] *= ref / rnew;
+          ref = rnew, iref = 1.f / rnew;
+        }
 #pragma unroll
         for (int j = 0; j < G::NT; ++j) {
-          o[j][0] *= fo, o[j][1] *= fo;
-          o[j][2] *= fo, o[j][3] *= fo;
+          o[j][0] *= f[0], o[j][1] *= f[1];
+          o[j][2] *= f[0], o[j][3] *= f[1];
         }
-        m = mnew;
-        if (rnew != ref) ref = rnew, iref = 1.f / rnew;
       }
-      const float mm = m == -INFINITY ? 0.f : m;
-      uint32_t ph[2 * PW], pl[2 * PW];
+      const float mm[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      uint32_t bh[PW][2], bl[PW][2];  // weights of keys 0..7, 8..15 of the page as B fragments
 #pragma unroll
-      for (int i = 0; i < 2 * PW; ++i) {
-        float p0 = ex2(sc[i][0] - mm), p1 = ex2(sc[i][1] - mm);
-        l += p0 + p1;
-        if constexpr (Q8) p0 *= vs[i][0] * iref, p1 *= vs[i][1] * iref;
-        ph[i] = pack<Q8>(p0, p1);
-        const float2 back = unpack<Q8>(ph[i]);
-        pl[i] = pack<Q8>(p0 - back.x, p1 - back.y);
-      }
-      // O += P V: lanes (g, t) hold keys 2t, 2t+1, 2t+8, 2t+9 of columns v_elem(g, .).
+      for (int p = 0; p < PW; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float p0 = ex2(sc[p][2 * e] - mm[0]), p1 = ex2(sc[p][2 * e + 1] - mm[1]);
+          l[0] += p0, l[1] += p1;
+          if constexpr (Q8) p0 *= vs[p][e] * iref, p1 *= vs[p][e] * iref;
+          const uint32_t high = pack<Q8>(p0, p1);
+          const float2 back = unpack<Q8>(high);
+          const uint32_t low = pack<Q8>(p0 - back.x, p1 - back.y);
+          if constexpr (WIDE) {
+            bh[p][e] = transpose8(high);
+            bl[p][e] = transpose8(low);
+          } else {
+            bh[p][e] = transpose8(t < 2 ? high : low);
+          }
+        }
+      // O^T += V^T P^T: lanes (g, t) hold keys 2t, 2t+1, 2t+8, 2t+9 of elements v_elem(g, .).
 #pragma unroll
       for (int p = 0; p < PW; ++p) {
         const uint32_t page = base + G::KREG + (uint32_t)((sub * PW + p) * A.hpc) * G::CELL;
         const uint32_t vb = valid >> (16 * p);
+        auto product = [&](float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          mma<Q8>(d, a0, a1, a2, a3, bh[p][0], bh[p][1]);
+          if constexpr (WIDE) mma<Q8>(d, a0, a1, a2, a3, bl[p][0], bl[p][1]);
+        };
 #pragma unroll
         for (int x = 0; x < G::NX; ++x) {
           constexpr int VB = G::SB / 8;  // bytes of a slice row this lane takes
@@ -580,17 +644,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
             if constexpr (Q8) {  // 4 elements per word
               const uint32_t a01 = __byte_perm(w[0][e], w[1][e], 0x5140), a23 = __byte_perm(w[0][e], w[1][e], 0x7362);
               const uint32_t b01 = __byte_perm(w[2][e], w[3][e], 0x5140), b23 = __byte_perm(w[2][e], w[3][e], 0x7362);
-              const int j = x * G::VE + e * 4;
-              mma<true>(o[j], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a01), widen(b01));
-              mma<true>(o[j + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a01 >> 16), widen(b01 >> 16));
-              mma<true>(o[j + 2], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a23), widen(b23));
-              mma<true>(o[j + 3], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], widen(a23 >> 16), widen(b23 >> 16));
+              const int j = (x * G::VE + e * 4) / 2;
+              product(o[j], widen(a01), widen_hi(a01), widen(b01), widen_hi(b01));
+              product(o[j + 1], widen(a23), widen_hi(a23), widen(b23), widen_hi(b23));
             } else {  // 2 elements per word
-              const int j = x * G::VE + e * 2;
-              mma<false>(o[j], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1],
-                         __byte_perm(w[0][e], w[1][e], 0x5410), __byte_perm(w[2][e], w[3][e], 0x5410));
-              mma<false>(o[j + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1],
-                         __byte_perm(w[0][e], w[1][e], 0x7632), __byte_perm(w[2][e], w[3][e], 0x7632));
+              product(o[(x * G::VE + e * 2) / 2], __byte_perm(w[0][e], w[1][e], 0x5410), __byte_perm(w[0][e], w[1][e], 0x7632),
+                      __byte_perm(w[2][e], w[3][e], 0x5410), __byte_perm(w[2][e], w[3][e], 0x7632));
             }
           }
         }
@@ -603,33 +662,42 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     return;
   }
-  // This lane: columns v_elem(2t, j), v_elem(2t + 1, j) of query head g; high and low weight parts added.
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (!live || g >= nq) return;
-  const float fin = Q8 ? ref : 1.f;
-  if (A.chunks == 0 && row_parts(L, A.first, A.split, A.wph) <= 1) {
-    const float inv = l > 0.f ? fin / l : 0.f;  // no keys: zeros
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)qh * HD;
+  // Sums over the keys; high and low weight parts of a narrow group added.
 #pragma unroll
-    for (int j = 0; j < G::NT; j += 4)
+  for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<uint2*>(dst + G::v_elem(2 * t + e, j)) =
-            make_uint2(pack<false>((o[j][e] + o[j][2 + e]) * inv, (o[j + 1][e] + o[j + 1][2 + e]) * inv),
-                       pack<false>((o[j + 2][e] + o[j + 2][2 + e]) * inv, (o[j + 3][e] + o[j + 3][2 + e]) * inv));
-    return;
+    for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int j = 0; j < G::NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
   }
-  const size_t pi = ((size_t)row * a.n_heads + qh) * A.parts + A.chunks + sp * A.wph + sub;
-  float* po = A.part_o + pi * HD;
+  if (!live) return;
+  const float fin = Q8 ? ref : 1.f;
+  const bool direct = A.chunks == 0 && row_parts(L, A.first, A.split, A.wph) <= 1;
 #pragma unroll
-  for (int j = 0; j < G::NT; j += 4)
+  for (int e = 0; e < 2; ++e) {  // query heads q0 + 2t, q0 + 2t + 1
+    const int qi = 2 * t + e;
+    if (qi >= nq || (!WIDE && t >= 2)) continue;
+    if (direct) {
+      const float inv = l[e] > 0.f ? fin / l[e] : l[e] == 0.f ? 0.f : l[e];  // no keys: zeros; NaN stays
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)(q0 + qi) * HD;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      *reinterpret_cast<float4*>(po + G::v_elem(2 * t + e, j)) =
-          make_float4((o[j][e] + o[j][2 + e]) * fin, (o[j + 1][e] + o[j + 1][2 + e]) * fin,
-                      (o[j + 2][e] + o[j + 2][2 + e]) * fin, (o[j + 3][e] + o[j + 3][2 + e]) * fin);
-  if (t == 0) A.part_ml[pi] = make_float2(m, l);
+      for (int i = 0; i < HD / 8; i += 4)
+        *reinterpret_cast<uint2*>(dst + G::v_elem(g, i)) =
+            make_uint2(pack<false>(o[i / 2][e] * inv, o[i / 2][2 + e] * inv),
+                       pack<false>(o[i / 2 + 1][e] * inv, o[i / 2 + 1][2 + e] * inv));
+    } else {
+      const size_t pi = ((size_t)row * a.n_heads + q0 + qi) * A.parts + A.chunks + sp * A.wph + sub;
+      float* po = A.part_o + pi * HD;
+#pragma unroll
+      for (int i = 0; i < HD / 8; i += 4)
+        *reinterpret_cast<float4*>(po + G::v_elem(g, i)) =
+            make_float4(o[i / 2][e] * fin, o[i / 2][2 + e] * fin, o[i / 2 + 1][e] * fin, o[i / 2 + 1][2 + e] * fin);
+      if (g == 0) A.part_ml[pi] = make_float2(m[e], l[e]);
+    }
+  }
 }
 
 // Join a row's partials in split order: one warp per (row, query head), lane j
@@ -655,9 +723,11 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
     }
     const int* t0 = a.cache.block_table + (size_t)base * a.cache.max_blocks;
     const int* t1 = a.cache.block_table + (size_t)seq * a.cache.max_blocks;
-    bool same = true;
-    for (int p = lane; p < min(A.first, pos + 1 + 15) / 16; p += 32) same = same && t0[p] == t1[p];
-    if (!same) report(a.status, CDB_OPS_NOT_SHARED);
+    int differ = 0;
+    const int pages = min(A.first, max(pos, -1) + 16) / 16;
+#pragma unroll 8
+    for (int p = lane; p < pages; p += 32) differ |= t0[p] ^ t1[p];
+    if (differ) report(a.status, CDB_OPS_NOT_SHARED);
   }
   const int L = pos + 1;
   const int parts = A.chunks + row_parts(L, A.first, A.split, A.wph);
@@ -678,22 +748,22 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
     for (int k = 0; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       l += __shfl_sync(0xffffffffu, ls, k);
-      if (cols && wk > 0.f) {
+      if (cols && wk != 0.f) {
         const float4 x = *reinterpret_cast<const float4*>(A.part_o + (pi + s0 + k) * HD + 4 * lane);
         v.x = fmaf(x.x, wk, v.x), v.y = fmaf(x.y, wk, v.y), v.z = fmaf(x.z, wk, v.z), v.w = fmaf(x.w, wk, v.w);
       }
     }
   }
   if (!cols) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no keys: zeros; NaN stays
   uint2 r;
   r.x = pack<false>(v.x * inv, v.y * inv);
   r.y = pack<false>(v.z * inv, v.w * inv);
   *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)h * HD + 4 * lane) = r;
 }
 
-template <int HD, bool Q8>
-cudaError_t launch(cudaStream_t s, const Args& A) {
+template <int HD, bool Q8, bool WIDE>
+cudaError_t launch_as(cudaStream_t s, const Args& A) {
   using G = Geo<HD, Q8>;
   const cdb_paged_cache& c = A.a.cache;
   CUtensorMap tm;
@@ -703,14 +773,19 @@ cudaError_t launch(cudaStream_t s, const Args& A) {
   const int dev = current_device();
   if (!set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k_decode<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
+        cudaFuncSetAttribute(k_decode<HD, Q8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const int splits = max(1, (A.a.max_ctx - A.first + A.split - 1) / A.split);
+  const int splits = std::max(1, (A.a.max_ctx - A.first + A.split - 1) / A.split);
   count_launch();
-  cudaError_t e = launch_pdl(k_decode<HD, Q8>, dim3((unsigned)A.a.rows * A.nhg, splits), dim3((kWarps + 1) * 32), G::SMEM,
-                             s, tm, A);
+  return launch_pdl(k_decode<HD, Q8, WIDE>, dim3((unsigned)A.a.rows * A.nhg, splits), dim3((kWarps + 1) * 32), G::SMEM, s, tm,
+                    A);
+}
+
+template <int HD, bool Q8>
+cudaError_t launch(cudaStream_t s, const Args& A) {
+  const cudaError_t e = A.group > 4 ? launch_as<HD, Q8, true>(s, A) : launch_as<HD, Q8, false>(s, A);
   if (e != cudaSuccess || (A.chunks == 0 && A.parts <= 1)) return e;
   count_launch();
   const long long items = (long long)A.a.rows * A.a.n_heads;

@@ -56,17 +56,20 @@ struct Geo {
   static constexpr int QBYTES = NX * QSLICE;
   static constexpr int KSLICE = kKeys * 128;
   static constexpr int KVB = NX * KSLICE;             // K (or V) of a block
-  static constexpr int STAGE = 2 * KVB;
-  static constexpr int NS = 4;                        // blocks between copy and last use
+  // K and V have rings of their own: K is given back as soon as its scores are
+  // computed, two blocks before its V is used, so more blocks are in flight.
+  static constexpr int KS = Q8 ? 3 : 5;
+  static constexpr int VS = Q8 ? 4 : 6;
   static constexpr int RAWKV = kKeys * HD;            // codes of K (or V) of a block
   static constexpr int RAW = Q8 ? 2 * RAWKV + 2 * kKeys * 4 : 0;
   static constexpr int NR = Q8 ? 3 : 0;               // code blocks in flight
-  static constexpr int OFF_KV = QBYTES;
-  static constexpr int OFF_RAW = OFF_KV + NS * STAGE;
-  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: scales of the blocks in use, [NS][K, V][kKeys]
-  static constexpr int OFF_XCH = OFF_SC + (Q8 ? NS * 2 * kKeys * 4 : 0);  // float2 [2][kRows]
+  static constexpr int OFF_K = QBYTES;
+  static constexpr int OFF_V = OFF_K + KS * KVB;
+  static constexpr int OFF_RAW = OFF_V + VS * KVB;
+  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: scales of the blocks in use, [VS][K, V][kKeys]
+  static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * 2 * kKeys * 4 : 0);  // float2 [2][kRows]
   static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8;
-  static constexpr int NBAR = 2 + 2 * NS + 4 + 4 + 2 + 2 * 3;
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 4 + 4 + 2 + 2 * 3;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int THREADS = 320 + (Q8 ? 128 : 0);
   static constexpr int O_COL = 0;                     // [2][HD]
@@ -92,13 +95,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem;
-  uint8_t* kvs = smem + G::OFF_KV;
   float2* xch = reinterpret_cast<float2*>(smem + G::OFF_XCH);
   uint64_t* qbar = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);
   uint64_t* done = qbar + 1;
-  uint64_t* kv_full = done + 1;
-  uint64_t* kv_empty = kv_full + G::NS;
-  uint64_t* s_full = kv_empty + G::NS;  // [group][buffer]
+  uint64_t* k_full = done + 1;
+  uint64_t* k_empty = k_full + G::KS;
+  uint64_t* v_full = k_empty + G::KS;
+  uint64_t* v_empty = v_full + G::VS;
+  uint64_t* s_full = v_empty + G::VS;   // [group][buffer]
   uint64_t* p_full = s_full + 4;        // [group][buffer]
   uint64_t* o_done = p_full + 4;        // [group]
   uint64_t* raw_full = o_done + 2;
@@ -114,9 +118,13 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     if (!Q8) asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
     mbar_init(qbar, 1);
     mbar_init(done, 1);
-    for (int s = 0; s < G::NS; ++s) {
-      mbar_init(&kv_full[s], Q8 ? 4 : 1);
-      mbar_init(&kv_empty[s], 1);
+    for (int s = 0; s < G::KS; ++s) {
+      mbar_init(&k_full[s], Q8 ? 4 : 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < G::VS; ++s) {
+      mbar_init(&v_full[s], Q8 ? 4 : 1);
+      mbar_init(&v_empty[s], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -164,12 +172,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     }
     bool ok = true;
     int issued = 0;
-    uint64_t* full = Q8 ? raw_full : kv_full;
-    uint64_t* empty = Q8 ? raw_empty : kv_empty;
-    constexpr int N = Q8 ? 3 : G::NS;
     int blk_l = -1;
     for (int j = 0; j < nb; ++j) {
-      const int s = j % N;
       if ((j & 7) == 0) {  // table entries of the next eight blocks, one per lane
         const int pg = 4 * j + lane;
         blk_l = base >= 0 && pg < npg ? bt[pg] : -1;
@@ -177,38 +181,52 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       }
       const int blk = __shfl_sync(0xffffffffu, blk_l, ((j & 7) * 4 + lane) & 31);
       const bool mine = lane < 4 && blk >= 0;
-      const int n = __popc(__ballot_sync(0xffffffffu, mine));
-      if (j >= N && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((j / N) - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) mbar_arrive_tx(&full[s], (uint32_t)n * (Q8 ? 2 * 16 * HD + 2 * 64 : 2 * G::NX * 16 * 128));
-      __syncwarp();
-      if (mine) {
-        const long long head = ((long long)blk * c.n_kv_slots + a.slot_base) * 2 * c.n_kv_heads + kh;
-        if constexpr (Q8) {
+      const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine));
+      const long long head = ((long long)blk * c.n_kv_slots + a.slot_base) * 2 * c.n_kv_heads + kh;
+      if constexpr (Q8) {
+        const int s = j % G::NR;
+        if (j >= G::NR && !(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[s], ((j / G::NR) - 1) & 1)))) break;
+        if (lane == 0) mbar_arrive_tx(&raw_full[s], n * (2 * 16 * HD + 2 * 64));
+        __syncwarp();
+        if (mine) {
           const uint32_t st = su32(smem + G::OFF_RAW + (size_t)s * G::RAW);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const long long at = (head + kv * c.n_kv_heads) * 16;
-            bulk_1d(st + kv * G::RAWKV + lane * 16 * HD, static_cast<const uint8_t*>(c.pool) + at * HD, 16 * HD, &full[s]);
-            bulk_1d(st + 2 * G::RAWKV + (kv * kKeys + lane * 16) * 4, c.scales + at, 64, &full[s]);
-          }
-        } else {
-          const uint32_t st = su32(kvs + (size_t)s * G::STAGE);
-          const int y = (int)(head * 16);
-          for (int x = 0; x < G::NX; ++x) {
-            tma_2d(st + x * G::KSLICE + lane * 16 * 128, &tmk, &full[s], x * 128, y, pol);
-            tma_2d(st + G::KVB + x * G::KSLICE + lane * 16 * 128, &tmk, &full[s], x * 128, y + c.n_kv_heads * 16, pol);
+            bulk_1d(st + kv * G::RAWKV + lane * 16 * HD, static_cast<const uint8_t*>(c.pool) + at * HD, 16 * HD, &raw_full[s]);
+            bulk_1d(st + 2 * G::RAWKV + (kv * kKeys + lane * 16) * 4, c.scales + at, 64, &raw_full[s]);
           }
         }
+      } else {
+        const int sk = j % G::KS, sv = j % G::VS;
+        const int y = (int)(head * 16);
+        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[sk], ((j / G::KS) - 1) & 1)))) break;
+        if (lane == 0) mbar_arrive_tx(&k_full[sk], n * (G::NX * 16 * 128));
+        __syncwarp();
+        if (mine)
+          for (int x = 0; x < G::NX; ++x)
+            tma_2d(su32(smem + G::OFF_K + sk * G::KVB) + x * G::KSLICE + lane * 16 * 128, &tmk, &k_full[sk], x * 128, y, pol);
+        issued = 2 * j + 1;
+        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[sv], ((j / G::VS) - 1) & 1)))) break;
+        if (lane == 0) mbar_arrive_tx(&v_full[sv], n * (G::NX * 16 * 128));
+        __syncwarp();
+        if (mine)
+          for (int x = 0; x < G::NX; ++x)
+            tma_2d(su32(smem + G::OFF_V + sv * G::KVB) + x * G::KSLICE + lane * 16 * 128, &tmk, &v_full[sv], x * 128,
+                   y + c.n_kv_heads * 16, pol);
       }
-      issued = j + 1;
+      issued = 2 * j + 2;
     }
     if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     // Copies in flight land before the CTA may leave (at once when everything was used).
     mbar_wait(qbar, 0);
-    for (int j = max(0, issued - N); j < issued; ++j) mbar_wait(&full[j % N], (j / N) & 1);
+    const int nk = (issued + 1) / 2, nv = issued / 2;
+    if constexpr (Q8) {
+      for (int j = max(0, nv - G::NR); j < nv; ++j) mbar_wait(&raw_full[j % G::NR], (j / G::NR) & 1);
+    } else {
+      for (int j = max(0, nk - G::KS); j < nk; ++j) mbar_wait(&k_full[j % G::KS], (j / G::KS) & 1);
+      for (int j = max(0, nv - G::VS); j < nv; ++j) mbar_wait(&v_full[j % G::VS], (j / G::VS) & 1);
+    }
   } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
@@ -216,33 +234,35 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       const uint32_t qa = su32(qs);
       bool ok = mbar_wait(qbar, 0);
       auto scores = [&](int i) -> bool {  // S of block i: group i & 1, buffer (i >> 1) & 1
-        const int s = i % G::NS, g = i & 1, n = i >> 1;
-        if (!mbar_wait(&kv_full[s], (i / G::NS) & 1)) return false;
+        const int s = i % G::KS, g = i & 1, n = i >> 1;
+        if (!mbar_wait(&k_full[s], (i / G::KS) & 1)) return false;
         // The buffer held the weights of the group's block n - 2.
         if (n >= 2 && !mbar_wait(&o_done[g], (n - 2) & 1)) return false;
         fence_after();
-        const uint32_t kb = su32(kvs + (size_t)s * G::STAGE);
+        const uint32_t kb = su32(smem + G::OFF_K + s * G::KVB);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           mma_ss(tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys, desc_k(qa + (kk / 4) * G::QSLICE + (kk % 4) * 32),
                  desc_k(kb + (kk / 4) * G::KSLICE + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
         commit(&s_full[g * 2 + (n & 1)]);
+        commit(&k_empty[s]);
         return true;
       };
       if (ok) ok = scores(0);
       if (ok && nb > 1) ok = scores(1);
       for (int i = 0; ok && i < nb; ++i) {
         if (i + 2 < nb && !(ok = scores(i + 2))) break;
-        const int s = i % G::NS, g = i & 1, n = i >> 1;
+        const int s = i % G::VS, g = i & 1, n = i >> 1;
+        if (!(ok = mbar_wait(&v_full[s], (i / G::VS) & 1))) break;
         if (!(ok = mbar_wait(&p_full[g * 2 + (n & 1)], (n >> 1) & 1))) break;
         fence_after();
-        const uint32_t vb = su32(kvs + (size_t)s * G::STAGE + G::KVB);
+        const uint32_t vb = su32(smem + G::OFF_V + s * G::KVB);
         const int steps = min(4, npg - 4 * i);  // pages behind the chunk were not copied
         for (int kk = 0; kk < steps; ++kk)
           mma_ts(tmem + G::O_COL + g * HD, tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys + kk * 8,
                  desc_mn(vb + kk * 2048, G::KSLICE), idO, (n > 0 || kk > 0) ? 1u : 0u);
         commit(&o_done[g]);
-        commit(&kv_empty[s]);
+        commit(&v_empty[s]);
       }
       if (!ok) report(a.status, CDB_OPS_TIMEOUT);
       commit(done);  // every MMA issued above completes before TMEM is released
@@ -254,20 +274,15 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       const int tid = threadIdx.x - 320;
       bool ok = true;
       for (int j = 0; j < nb; ++j) {
-        const int s = j % G::NS, r = j % 3;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[r], (j / 3) & 1)))) break;
-        if (j >= G::NS && !(ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((j / G::NS) - 1) & 1)))) break;
+        const int sk = j % G::KS, sv = j % G::VS, r = j % G::NR;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[r], (j / G::NR) & 1)))) break;
         const uint8_t* raw = smem + G::OFF_RAW + (size_t)r * G::RAW;
-        // The scales move along: the code block is given back before the softmax group reads them.
-        reinterpret_cast<float*>(smem + G::OFF_SC)[s * 2 * kKeys + tid] = reinterpret_cast<const float*>(raw + 2 * G::RAWKV)[tid];
         constexpr int C = HD / 16;  // 16-code pieces of a key row
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t dst = su32(kvs + (size_t)s * G::STAGE + kv * G::KVB);
+        auto turn = [&](const uint8_t* src, uint32_t dst) {
 #pragma unroll 4
           for (int u = tid; u < kKeys * C; u += 128) {
             const int key = u / C, p = u % C;
-            const uint4 w = *reinterpret_cast<const uint4*>(raw + kv * G::RAWKV + key * HD + p * 16);
+            const uint4 w = *reinterpret_cast<const uint4*>(src + key * HD + p * 16);
             uint32_t o[8];
             const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -281,11 +296,20 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
             st_shared_v4(line + ((c0 ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
             st_shared_v4(line + (((c0 + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
-        }
+        };
+        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[sk], ((j / G::KS) - 1) & 1)))) break;
+        turn(raw, su32(smem + G::OFF_K + sk * G::KVB));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[sk]);
+        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[sv], ((j / G::VS) - 1) & 1)))) break;
+        // The scales move along: the code block is given back before the softmax group reads them.
+        reinterpret_cast<float*>(smem + G::OFF_SC)[sv * 2 * kKeys + tid] = reinterpret_cast<const float*>(raw + 2 * G::RAWKV)[tid];
+        turn(raw + G::RAWKV, su32(smem + G::OFF_V + sv * G::KVB));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&kv_full[s]);
+          mbar_arrive(&v_full[sv]);
           mbar_arrive(&raw_empty[r]);
         }
       }
@@ -300,7 +324,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     const int seq = in ? a.seq[br] : -1, pos = in ? a.pos[br] : -1;
     const bool live = in && seq >= 0 && seq < c.n_seqs && pos < a.max_ctx;
     const int lim = min(pos, k_hi - 1) - k_lo;  // last key of this row, from the chunk's first
-    const float scale = a.scale * 1.4426950408889634f;
+    // Scores in the log2 domain; a negative factor turns the scores around first, so that the
+    // maximum can be taken before the factor is applied.
+    const bool turn_round = a.scale < 0.f;
+    const float scale = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);  // not 0: a masked score stays -inf
     constexpr float kTau = 8.f;  // rescale O only when the row maximum grows by more than 2^8
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t to = trow + G::O_COL + g * HD;
@@ -315,10 +342,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       float sv[64];
       tmem_ld32(ts, sv);
       tmem_ld32(ts + 32, sv + 32);
+      if (turn_round) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
+      }
       const float4* ks = nullptr;  // scales of the block's keys, then of its values
       if constexpr (Q8) {
-        const int st = i % G::NS;  // complete: the scores came from it
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[st], (i / G::NS) & 1)))) break;
+        const int st = i % G::VS;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (i / G::VS) & 1)))) break;
         ks = reinterpret_cast<const float4*>(smem + G::OFF_SC + st * 2 * kKeys * 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 4; ++k) {
@@ -327,20 +358,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         }
       }
       const int left = lim - i * kKeys;  // keys 0..left of the block are this row's
-      float mx = -INFINITY;
-      if (__all_sync(0xffffffffu, left >= kKeys - 1)) {
+      if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          sv[k] *= scale;
-          mx = fmaxf(mx, sv[k]);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          sv[k] = k <= left ? sv[k] * scale : -INFINITY;
-          mx = fmaxf(mx, sv[k]);
-        }
+        for (int k = 0; k < 64; ++k) sv[k] = k <= left ? sv[k] : -INFINITY;
       }
+      float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x4[e] = max3(x4[e], sv[k + 2 * e], sv[k + 2 * e + 1]);
+      const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale;
       const float mnew = mx > m + kTau ? mx : m;
       if (n > 0 && __any_sync(0xffffffffu, mnew != m)) {
         // O holds the group's earlier blocks against the old maximum.
@@ -360,11 +387,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       m = mnew;
       const float mm = m == -INFINITY ? 0.f : m;
       uint32_t p[32];
+      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+      uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
-        const float x0 = ex2(sv[2 * e] - mm), x1 = ex2(sv[2 * e + 1] - mm);
-        const float x2 = ex2(sv[2 * e + 2] - mm), x3 = ex2(sv[2 * e + 3] - mm);
-        l += (x0 + x1) + (x2 + x3);
+        float x0, x1, x2, x3;
+        unpair(fma2(pair(sv[2 * e], sv[2 * e + 1]), s2, m2), x0, x1);
+        unpair(fma2(pair(sv[2 * e + 2], sv[2 * e + 3]), s2, m2), x2, x3);
+        x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+        l2[0] = add2(l2[0], pair(x0, x1));
+        l2[1] = add2(l2[1], pair(x2, x3));
         if constexpr (Q8) {
           const float4 f = ks[kKeys / 4 + e / 2];
           // No weight times a scale that may be NaN (pages behind the chunk).
@@ -375,6 +407,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           p[e + 1] = pack_bf16(x2, x3);
         }
       }
+      float la, lb, lc, ld;
+      unpair(l2[0], la, lb);
+      unpair(l2[1], lc, ld);
+      l = (la + lb) + (lc + ld);
       tmem_st32(ts, p);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();

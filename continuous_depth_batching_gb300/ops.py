@@ -81,18 +81,19 @@ class _Op:
         """Device pointer of a contiguous vector of at least n elements."""
         if t is None:
             return None
-        if t.dtype != dtype or t.device.index != self.dev or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        if t.dtype is not dtype or t.get_device() != self.dev or t.numel() < n or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous {dtype} vector of at least {n} on cuda:{self.dev}, got "
                              f"{tuple(t.shape)} {t.dtype} on {t.device}")
         return t.data_ptr()
 
     def _mat(self, name, t, dtypes, rows, cols):
         """Device pointer and row stride of a [>= rows, >= cols] matrix with contiguous rows."""
-        if (t.dtype not in dtypes or t.device.index != self.dev or t.dim() != 2 or t.shape[0] < rows or
-                t.shape[1] < cols or (t.stride(1) != 1 and t.shape[1] > 1)):
+        shape, stride = t.shape, t.stride()
+        if (t.dtype not in dtypes or t.get_device() != self.dev or len(shape) != 2 or shape[0] < rows or
+                shape[1] < cols or (stride[1] != 1 and shape[1] > 1)):
             raise ValueError(f"{name}: expected [{rows}, {cols}] with contiguous rows of {dtypes} on cuda:{self.dev}, "
-                             f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-        return t.data_ptr(), max(t.stride(0), t.shape[1])
+                             f"got {tuple(shape)} {t.dtype} on {t.device}")
+        return t.data_ptr(), max(stride[0], shape[1])
 
 
 class Sampler(_Op):
