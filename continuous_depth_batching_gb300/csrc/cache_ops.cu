@@ -415,25 +415,30 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         break;
       }
       const uint32_t cell = (uint32_t)A.hpc * G::CELL;  // one page of the CTA's heads, K or V
-      if (lane == 0) {
+      const uint32_t stage = su32(smem + (size_t)s * G::STAGE);
+      if (elect_one()) {
         masks[s] = mask;
         mbar_arrive_tx(&full[s], (uint32_t)__popc(mask) * (2 * cell + (Q8 ? 2u * heads * 64 : 0u)));
       }
       __syncwarp();
-      if (ok) {
-        // Rows of head k0's page at this block and slot; V follows n_kv_heads pages later.
-        const long long head0 = ((long long)blk * c.n_kv_slots + slot) * 2 * c.n_kv_heads + k0;
-        const uint32_t base = su32(smem + (size_t)s * G::STAGE) + lane * cell;
+      for (int i = 0; i < pps; ++i) {
+        const int b = __shfl_sync(0xffffffffu, blk, i);
+        if (!((mask >> i) & 1u)) continue;
+        if (elect_one()) {
+          // Rows of head k0's page at this block and slot; V follows n_kv_heads pages later.
+          const long long head0 = ((long long)b * c.n_kv_slots + slot) * 2 * c.n_kv_heads + k0;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int y = (int)((head0 + kv * c.n_kv_heads) * 16);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int y = (int)((head0 + kv * c.n_kv_heads) * 16);
 #pragma unroll
-          for (int x = 0; x < G::NX; ++x)
-            tma_2d(base + kv * G::KREG + x * (A.hpc * 16 * G::SB), &tm, &full[s], x * G::SB, y, pol);
-          if constexpr (Q8)
-            bulk_1d(su32(smem + (size_t)s * G::STAGE) + 2 * G::KREG + (kv * G::PG + lane * A.hpc) * 64,
-                    c.scales + (head0 + kv * c.n_kv_heads) * 16, (uint32_t)heads * 64, &full[s]);
+            for (int x = 0; x < G::NX; ++x)
+              tma_2d(stage + i * cell + kv * G::KREG + x * (A.hpc * 16 * G::SB), &tm, &full[s], x * G::SB, y, pol);
+            if constexpr (Q8)
+              bulk_1d(stage + 2 * G::KREG + (kv * G::PG + i * A.hpc) * 64, c.scales + (head0 + kv * c.n_kv_heads) * 16,
+                      (uint32_t)heads * 64, &full[s]);
+          }
         }
+        __syncwarp();
       }
       issued = st + 1;
     }

@@ -16,16 +16,24 @@
 // the other group is in its exponentials.  The two are joined at the end.
 //   warps 0-3, 4-7  softmax groups: thread t owns query row t (its TMEM lane);
 //                   it reads its 64 scores, and writes the weights back over
-//                   them as bf16 (rounding each weight by at most 2^-9 of it,
-//                   less than the bf16 output's own rounding; the sum that
-//                   normalises is of the fp32 weights): the weights are the A
-//                   operand of the second product straight from TMEM;
-//   warp 8          TMA producer (q tile, key blocks);
-//   warp 9          MMA issuer: S = Q K^T (128 x 64), O += P V;
-//   warps 10-13     e4m3 only: turn code blocks into bf16 K and V in the MMA's
-//                   swizzled layout.  Codes are exact in bf16; a key's scale
-//                   multiplies its fp32 score, a value's scale its weight
-//                   before that is rounded, so e4m3 costs no further rounding.
+//                   them in 16 bits (each rounded by at most 2^-8 of it in
+//                   bf16, less than the output's own rounding does to a sum;
+//                   the sum that normalises is of the fp32 weights): the
+//                   weights are the A operand of the second product straight
+//                   from TMEM;
+//   warps 8, 11     TMA producers: q tile and K blocks, V blocks (a copy takes its
+//                   warp some 40 cycles to issue, and a block is 16 of them);
+//   warp 9          issues S = Q K^T (128 x 64), up to four blocks ahead;
+//   warp 10         issues O += P V;
+//   warps 12-15     e4m3 only: widen code blocks to fp16 in the MMA's swizzled
+//                   layout (exactly; one conversion per two codes, where bf16
+//                   would take four instructions).  A key's scale multiplies
+//                   its fp32 score, a value's scale its weight, relative to
+//                   the largest value scale so far (fp16's range), and q is
+//                   turned to fp16 in place, each row by a power of two.
+// Waits and issues of one block cost a warp some 500 cycles (a commit about
+// 140, a wait 100), as much as the products themselves: hence two issuing warps,
+// one commit per product, and pairs of barriers that two lanes wait for at once.
 // TMEM: two output accumulators of head_dim columns, two score buffers of 64
 // columns per group.  V is an N-major B operand in its stored order.  Every
 // mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT, lets
@@ -58,7 +66,7 @@ struct Geo {
   static constexpr int KVB = NX * KSLICE;             // K (or V) of a block
   // K and V have rings of their own: K is given back as soon as its scores are
   // computed, two blocks before its V is used, so more blocks are in flight.
-  static constexpr int KS = Q8 ? 3 : 5;
+  static constexpr int KS = Q8 ? 4 : 5;
   static constexpr int VS = Q8 ? 4 : 6;
   static constexpr int RAWKV = kKeys * HD;            // codes of K (or V) of a block
   static constexpr int RAW = Q8 ? 2 * RAWKV + 2 * kKeys * 4 : 0;
@@ -66,12 +74,13 @@ struct Geo {
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_V = OFF_K + KS * KVB;
   static constexpr int OFF_RAW = OFF_V + VS * KVB;
-  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: scales of the blocks in use, [VS][K, V][kKeys]
-  static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * 2 * kKeys * 4 : 0);  // float2 [2][kRows]
-  static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8;
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 4 + 4 + 2 + 2 * 3;
+  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: [VS] scales of K, of V, and two maxima of V's
+  static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * (2 * kKeys + 4) * 4 : 0);  // float2 [2][kRows], float [2]
+  static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8 + 16;
+  static constexpr int NBAR = 4 + 2 * KS + 2 * VS + 4 + 2 * 3;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
-  static constexpr int THREADS = 320 + (Q8 ? 128 : 0);
+  static constexpr int SCN = 2 * kKeys + 4;
+  static constexpr int THREADS = 384 + (Q8 ? 128 : 0);
   static constexpr int O_COL = 0;                     // [2][HD]
   static constexpr int S_COL = 2 * HD;                // [2 groups][2 buffers][64]
   static constexpr int TMEM_COLS = 512;
@@ -97,15 +106,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint8_t* qs = smem;
   float2* xch = reinterpret_cast<float2*>(smem + G::OFF_XCH);
   uint64_t* qbar = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);
-  uint64_t* done = qbar + 1;
-  uint64_t* k_full = done + 1;
-  uint64_t* k_empty = k_full + G::KS;
-  uint64_t* v_full = k_empty + G::KS;
-  uint64_t* v_empty = v_full + G::VS;
-  uint64_t* s_full = v_empty + G::VS;   // [group][buffer]
-  uint64_t* p_full = s_full + 4;        // [group][buffer]
-  uint64_t* o_done = p_full + 4;        // [group]
-  uint64_t* raw_full = o_done + 2;
+  uint64_t* q_ready = qbar + 1;         // e4m3: q is fp16
+  uint64_t* done = q_ready + 1;         // [2]: both issuing warps' last MMAs
+  uint64_t* k_full = done + 2;
+  uint64_t* s_full = k_full + G::KS;    // scores of the block in this K slot are complete: the slot is free
+  uint64_t* v_full = s_full + G::KS;
+  uint64_t* o_done = v_full + G::VS;    // the product with the V slot is complete: slot and weights are free
+  uint64_t* p_full = o_done + G::VS;    // [group][buffer]
+  uint64_t* raw_full = p_full + 4;
   uint64_t* raw_empty = raw_full + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + 3);
 
@@ -117,23 +125,20 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tmq) : "memory");
     if (!Q8) asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
     mbar_init(qbar, 1);
-    mbar_init(done, 1);
+    mbar_init(q_ready, 8);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     for (int s = 0; s < G::KS; ++s) {
       mbar_init(&k_full[s], Q8 ? 4 : 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&s_full[s], 1);
     }
     for (int s = 0; s < G::VS; ++s) {
       mbar_init(&v_full[s], Q8 ? 4 : 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&o_done[s], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-    }
-    mbar_init(&o_done[0], 1);
-    mbar_init(&o_done[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_full[i], 2);
       mbar_init(&raw_empty[i], 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -154,8 +159,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;  // >= 1
   const int npg = (k_hi - k_lo) / 16;
 
-  if (warp == 8) {
-    // ---------------- producer ----------------
+  if (warp == 8 || warp == 11) {
+    // ---------------- producers ----------------
+    constexpr int kPage = 16 * HD * (Q8 ? 1 : 2);  // bytes of a page of one head, K or V
+    const int kv = warp == 8 ? 0 : 1;
     // The first sequence of the batch names the prefix's blocks.
     int base = -1;
     for (int r0 = 0; r0 < a.rows && base < 0; r0 += 32) {
@@ -166,112 +173,117 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     const int* bt = c.block_table + (size_t)max(base, 0) * c.max_blocks + k_lo / 16;
     uint64_t pol;  // the prefix is read again by the other tiles and by the next steps
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-    if (lane == 0) {
+    if (kv == 0 && elect_one()) {
       mbar_arrive_tx(qbar, (uint32_t)(G::NX * A.group * A.tile_rows * 128));
       for (int x = 0; x < G::NX; ++x) tma_3d(su32(qs + x * G::QSLICE), &tmq, qbar, x * 64, kh * A.group, row0);
     }
+    __syncwarp();
+    // The ring this warp fills: K or V slots, or its half of the code slots.
+    const int slots = Q8 ? G::NR : kv ? G::VS : G::KS;
+    uint64_t* full = Q8 ? raw_full : kv ? v_full : k_full;
+    uint64_t* empty = Q8 ? raw_empty : kv ? o_done : s_full;
+    const uint32_t ring = su32(smem + (Q8 ? G::OFF_RAW + kv * G::RAWKV : kv ? G::OFF_V : G::OFF_K));
     bool ok = true;
-    int issued = 0;
-    int blk_l = -1;
+    int issued = 0, blk_l = -1, s = 0;
+    uint32_t parity = 1;  // of the slot's last use, from the second round on
     for (int j = 0; j < nb; ++j) {
       if ((j & 7) == 0) {  // table entries of the next eight blocks, one per lane
         const int pg = 4 * j + lane;
         blk_l = base >= 0 && pg < npg ? bt[pg] : -1;
         if (base >= 0 && pg < npg && (blk_l < 0 || blk_l >= c.kv_blocks)) report(a.status, CDB_OPS_BAD_BLOCK), blk_l = -1;
       }
-      const int blk = __shfl_sync(0xffffffffu, blk_l, ((j & 7) * 4 + lane) & 31);
-      const bool mine = lane < 4 && blk >= 0;
-      const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine));
-      const long long head = ((long long)blk * c.n_kv_slots + a.slot_base) * 2 * c.n_kv_heads + kh;
-      if constexpr (Q8) {
-        const int s = j % G::NR;
-        if (j >= G::NR && !(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[s], ((j / G::NR) - 1) & 1)))) break;
-        if (lane == 0) mbar_arrive_tx(&raw_full[s], n * (2 * 16 * HD + 2 * 64));
-        __syncwarp();
-        if (mine) {
-          const uint32_t st = su32(smem + G::OFF_RAW + (size_t)s * G::RAW);
+      int blk[4], n = 0;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const long long at = (head + kv * c.n_kv_heads) * 16;
-            bulk_1d(st + kv * G::RAWKV + lane * 16 * HD, static_cast<const uint8_t*>(c.pool) + at * HD, 16 * HD, &raw_full[s]);
-            bulk_1d(st + 2 * G::RAWKV + (kv * kKeys + lane * 16) * 4, c.scales + at, 64, &raw_full[s]);
+      for (int i = 0; i < 4; ++i) {
+        blk[i] = __shfl_sync(0xffffffffu, blk_l, (j & 7) * 4 + i);
+        n += blk[i] >= 0;
+      }
+      if (j >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], parity)))) break;
+      if (elect_one()) {
+        mbar_arrive_tx(&full[s], (uint32_t)n * (kPage + (Q8 ? 64 : 0)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (blk[i] < 0) continue;
+          // Key rows before this head's page (V follows n_kv_heads pages after K).
+          const long long at = ((((long long)blk[i] * c.n_kv_slots + a.slot_base) * 2 + kv) * c.n_kv_heads + kh) * 16;
+          if constexpr (Q8) {
+            const uint32_t st = ring + s * G::RAW;
+            bulk_1d(st + i * kPage, static_cast<const uint8_t*>(c.pool) + at * HD, kPage, &full[s]);
+            bulk_1d(st - kv * G::RAWKV + 2 * G::RAWKV + (kv * kKeys + i * 16) * 4, c.scales + at, 64, &full[s]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < G::NX; ++x)
+              tma_2d(ring + s * G::KVB + x * G::KSLICE + i * 16 * 128, &tmk, &full[s], x * 128, (int)at, pol);
           }
         }
-      } else {
-        const int sk = j % G::KS, sv = j % G::VS;
-        const int y = (int)(head * 16);
-        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[sk], ((j / G::KS) - 1) & 1)))) break;
-        if (lane == 0) mbar_arrive_tx(&k_full[sk], n * (G::NX * 16 * 128));
-        __syncwarp();
-        if (mine)
-          for (int x = 0; x < G::NX; ++x)
-            tma_2d(su32(smem + G::OFF_K + sk * G::KVB) + x * G::KSLICE + lane * 16 * 128, &tmk, &k_full[sk], x * 128, y, pol);
-        issued = 2 * j + 1;
-        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[sv], ((j / G::VS) - 1) & 1)))) break;
-        if (lane == 0) mbar_arrive_tx(&v_full[sv], n * (G::NX * 16 * 128));
-        __syncwarp();
-        if (mine)
-          for (int x = 0; x < G::NX; ++x)
-            tma_2d(su32(smem + G::OFF_V + sv * G::KVB) + x * G::KSLICE + lane * 16 * 128, &tmk, &v_full[sv], x * 128,
-                   y + c.n_kv_heads * 16, pol);
       }
-      issued = 2 * j + 2;
+      __syncwarp();
+      issued = j + 1;
+      if (++s == slots) s = 0, parity ^= 1;
     }
     if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     // Copies in flight land before the CTA may leave (at once when everything was used).
-    mbar_wait(qbar, 0);
-    const int nk = (issued + 1) / 2, nv = issued / 2;
-    if constexpr (Q8) {
-      for (int j = max(0, nv - G::NR); j < nv; ++j) mbar_wait(&raw_full[j % G::NR], (j / G::NR) & 1);
-    } else {
-      for (int j = max(0, nk - G::KS); j < nk; ++j) mbar_wait(&k_full[j % G::KS], (j / G::KS) & 1);
-      for (int j = max(0, nv - G::VS); j < nv; ++j) mbar_wait(&v_full[j % G::VS], (j / G::VS) & 1);
-    }
+    if (kv == 0) mbar_wait(qbar, 0);
+    for (int j = max(0, issued - slots); j < issued; ++j) mbar_wait(&full[j % slots], (j / slots) & 1);
   } else if (warp == 9) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(kRows, kKeys, false), idO = idesc_bf16(kRows, HD, true);
-      const uint32_t qa = su32(qs);
-      bool ok = mbar_wait(qbar, 0);
-      auto scores = [&](int i) -> bool {  // S of block i: group i & 1, buffer (i >> 1) & 1
-        const int s = i % G::KS, g = i & 1, n = i >> 1;
-        if (!mbar_wait(&k_full[s], (i / G::KS) & 1)) return false;
-        // The buffer held the weights of the group's block n - 2.
-        if (n >= 2 && !mbar_wait(&o_done[g], (n - 2) & 1)) return false;
-        fence_after();
-        const uint32_t kb = su32(smem + G::OFF_K + s * G::KVB);
+    // ---------------- scores ----------------
+    constexpr uint32_t id = idesc_16(!Q8, kRows, kKeys, false);
+    const uint64_t qd = desc_k(su32(qs)), kd = desc_k(su32(smem + G::OFF_K));  // addresses count in 16-byte units
+    bool ok = __all_sync(0xffffffffu, mbar_wait(Q8 ? q_ready : qbar, 0));
+    for (int i = 0; ok && i < nb; ++i) {  // block i: group i & 1, buffer (i >> 1) & 1
+      const int s = i % G::KS;
+      // Lane 1 waits for the product with the weights that the buffer held, block i - 4's; the others for K.
+      uint64_t* bar = &k_full[s];
+      uint32_t parity = (i / G::KS) & 1;
+      if (lane == 1 && i >= 4) bar = &o_done[(i - 4) % G::VS], parity = ((i - 4) / G::VS) & 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)))) break;
+      fence_after();
+      const uint64_t kb = kd + (uint32_t)(s * (G::KVB / 16));
+      const uint32_t d = tmem + G::S_COL + ((i & 1) * 2 + ((i >> 1) & 1)) * kKeys;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss(tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys, desc_k(qa + (kk / 4) * G::QSLICE + (kk % 4) * 32),
-                 desc_k(kb + (kk / 4) * G::KSLICE + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
-        commit(&s_full[g * 2 + (n & 1)]);
-        commit(&k_empty[s]);
-        return true;
-      };
-      if (ok) ok = scores(0);
-      if (ok && nb > 1) ok = scores(1);
-      for (int i = 0; ok && i < nb; ++i) {
-        if (i + 2 < nb && !(ok = scores(i + 2))) break;
-        const int s = i % G::VS, g = i & 1, n = i >> 1;
-        if (!(ok = mbar_wait(&v_full[s], (i / G::VS) & 1))) break;
-        if (!(ok = mbar_wait(&p_full[g * 2 + (n & 1)], (n >> 1) & 1))) break;
-        fence_after();
-        const uint32_t vb = su32(smem + G::OFF_V + s * G::KVB);
-        const int steps = min(4, npg - 4 * i);  // pages behind the chunk were not copied
-        for (int kk = 0; kk < steps; ++kk)
-          mma_ts(tmem + G::O_COL + g * HD, tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys + kk * 8,
-                 desc_mn(vb + kk * 2048, G::KSLICE), idO, (n > 0 || kk > 0) ? 1u : 0u);
-        commit(&o_done[g]);
-        commit(&v_empty[s]);
+          mma_ss(d, qd + ((kk / 4) * G::QSLICE + (kk % 4) * 32) / 16, kb + ((kk / 4) * G::KSLICE + (kk % 4) * 32) / 16, id,
+                 kk > 0 ? 1u : 0u);
+        commit(&s_full[s]);
       }
-      if (!ok) report(a.status, CDB_OPS_TIMEOUT);
-      commit(done);  // every MMA issued above completes before TMEM is released
-      mbar_wait(done, 0);
+      __syncwarp();
     }
-  } else if (warp >= 10) {
+    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    if (elect_one()) commit(&done[0]);  // every MMA issued above completes before TMEM is released
+    __syncwarp();
+    mbar_wait(&done[0], 0);
+  } else if (warp == 10) {
+    // ---------------- weights times values ----------------
+    constexpr uint32_t id = idesc_16(!Q8, kRows, HD, true);
+    const uint64_t vd = desc_mn(su32(smem + G::OFF_V), G::KSLICE);
+    bool ok = true;
+    for (int i = 0; i < nb; ++i) {
+      const int s = i % G::VS, g = i & 1, n = i >> 1;
+      const bool other = lane == 1;  // lane 1 waits for V, the others for the weights
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &v_full[s] : &p_full[g * 2 + (n & 1)],
+                                                   other ? (i / G::VS) & 1 : (n >> 1) & 1))))
+        break;
+      fence_after();
+      const uint64_t vb = vd + (uint32_t)(s * (G::KVB / 16));
+      const uint32_t d = tmem + G::O_COL + g * HD, p = tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys;
+      const int steps = npg - 4 * i;  // pages behind the chunk were not copied
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * 2048) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
+        commit(&o_done[s]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    if (elect_one()) commit(&done[1]);
+    __syncwarp();
+    mbar_wait(&done[1], 0);
+  } else if (warp >= 12) {
     // ---------------- code converters (e4m3) ----------------
     if constexpr (Q8) {
-      const int tid = threadIdx.x - 320;
+      const int tid = threadIdx.x - 384;
       bool ok = true;
       for (int j = 0; j < nb; ++j) {
         const int sk = j % G::KS, sv = j % G::VS, r = j % G::NR;
@@ -283,28 +295,26 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           for (int u = tid; u < kKeys * C; u += 128) {
             const int key = u / C, p = u % C;
             const uint4 w = *reinterpret_cast<const uint4*>(src + key * HD + p * 16);
-            uint32_t o[8];
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 x = widen2(in[e]), y = widen2(in[e] >> 16);
-              o[2 * e] = pack_bf16(x.x, x.y);
-              o[2 * e + 1] = pack_bf16(y.x, y.y);
-            }
             const uint32_t line = dst + (p / 4) * G::KSLICE + key * 128;
             const int c0 = (p % 4) * 2;
-            st_shared_v4(line + ((c0 ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
-            st_shared_v4(line + (((c0 + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+            st_shared_v4(line + ((c0 ^ (key & 7)) << 4), widen(w.x), widen_hi(w.x), widen(w.y), widen_hi(w.y));
+            st_shared_v4(line + (((c0 + 1) ^ (key & 7)) << 4), widen(w.z), widen_hi(w.z), widen(w.w), widen_hi(w.w));
           }
         };
-        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[sk], ((j / G::KS) - 1) & 1)))) break;
+        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sk], ((j / G::KS) - 1) & 1)))) break;
         turn(raw, su32(smem + G::OFF_K + sk * G::KVB));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[sk]);
-        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[sv], ((j / G::VS) - 1) & 1)))) break;
+        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[sv], ((j / G::VS) - 1) & 1)))) break;
         // The scales move along: the code block is given back before the softmax group reads them.
-        reinterpret_cast<float*>(smem + G::OFF_SC)[sv * 2 * kKeys + tid] = reinterpret_cast<const float*>(raw + 2 * G::RAWKV)[tid];
+        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + sv * G::SCN;
+        const float f = reinterpret_cast<const float*>(raw + 2 * G::RAWKV)[tid];
+        sc[tid] = f;
+        if (tid >= kKeys) {  // the largest of the value scales that were copied, by halves (as integers: none is negative)
+          const uint32_t fm = __reduce_max_sync(0xffffffffu, (tid - kKeys) / 16 < npg - 4 * j ? __float_as_uint(f) : 0u);
+          if (lane == 0) sc[2 * kKeys + (tid - kKeys) / 32] = __uint_as_float(fm);
+        }
         turn(raw + G::RAWKV, su32(smem + G::OFF_V + sv * G::KVB));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -327,16 +337,60 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     // Scores in the log2 domain; a negative factor turns the scores around first, so that the
     // maximum can be taken before the factor is applied.
     const bool turn_round = a.scale < 0.f;
-    const float scale = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);  // not 0: a masked score stays -inf
+    float scale = fabsf(a.scale) * 1.4426950408889634f;
     constexpr float kTau = 8.f;  // rescale O only when the row maximum grows by more than 2^8
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t to = trow + G::O_COL + g * HD;
     float m = -INFINITY, l = 0.f;
+    float ref = 0x1p-126f, iref = 0x1p126f;  // e4m3: value scale the weights are relative to, its reciprocal
+    float up = 1.f;                          // e4m3: what q was divided by
     bool ok = true;
+    if constexpr (Q8) {
+      // q to fp16 in place: the groups take a slice each (head_dim 64: the first group), every thread its row.
+      ok = __all_sync(0xffffffffu, mbar_wait(qbar, 0));
+      float mx = 0.f;
+#pragma unroll
+      for (int x = 0; x < G::NX; ++x)
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 w = *reinterpret_cast<const uint4*>(qs + x * G::QSLICE + r * 128 + ch * 16);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+        }
+      // 2^-e and 2^e for mx = 2^e f; 1 for zero, tiny, infinite or NaN maxima.
+      const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
+      const bool norm = eb > 0x00800000u && eb < 0x7E000000u;
+      const float down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f;
+      up = norm ? __uint_as_float(eb) : 1.f;
+      asm volatile("bar.sync 2, 256;" ::: "memory");  // both groups have read the row
+      if (g < G::NX) {
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          uint4* at = reinterpret_cast<uint4*>(qs + g * G::QSLICE + r * 128 + ch * 16);
+          const uint4 w = *at;
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xFFFF0000u) * down);
+          *at = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    }
+    scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     int n = 0;  // blocks of this group so far
-    for (int i = g; i < nb; i += 2, ++n) {
+    for (int i = g; ok && i < nb; i += 2, ++n) {
       const int b = g * 2 + (n & 1);
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (n >> 1) & 1)))) break;
+      // Lane 1 waits for the scales too (e4m3), which come with V.
+      const bool other = Q8 && lane == 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1) &&
+                                             (!other || mbar_wait(&v_full[i % G::VS], (i / G::VS) & 1)))))
+        break;
       fence_after();
       const uint32_t ts = trow + G::S_COL + b * kKeys;
       float sv[64];
@@ -347,15 +401,15 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
       }
       const float4* ks = nullptr;  // scales of the block's keys, then of its values
+      float vmax = 0.f;
       if constexpr (Q8) {
-        const int st = i % G::VS;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (i / G::VS) & 1)))) break;
-        ks = reinterpret_cast<const float4*>(smem + G::OFF_SC + st * 2 * kKeys * 4);
+        ks = reinterpret_cast<const float4*>(smem + G::OFF_SC + (i % G::VS) * G::SCN * 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 4; ++k) {
           const float4 f = ks[k];
           sv[4 * k] *= f.x, sv[4 * k + 1] *= f.y, sv[4 * k + 2] *= f.z, sv[4 * k + 3] *= f.w;
         }
+        vmax = fmaxf(ks[kKeys / 2].x, ks[kKeys / 2].y);
       }
       const int left = lim - i * kKeys;  // keys 0..left of the block are this row's
       if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
@@ -369,22 +423,27 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         for (int e = 0; e < 4; ++e) x4[e] = max3(x4[e], sv[k + 2 * e], sv[k + 2 * e + 1]);
       const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale;
       const float mnew = mx > m + kTau ? mx : m;
-      if (n > 0 && __any_sync(0xffffffffu, mnew != m)) {
-        // O holds the group's earlier blocks against the old maximum.
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[g], (n - 1) & 1)))) break;
-        fence_after();
+      const float rnew = Q8 && vmax > 64.f * ref ? vmax : ref;  // the same in every thread
+      if (__any_sync(0xffffffffu, mnew != m) || rnew != ref) {
         const float f = m == -INFINITY ? 0.f : ex2(m - mnew);
-#pragma unroll 1
-        for (int c0 = 0; c0 < HD; c0 += 32) {
-          float v[32];
-          tmem_ld32(to + c0, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= f;
-          tmem_st32(to + c0, reinterpret_cast<const uint32_t*>(v));
-        }
         l *= f;
+        m = mnew;
+        if (n > 0) {
+          // O holds the group's earlier blocks against the old maximum.
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[(i - 2) % G::VS], ((i - 2) / G::VS) & 1)))) break;
+          fence_after();
+          const float fo = Q8 ? f * (ref / rnew) : f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 32) {
+            float v[32];
+            tmem_ld32(to + c0, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= fo;
+            tmem_st32(to + c0, reinterpret_cast<const uint32_t*>(v));
+          }
+        }
+        if (Q8 && rnew != ref) ref = rnew, iref = 1.f / rnew;
       }
-      m = mnew;
       const float mm = m == -INFINITY ? 0.f : m;
       uint32_t p[32];
       const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
@@ -399,9 +458,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         l2[1] = add2(l2[1], pair(x2, x3));
         if constexpr (Q8) {
           const float4 f = ks[kKeys / 4 + e / 2];
-          // No weight times a scale that may be NaN (pages behind the chunk).
-          p[e] = pack_bf16(x0 > 0.f ? x0 * f.x : 0.f, x1 > 0.f ? x1 * f.y : 0.f);
-          p[e + 1] = pack_bf16(x2 > 0.f ? x2 * f.z : 0.f, x3 > 0.f ? x3 * f.w : 0.f);
+          // Keys behind the chunk may have any scale, NaN too, but their pages are not multiplied.
+          p[e] = pack_f16(x0 * (f.x * iref), x1 * (f.y * iref));
+          p[e + 1] = pack_f16(x2 * (f.z * iref), x3 * (f.w * iref));
         } else {
           p[e] = pack_bf16(x0, x1);
           p[e + 1] = pack_bf16(x2, x3);
@@ -417,9 +476,12 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[b]);
     }
-    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[g], (n - 1) & 1));
+    const int last = g + 2 * (n - 1);
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[last % G::VS], (last / G::VS) & 1));
     fence_after();
+    float2* xr = xch + 2 * kRows;  // e4m3: the groups' value scales
     xch[g * kRows + r] = make_float2(m, l);
+    if (Q8 && r == 0) reinterpret_cast<float*>(xr)[g] = ref;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (!ok) {
       if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
@@ -428,6 +490,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       const float2 e0 = xch[r], e1 = xch[kRows + r];
       const float mj = fmaxf(e0.x, e1.x);
       const float f0 = e0.x == -INFINITY ? 0.f : ex2(e0.x - mj), f1 = e1.x == -INFINITY ? 0.f : ex2(e1.x - mj);
+      const float r0 = Q8 ? reinterpret_cast<const float*>(xr)[0] : 1.f, r1 = Q8 ? reinterpret_cast<const float*>(xr)[1] : 1.f;
       const int h = kh * A.group + r % A.group;
       const size_t pi = ((size_t)br * a.n_heads + h) * A.parts + chunk;
       float* po = A.part_o + pi * HD + g * (HD / 2);
@@ -436,17 +499,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       for (int c0 = 0; c0 < HD / 2; c0 += 32) {
         float v[32], w[32];
         tmem_ld32(t0 + c0, v);
-        if (nb > 1) {
-          tmem_ld32(t0 + HD + c0, w);
+        if (nb > 1) tmem_ld32(t0 + HD + c0, w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = v[e] * f0 + w[e] * f1;
-        }
+        for (int e = 0; e < 32; ++e) v[e] = v[e] * (f0 * r0) + (nb > 1 ? w[e] * (f1 * r1) : 0.f);
         if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(po + c0 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
-      // A single block leaves group 1 without a state: f0 is 1 (or the row has no key at all).
       if (live && g == 0) A.part_ml[pi] = make_float2(mj, e0.y * f0 + e1.y * f1);
     }
   }
