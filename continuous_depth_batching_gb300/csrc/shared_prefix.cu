@@ -21,21 +21,26 @@
 //                   the sum that normalises is of the fp32 weights): the
 //                   weights are the A operand of the second product straight
 //                   from TMEM;
-//   warps 8, 11     TMA producers: q tile and K blocks, V blocks (a copy takes its
-//                   warp some 40 cycles to issue, and a block is 16 of them);
-//   warp 9          issues S = Q K^T (128 x 64), up to four blocks ahead;
+//   warps 8, 11     TMA producers: q tile and K blocks, V blocks.  A copy takes
+//                   its warp some 70 cycles to issue, so a page is one copy: a
+//                   4-dimensional box lays its 128-byte slices out as
+//                   [8 keys][slice][key][128 bytes], which both operands read;
+//   warp 9          issues S = Q K^T (128 x 64), up to three blocks ahead, with q
+//                   from TMEM too (the softmax groups put it there): shared
+//                   memory has to feed K and V only, 64 KB a block with the
+//                   copies, where q would add 32;
 //   warp 10         issues O += P V;
 //   warps 12-15     e4m3 only: widen code blocks to fp16 in the MMA's swizzled
 //                   layout (exactly; one conversion per two codes, where bf16
 //                   would take four instructions).  A key's scale multiplies
 //                   its fp32 score, a value's scale its weight, relative to
-//                   the largest value scale so far (fp16's range), and q is
-//                   turned to fp16 in place, each row by a power of two.
+//                   the largest value scale so far (fp16's range); q becomes
+//                   fp16, each row divided by a power of two.
 // Waits and issues of one block cost a warp some 500 cycles (a commit about
 // 140, a wait 100), as much as the products themselves: hence two issuing warps,
 // one commit per product, and pairs of barriers that two lanes wait for at once.
-// TMEM: two output accumulators of head_dim columns, two score buffers of 64
-// columns per group.  V is an N-major B operand in its stored order.  Every
+// TMEM: two output accumulators of head_dim columns, q in head_dim / 2, three
+// score buffers of 64 columns (all 512 with head_dim 128).  V is an N-major B operand in its stored order.  Every
 // mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT, lets
 // its own copies and MMAs finish (bounded), frees TMEM and returns.
 #include "../../include/cdb.h"
@@ -62,27 +67,29 @@ struct Geo {
   static constexpr int NX = HD / 64;                  // 128-byte slices of a bf16 row
   static constexpr int QSLICE = kRows * 128;
   static constexpr int QBYTES = NX * QSLICE;
-  static constexpr int KSLICE = kKeys * 128;
-  static constexpr int KVB = NX * KSLICE;             // K (or V) of a block
+  static constexpr int OCT = NX * 1024;               // 8 keys of a block, slice by slice
+  static constexpr int PAGE = 2 * OCT;
+  static constexpr int KVB = 4 * PAGE;                // K (or V) of a block
   // K and V have rings of their own: K is given back as soon as its scores are
   // computed, two blocks before its V is used, so more blocks are in flight.
-  static constexpr int KS = Q8 ? 4 : 5;
+  static constexpr int KS = Q8 ? 3 : 5;
   static constexpr int VS = Q8 ? 4 : 6;
   static constexpr int RAWKV = kKeys * HD;            // codes of K (or V) of a block
   static constexpr int RAW = Q8 ? 2 * RAWKV + 2 * kKeys * 4 : 0;
-  static constexpr int NR = Q8 ? 3 : 0;               // code blocks in flight
+  static constexpr int NR = Q8 ? 4 : 0;               // code blocks in flight
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_V = OFF_K + KS * KVB;
   static constexpr int OFF_RAW = OFF_V + VS * KVB;
   static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: [VS] scales of K, of V, and two maxima of V's
   static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * (2 * kKeys + 4) * 4 : 0);  // float2 [2][kRows], float [2]
   static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8 + 16;
-  static constexpr int NBAR = 4 + 2 * KS + 2 * VS + 4 + 2 * 3;
+  static constexpr int NBAR = 4 + 2 * KS + 2 * VS + 3 + 2 * 4;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int SCN = 2 * kKeys + 4;
   static constexpr int THREADS = 384 + (Q8 ? 128 : 0);
   static constexpr int O_COL = 0;                     // [2][HD]
-  static constexpr int S_COL = 2 * HD;                // [2 groups][2 buffers][64]
+  static constexpr int Q_COL = 2 * HD;                // head_dim / 2, two 16-bit elements per column
+  static constexpr int S_COL = Q_COL + HD / 2;        // [3][64]: block i's scores, then weights, in buffer i % 3
   static constexpr int TMEM_COLS = 512;
 };
 
@@ -96,6 +103,18 @@ struct Args {
   float2* part_ml;
 };
 
+// The first sequence of the batch, which names the prefix's blocks (-1: none).
+__device__ __forceinline__ int first_sequence(const cdb_attention_args& a) {
+  const int lane = threadIdx.x & 31;
+  int base = -1;
+  for (int r0 = 0; r0 < a.rows && base < 0; r0 += 32) {
+    const int s = r0 + lane < a.rows ? a.seq[r0 + lane] : -1;
+    const uint32_t has = __ballot_sync(0xffffffffu, s >= 0 && s < a.cache.n_seqs);
+    if (has) base = __shfl_sync(0xffffffffu, s, __ffs(has) - 1);
+  }
+  return base;
+}
+
 template <int HD, bool Q8>
 __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     k_shared_prefix(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -106,16 +125,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint8_t* qs = smem;
   float2* xch = reinterpret_cast<float2*>(smem + G::OFF_XCH);
   uint64_t* qbar = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);
-  uint64_t* q_ready = qbar + 1;         // e4m3: q is fp16
+  uint64_t* q_ready = qbar + 1;         // q is in TMEM
   uint64_t* done = q_ready + 1;         // [2]: both issuing warps' last MMAs
   uint64_t* k_full = done + 2;
   uint64_t* s_full = k_full + G::KS;    // scores of the block in this K slot are complete: the slot is free
   uint64_t* v_full = s_full + G::KS;
   uint64_t* o_done = v_full + G::VS;    // the product with the V slot is complete: slot and weights are free
-  uint64_t* p_full = o_done + G::VS;    // [group][buffer]
-  uint64_t* raw_full = p_full + 4;
-  uint64_t* raw_empty = raw_full + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + 3);
+  uint64_t* p_full = o_done + G::VS;    // the weights in the score buffer are complete
+  uint64_t* raw_full = p_full + 3;
+  uint64_t* raw_empty = raw_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + 4);
 
   const cdb_attention_args& a = A.a;
   const cdb_paged_cache& c = a.cache;
@@ -123,21 +142,21 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   const int kh = blockIdx.x, row0 = blockIdx.y * A.tile_rows, chunk = blockIdx.z;
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tmq) : "memory");
-    if (!Q8) asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
     mbar_init(qbar, 1);
     mbar_init(q_ready, 8);
     mbar_init(&done[0], 1);
     mbar_init(&done[1], 1);
     for (int s = 0; s < G::KS; ++s) {
-      mbar_init(&k_full[s], Q8 ? 4 : 1);
+      mbar_init(&k_full[s], Q8 ? 2 : 1);
       mbar_init(&s_full[s], 1);
     }
     for (int s = 0; s < G::VS; ++s) {
-      mbar_init(&v_full[s], Q8 ? 4 : 1);
+      mbar_init(&v_full[s], Q8 ? 2 : 1);
       mbar_init(&o_done[s], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 3; ++i) mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&raw_full[i], 2);
       mbar_init(&raw_empty[i], 4);
     }
@@ -163,13 +182,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     // ---------------- producers ----------------
     constexpr int kPage = 16 * HD * (Q8 ? 1 : 2);  // bytes of a page of one head, K or V
     const int kv = warp == 8 ? 0 : 1;
-    // The first sequence of the batch names the prefix's blocks.
-    int base = -1;
-    for (int r0 = 0; r0 < a.rows && base < 0; r0 += 32) {
-      const int s = r0 + lane < a.rows ? a.seq[r0 + lane] : -1;
-      const uint32_t has = __ballot_sync(0xffffffffu, s >= 0 && s < c.n_seqs);
-      if (has) base = __shfl_sync(0xffffffffu, s, __ffs(has) - 1);
-    }
+    const int base = first_sequence(a);
     const int* bt = c.block_table + (size_t)max(base, 0) * c.max_blocks + k_lo / 16;
     uint64_t pol;  // the prefix is read again by the other tiles and by the next steps
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
@@ -207,14 +220,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           // Key rows before this head's page (V follows n_kv_heads pages after K).
           const long long at = ((((long long)blk[i] * c.n_kv_slots + a.slot_base) * 2 + kv) * c.n_kv_heads + kh) * 16;
           if constexpr (Q8) {
-            const uint32_t st = ring + s * G::RAW;
-            bulk_1d(st + i * kPage, static_cast<const uint8_t*>(c.pool) + at * HD, kPage, &full[s]);
-            bulk_1d(st - kv * G::RAWKV + 2 * G::RAWKV + (kv * kKeys + i * 16) * 4, c.scales + at, 64, &full[s]);
-          } else {
-#pragma unroll
-            for (int x = 0; x < G::NX; ++x)
-              tma_2d(ring + s * G::KVB + x * G::KSLICE + i * 16 * 128, &tmk, &full[s], x * 128, (int)at, pol);
-          }
+            tma_2d(ring + s * G::RAW + i * kPage, &tmk, &full[s], 0, (int)at, pol);
+            bulk_1d(ring + s * G::RAW + (2 - kv) * G::RAWKV + (kv * kKeys + i * 16) * 4, c.scales + at, 64, &full[s]);
+          } else
+            tma_4d(ring + s * G::KVB + i * G::PAGE, &tmk, &full[s], 0, 0, 0, (int)(at / 8), pol);
         }
       }
       __syncwarp();
@@ -228,23 +237,22 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   } else if (warp == 9) {
     // ---------------- scores ----------------
     constexpr uint32_t id = idesc_16(!Q8, kRows, kKeys, false);
-    const uint64_t qd = desc_k(su32(qs)), kd = desc_k(su32(smem + G::OFF_K));  // addresses count in 16-byte units
-    bool ok = __all_sync(0xffffffffu, mbar_wait(Q8 ? q_ready : qbar, 0));
-    for (int i = 0; ok && i < nb; ++i) {  // block i: group i & 1, buffer (i >> 1) & 1
+    const uint64_t kd = desc_k(su32(smem + G::OFF_K), G::OCT);  // addresses in 16-byte units
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_ready, 0));
+    for (int i = 0; ok && i < nb; ++i) {
       const int s = i % G::KS;
-      // Lane 1 waits for the product with the weights that the buffer held, block i - 4's; the others for K.
+      // Lane 1 waits for the product with the weights that the buffer held, block i - 3's; the others for K.
       uint64_t* bar = &k_full[s];
       uint32_t parity = (i / G::KS) & 1;
-      if (lane == 1 && i >= 4) bar = &o_done[(i - 4) % G::VS], parity = ((i - 4) / G::VS) & 1;
+      if (lane == 1 && i >= 3) bar = &o_done[(i - 3) % G::VS], parity = ((i - 3) / G::VS) & 1;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)))) break;
       fence_after();
       const uint64_t kb = kd + (uint32_t)(s * (G::KVB / 16));
-      const uint32_t d = tmem + G::S_COL + ((i & 1) * 2 + ((i >> 1) & 1)) * kKeys;
+      const uint32_t d = tmem + G::S_COL + (i % 3) * kKeys;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss(d, qd + ((kk / 4) * G::QSLICE + (kk % 4) * 32) / 16, kb + ((kk / 4) * G::KSLICE + (kk % 4) * 32) / 16, id,
-                 kk > 0 ? 1u : 0u);
+          mma_ts(d, tmem + G::Q_COL + kk * 8, kb + ((kk / 4) * 1024 + (kk % 4) * 32) / 16, id, kk > 0 ? 1u : 0u);
         commit(&s_full[s]);
       }
       __syncwarp();
@@ -256,22 +264,20 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   } else if (warp == 10) {
     // ---------------- weights times values ----------------
     constexpr uint32_t id = idesc_16(!Q8, kRows, HD, true);
-    const uint64_t vd = desc_mn(su32(smem + G::OFF_V), G::KSLICE);
+    const uint64_t vd = desc_mn(su32(smem + G::OFF_V), 1024, G::OCT);
     bool ok = true;
     for (int i = 0; i < nb; ++i) {
       const int s = i % G::VS, g = i & 1, n = i >> 1;
       const bool other = lane == 1;  // lane 1 waits for V, the others for the weights
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &v_full[s] : &p_full[g * 2 + (n & 1)],
-                                                   other ? (i / G::VS) & 1 : (n >> 1) & 1))))
-        break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &v_full[s] : &p_full[i % 3], (other ? i / G::VS : i / 3) & 1)))) break;
       fence_after();
       const uint64_t vb = vd + (uint32_t)(s * (G::KVB / 16));
-      const uint32_t d = tmem + G::O_COL + g * HD, p = tmem + G::S_COL + (g * 2 + (n & 1)) * kKeys;
+      const uint32_t d = tmem + G::O_COL + g * HD, p = tmem + G::S_COL + (i % 3) * kKeys;
       const int steps = npg - 4 * i;  // pages behind the chunk were not copied
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * 2048) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
+          if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * G::PAGE) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
         commit(&o_done[s]);
       }
       __syncwarp();
@@ -283,43 +289,49 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   } else if (warp >= 12) {
     // ---------------- code converters (e4m3) ----------------
     if constexpr (Q8) {
-      const int tid = threadIdx.x - 384;
+      // Two warps for K, two for V.  8 codes to 16 bytes at a time: the lanes of a half warp (hd 64: a quarter)
+      // take a key's row, so loads and stores of a warp meet every bank once, and the addresses of one thread
+      // are a constant apart.
+      const int kv = warp >= 14 ? 1 : 0, tid = (threadIdx.x - 384) & 63;
+      constexpr int C = HD / 8, KI = 64 / C;  // 8-code pieces of a row, rows of one step
+      const int key = tid / C, p = tid % C;
+      const int slots = kv ? G::VS : G::KS;
+      uint64_t* full = kv ? v_full : k_full;
+      uint64_t* empty = kv ? o_done : s_full;
+      const uint32_t to = su32(smem + (kv ? G::OFF_V : G::OFF_K)) + (p / 8) * 1024;
       bool ok = true;
       for (int j = 0; j < nb; ++j) {
-        const int sk = j % G::KS, sv = j % G::VS, r = j % G::NR;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[r], (j / G::NR) & 1)))) break;
+        const int s = j % slots, r = j % G::NR;
+        const bool other = lane == 1 && j >= slots;  // lane 1 waits for the slot, the others for the codes
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &empty[s] : &raw_full[r],
+                                                     other ? ((j / slots) - 1) & 1 : (j / G::NR) & 1))))
+          break;
         const uint8_t* raw = smem + G::OFF_RAW + (size_t)r * G::RAW;
-        constexpr int C = HD / 16;  // 16-code pieces of a key row
-        auto turn = [&](const uint8_t* src, uint32_t dst) {
-#pragma unroll 4
-          for (int u = tid; u < kKeys * C; u += 128) {
-            const int key = u / C, p = u % C;
-            const uint4 w = *reinterpret_cast<const uint4*>(src + key * HD + p * 16);
-            const uint32_t line = dst + (p / 4) * G::KSLICE + key * 128;
-            const int c0 = (p % 4) * 2;
-            st_shared_v4(line + ((c0 ^ (key & 7)) << 4), widen(w.x), widen_hi(w.x), widen(w.y), widen_hi(w.y));
-            st_shared_v4(line + (((c0 + 1) ^ (key & 7)) << 4), widen(w.z), widen_hi(w.z), widen(w.w), widen_hi(w.w));
-          }
-        };
-        if (j >= G::KS && !(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sk], ((j / G::KS) - 1) & 1)))) break;
-        turn(raw, su32(smem + G::OFF_K + sk * G::KVB));
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[sk]);
-        if (j >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[sv], ((j / G::VS) - 1) & 1)))) break;
-        // The scales move along: the code block is given back before the softmax group reads them.
-        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + sv * G::SCN;
-        const float f = reinterpret_cast<const float*>(raw + 2 * G::RAWKV)[tid];
-        sc[tid] = f;
-        if (tid >= kKeys) {  // the largest of the value scales that were copied, by halves (as integers: none is negative)
-          const uint32_t fm = __reduce_max_sync(0xffffffffu, (tid - kKeys) / 16 < npg - 4 * j ? __float_as_uint(f) : 0u);
-          if (lane == 0) sc[2 * kKeys + (tid - kKeys) / 32] = __uint_as_float(fm);
+        const uint8_t* src = raw + kv * G::RAWKV + key * HD + p * 8;
+        uint2 w[kKeys / KI];
+#pragma unroll
+        for (int u = 0; u < kKeys / KI; ++u) w[u] = *reinterpret_cast<const uint2*>(src + u * KI * HD);
+        if (kv) {
+          // The scales move along: the code block is given back before the softmax group reads them.
+          float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + s * G::SCN;
+          const float* f = reinterpret_cast<const float*>(raw + 2 * G::RAWKV);
+          const float fv = f[kKeys + tid];
+          sc[tid] = f[tid];
+          sc[kKeys + tid] = fv;
+          // The largest of the value scales that were copied, by halves (as integers: none is negative).
+          const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fv) : 0u);
+          if (lane == 0) sc[2 * kKeys + tid / 32] = __uint_as_float(fm);
         }
-        turn(raw + G::RAWKV, su32(smem + G::OFF_V + sv * G::KVB));
+#pragma unroll
+        for (int u = 0; u < kKeys / KI; ++u) {
+          const int k = key + u * KI;
+          st_shared_v4(to + s * G::KVB + (k / 8) * G::OCT + (k % 8) * 128 + (((p % 8) ^ (k % 8)) << 4), widen(w[u].x),
+                       widen_hi(w[u].x), widen(w[u].y), widen_hi(w[u].y));
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&v_full[sv]);
+          mbar_arrive(&full[s]);
           mbar_arrive(&raw_empty[r]);
         }
       }
@@ -345,54 +357,55 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     float ref = 0x1p-126f, iref = 0x1p126f;  // e4m3: value scale the weights are relative to, its reciprocal
     float up = 1.f;                          // e4m3: what q was divided by
     bool ok = true;
-    if constexpr (Q8) {
-      // q to fp16 in place: the groups take a slice each (head_dim 64: the first group), every thread its row.
+    {
+      // q to TMEM, row by row (two 16-bit elements per column): the groups take a 64-element slice each.
       ok = __all_sync(0xffffffffu, mbar_wait(qbar, 0));
-      float mx = 0.f;
+      float down = 1.f;
+      if constexpr (Q8) {
+        float mx = 0.f;
 #pragma unroll
-      for (int x = 0; x < G::NX; ++x)
+        for (int x = 0; x < G::NX; ++x)
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          const uint4 w = *reinterpret_cast<const uint4*>(qs + x * G::QSLICE + r * 128 + ch * 16);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          for (int ch = 0; ch < 8; ++ch) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qs + x * G::QSLICE + r * 128 + ((ch ^ (r & 7)) << 4));
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
-        }
-      // 2^-e and 2^e for mx = 2^e f; 1 for zero, tiny, infinite or NaN maxima.
-      const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
-      const bool norm = eb > 0x00800000u && eb < 0x7E000000u;
-      const float down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f;
-      up = norm ? __uint_as_float(eb) : 1.f;
-      asm volatile("bar.sync 2, 256;" ::: "memory");  // both groups have read the row
-      if (g < G::NX) {
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          uint4* at = reinterpret_cast<uint4*>(qs + g * G::QSLICE + r * 128 + ch * 16);
-          const uint4 w = *at;
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xFFFF0000u) * down);
-          *at = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+            for (int e = 0; e < 4; ++e)
+              mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+          }
+        // 2^-e and 2^e for mx = 2^e f; 1 for zero, tiny, infinite or NaN maxima.
+        const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
+        const bool norm = eb > 0x00800000u && eb < 0x7E000000u;
+        down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f;
+        up = norm ? __uint_as_float(eb) : 1.f;
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (g < G::NX) {
+        uint32_t h[32];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 w = *reinterpret_cast<const uint4*>(qs + g * G::QSLICE + r * 128 + ((ch ^ (r & 7)) << 4));
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[4 * ch + e] = Q8 ? pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xFFFF0000u) * down) : v[e];
+        }
+        tmem_st32(trow + G::Q_COL + g * 32, h);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+      fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     }
     scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     int n = 0;  // blocks of this group so far
     for (int i = g; ok && i < nb; i += 2, ++n) {
-      const int b = g * 2 + (n & 1);
       // Lane 1 waits for the scales too (e4m3), which come with V.
       const bool other = Q8 && lane == 1;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1) &&
                                              (!other || mbar_wait(&v_full[i % G::VS], (i / G::VS) & 1)))))
         break;
       fence_after();
-      const uint32_t ts = trow + G::S_COL + b * kKeys;
+      const uint32_t ts = trow + G::S_COL + (i % 3) * kKeys;
       float sv[64];
       tmem_ld32(ts, sv);
       tmem_ld32(ts + 32, sv + 32);
@@ -407,7 +420,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < kKeys / 4; ++k) {
           const float4 f = ks[k];
-          sv[4 * k] *= f.x, sv[4 * k + 1] *= f.y, sv[4 * k + 2] *= f.z, sv[4 * k + 3] *= f.w;
+          unpair(mul2(pair(sv[4 * k], sv[4 * k + 1]), pair(f.x, f.y)), sv[4 * k], sv[4 * k + 1]);
+          unpair(mul2(pair(sv[4 * k + 2], sv[4 * k + 3]), pair(f.z, f.w)), sv[4 * k + 2], sv[4 * k + 3]);
         }
         vmax = fmaxf(ks[kKeys / 2].x, ks[kKeys / 2].y);
       }
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       }
       const float mm = m == -INFINITY ? 0.f : m;
       uint32_t p[32];
-      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm), i2 = pair(iref, iref);
       uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
@@ -459,8 +473,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         if constexpr (Q8) {
           const float4 f = ks[kKeys / 4 + e / 2];
           // Keys behind the chunk may have any scale, NaN too, but their pages are not multiplied.
-          p[e] = pack_f16(x0 * (f.x * iref), x1 * (f.y * iref));
-          p[e + 1] = pack_f16(x2 * (f.z * iref), x3 * (f.w * iref));
+          unpair(mul2(mul2(pair(f.x, f.y), i2), pair(x0, x1)), x0, x1);
+          unpair(mul2(mul2(pair(f.z, f.w), i2), pair(x2, x3)), x2, x3);
+          p[e] = pack_f16(x0, x1);
+          p[e + 1] = pack_f16(x2, x3);
         } else {
           p[e] = pack_bf16(x0, x1);
           p[e + 1] = pack_bf16(x2, x3);
@@ -474,7 +490,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[b]);
+      if (lane == 0) mbar_arrive(&p_full[i % 3]);
     }
     const int last = g + 2 * (n - 1);
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[last % G::VS], (last / G::VS) & 1));
@@ -527,7 +543,7 @@ cudaError_t launch(cudaStream_t s, const Args& A, int chunks) {
   if (!tmap_bf16_3d(&tq, a.q, HD, a.n_heads, a.rows, (uint64_t)HD * 2, (uint64_t)a.ldq * 2, 64, A.group, A.tile_rows))
     return cudaErrorInvalidValue;
   const uint64_t rows = (uint64_t)c.kv_blocks * c.n_kv_slots * 2 * c.n_kv_heads * 16;
-  if (!Q8 && !tmap_u8_2d(&tk, c.pool, HD * 2, rows, HD * 2, 128, 16, 128)) return cudaErrorInvalidValue;
+  if (Q8 ? !tmap_u8_2d(&tk, c.pool, HD, rows, HD, HD, 16, 0) : !tmap_bf16_octets(&tk, c.pool, HD, rows)) return cudaErrorInvalidValue;
   static bool set[kMaxDevices] = {};
   const int dev = current_device();
   if (!set[dev]) {

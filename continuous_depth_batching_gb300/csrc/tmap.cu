@@ -107,4 +107,16 @@ bool tmap_bf16_3d(CUtensorMap* out, const void* p, uint64_t d0, uint64_t d1, uin
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tmap_bf16_octets(CUtensorMap* out, const void* p, uint64_t hd, uint64_t rows) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, 8, hd / 64, rows / 8};
+  const cuuint64_t strides[3] = {hd * 2, 128, hd * 16};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(hd / 64), 2};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace cdb

@@ -24,4 +24,8 @@ bool tmap_u8_2d(CUtensorMap* out, const void* p, uint64_t inner, uint64_t outer,
 bool tmap_bf16_3d(CUtensorMap* out, const void* p, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1, uint64_t stride2,
                   uint32_t b0, uint32_t b1, uint32_t b2);
 
+// bf16 rows of hd elements (a multiple of 64) seen as [rows / 8][hd / 64][8][64], box 2 x hd/64 x 8 x 64
+// (16 rows, their 64-element slices 8 rows at a time), 128-byte swizzle; not cached.
+bool tmap_bf16_octets(CUtensorMap* out, const void* p, uint64_t hd, uint64_t rows);
+
 }  // namespace cdb
