@@ -10,13 +10,17 @@
 // of plain fp32, the running sum over a large vocabulary is off by enough that
 // one draw in some ten thousand would cross a border.
 //
-// Thresholds (top-k by count, top-p by mass) come from a radix search without
-// sorting: a first histogram over 1024 equal steps of m - x, then histograms
-// over the ordered bit patterns of the chosen bin, until the bin holds exactly
-// what is needed or a single value.  Each CTA adds up its slice in its own
-// shared memory, all CTAs of the cluster then read one another's histograms
-// (distributed shared memory) and find the same bin; two histogram buffers
-// leave one cluster barrier per step.
+// Thresholds come from a radix search without sorting: a histogram over 1024
+// equal steps of m - x, then histograms over the ordered bit patterns of the
+// chosen bin, until the bin holds exactly what is needed or a single value.
+// top_k counts, after the maxima of single threads have ruled out most of the
+// row.  top_p guesses its bin from fp32 weights and then adds up the exact mass
+// above and in it, so each logit's exact weight is computed once.  Each CTA
+// works on its slice in its own shared memory, all CTAs of the cluster then
+// read one another's histograms or sums (distributed shared memory) and come to
+// the same decision; two histogram buffers leave one cluster barrier per step.
+// What bounds it: the instructions of the weights (about 45 for each logit that
+// has mass) and, with few rows, the barriers.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -66,25 +70,23 @@ struct Note {
   int pad;
 };
 struct Tail {
-  unsigned long long mass;  // kept mass strictly above the threshold value
-  unsigned int ties;        // entries equal to the threshold value
-  unsigned int pad;
+  unsigned long long mass, in, below;  // kept mass above the threshold value; top_p: mass above the bin, in it, below it
+  unsigned int ties, cnt;       // entries equal to the threshold value; top_p: entries of the bin
 };
 
-struct Shared {
+struct alignas(16) Shared {
   unsigned int hist[2][4][kBins];  // count, then the low, middle and high 16 bits of the masses
   uint2 tab[kTab];                 // 2^(j/64) * 2^44 (low, high words)
   int tab30[kTab];                 // 2^(j/64) * 2^30
   Note note[kMaxCluster];
   Tail tail[kMaxCluster];
-  unsigned long long wm[kWarps];   // per-warp values of the scans
-  unsigned int wc[kWarps];
+  unsigned long long wm[kWarps], wi[kWarps], wb[kWarps];  // per-warp values of the scans and sums
+  unsigned int wc[kWarps], wn[kWarps];
   unsigned long long found_m;
-  unsigned int found_c, found_bin, found_n;
+  unsigned int found_bin, found_n;
   unsigned int lo, hi;
   float fmx[kWarps], fmn[kWarps];
   int fi[kWarps];
-  int token;
 };
 
 // Ordered bit pattern of a float (never NaN); bf16 values use its upper half.
@@ -139,10 +141,6 @@ struct Weigher {
   }
 };
 
-__device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, int o) {
-  return __shfl_up_sync(0xffffffffu, v, o);
-}
-
 // floor(f * s) for a float f in [0, 1) and s < 2^63, exactly.
 __device__ __forceinline__ unsigned long long mul_floor(float f, unsigned long long s) {
   if (!(f > 0.f)) return 0;
@@ -178,31 +176,118 @@ struct Keep {
   unsigned int t, r;
 };
 
+// 16 bytes of logits as stored: 4 fp32 or 8 bf16.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4, kDrop = 0;  // kDrop: low key bits that a logit of this type never uses
+  float4 v;
+  __device__ __forceinline__ float get(int i) const { return reinterpret_cast<const float*>(&v)[i]; }
+  __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<float*>(&v)[i] = x; }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8, kDrop = 16;
+  uint4 v;
+  __device__ __forceinline__ float get(int i) const {
+    const unsigned int w = reinterpret_cast<const unsigned int*>(&v)[i >> 1];
+    return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
+  }
+  __device__ __forceinline__ void set(int i, float x) {
+    unsigned int& w = reinterpret_cast<unsigned int*>(&v)[i >> 1];
+    w = (i & 1) ? (w & 0xFFFFu) | __float_as_uint(x) : (w & 0xFFFF0000u) | (__float_as_uint(x) >> 16);
+  }
+};
+
+// The cluster's view of one row; every member function is called by all
+// threads of all its CTAs.
 template <typename T>
 struct Row {
-  static constexpr int kDrop = sizeof(T) == 2 ? 16 : 0;  // low key bits that a bf16 logit never uses
+  static constexpr int E = Vec<T>::N, kDrop = Vec<T>::kDrop;
   Shared& S;
-  const float* xs;  // this CTA's slice
-  int n;            // its length
-  int rank, nc;
-  int buf = 0;
-  float m;
+  cg::cluster_group& cl;
+  const Vec<T>* xs;  // this CTA's slice, filled up with -inf to nv vectors
+  int nv, rank, nc;
+  float m;           // largest logit
+  float own_max;     // largest logit this thread loaded
+  int buf = 0;       // histogram buffer of the next step
 
-  __device__ __forceinline__ unsigned int key(float x) const { return order_bits(x) >> kDrop; }
+  static __device__ __forceinline__ unsigned int key(float x) { return order_bits(x) >> kDrop; }
+  static __device__ __forceinline__ float value(unsigned int k) {  // of a key
+    return from_order((k << kDrop) | (kDrop && !(k & 0x8000u) ? 0xFFFFu : 0u));
+  }
 
-  // Sum of the cluster's histograms in buffer b, two bins per thread, then the
-  // first bin whose running count (BY_MASS: mass) reaches `need`; the values
-  // before it and in it go to S.found_*.  Every CTA finds the same.
-  template <bool BY_MASS>
-  __device__ __forceinline__ void find_bin(cg::cluster_group& cl, int b, unsigned long long need) {
+  // Every logit of the slice, in no particular order.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+      const Vec<T> v = xs[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(v.get(e));
+    }
+  }
+  // Vectors [v0, v1) by one warp.
+  template <typename F>
+  __device__ __forceinline__ void each_of(int v0, int v1, F f) const {
+#pragma unroll 2
+    for (int i = v0 + (threadIdx.x & 31); i < v1; i += 32) {
+      const Vec<T> v = xs[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(v.get(e));
+    }
+  }
+
+  __device__ __forceinline__ void clear(int b, int arrays) {
+    for (int i = threadIdx.x; i < arrays * kBins; i += kThreads) S.hist[b][0][i] = 0;
+  }
+  __device__ __forceinline__ void add_mass(int b, int bin, unsigned long long wt) {
+    atomicAdd(&S.hist[b][0][bin], 1u);
+    if (const unsigned int v = (unsigned int)wt & 0xFFFFu) atomicAdd(&S.hist[b][1][bin], v);
+    if (const unsigned int v = (unsigned int)(wt >> 16) & 0xFFFFu) atomicAdd(&S.hist[b][2][bin], v);
+    if (const unsigned int v = (unsigned int)(wt >> 32)) atomicAdd(&S.hist[b][3][bin], v);
+  }
+
+  // First of the 1024 bins (two per thread, v of each and its count c) whose
+  // running sum reaches `need`; the sum before it and its count go to S.found_*.
+  template <typename V>
+  __device__ __forceinline__ void find(const V* v, const unsigned int* c, V need) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    V* part = reinterpret_cast<V*>(S.wm);
+    V inc = v[0] + v[1];
+    const V mine = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const V up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) part[w] = inc;
+    if (tid == 0) S.found_bin = kBins;  // none
+    __syncthreads();
+    V before = inc - mine;
+    for (int i = 0; i < w; ++i) before += part[i];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (before < need && before + v[e] >= need) {
+        S.found_bin = 2 * tid + e;
+        S.found_m = (unsigned long long)before;
+        S.found_n = c[e];
+      }
+      before += v[e];
+    }
+    __syncthreads();
+  }
+  // The cluster's histograms in buffer b, added up.
+  template <bool BY_MASS>
+  __device__ __forceinline__ void find_bin(int b, unsigned long long need) {
+    const int tid = threadIdx.x;
     unsigned int c[2] = {0, 0};
     unsigned long long v[2] = {0, 0};
     for (int i = 0; i < nc; ++i) {
       const Shared* o = cl.map_shared_rank(&S, i);
       const uint2 a = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]);
-      c[0] += a.x;
-      c[1] += a.y;
+      c[0] += a.x, c[1] += a.y;
       if constexpr (BY_MASS) {
         const uint2 l0 = *reinterpret_cast<const uint2*>(&o->hist[b][1][2 * tid]);
         const uint2 l1 = *reinterpret_cast<const uint2*>(&o->hist[b][2][2 * tid]);
@@ -212,126 +297,132 @@ struct Row {
       }
     }
     if constexpr (!BY_MASS) v[0] = c[0], v[1] = c[1];
-    unsigned long long s = v[0] + v[1], inc = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long up = shfl_up64(inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) S.wm[w] = inc;
-    __syncthreads();
-    unsigned long long before = inc - s;
-    for (int i = 0; i < w; ++i) before += S.wm[i];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (before < need && before + v[e] >= need) {
-        S.found_bin = 2 * tid + e;
-        S.found_m = before;
-        S.found_n = c[e];
-      }
-      before += v[e];
-    }
-    __syncthreads();
+    find<unsigned long long>(v, c, need);
   }
 
-  __device__ __forceinline__ void add(int b, int bin, unsigned long long wt, bool by_mass) {
-    atomicAdd(&S.hist[b][0][bin], 1u);
-    if (by_mass) {
-      if (const unsigned int v = (unsigned int)wt & 0xFFFFu) atomicAdd(&S.hist[b][1][bin], v);
-      if (const unsigned int v = (unsigned int)(wt >> 16) & 0xFFFFu) atomicAdd(&S.hist[b][2][bin], v);
-      if (const unsigned int v = (unsigned int)(wt >> 32)) atomicAdd(&S.hist[b][3][bin], v);
-    }
-  }
-  __device__ __forceinline__ void clear(int b, bool by_mass) {
-    for (int i = threadIdx.x; i < (by_mass ? 4 : 1) * kBins; i += kThreads) S.hist[b][0][i] = 0;
-  }
-
-  // The threshold of the tokens above `base` (an earlier threshold; its ties
-  // are not among them): by count the `need` largest, by mass the shortest
-  // prefix with mass >= need.  need must be reachable.
-  template <bool BY_MASS>
-  __device__ Keep search(cg::cluster_group& cl, unsigned int base, unsigned long long need, float step, const Weigher& wt) {
+  // The keys with coarse(value) == bin into S.lo, S.hi: coarse() falls as the key grows, so its bounds come
+  // by bisection (warp 0: the smallest key with coarse <= bin, warp 1: with coarse <= bin - 1).
+  template <typename F>
+  __device__ __forceinline__ void bin_keys(int bin, F coarse) {
     const int tid = threadIdx.x;
-    const float top = m;
-    auto coarse = [&](float x) { return min(kBins - 1, (int)((top - x) * step)); };
-    // 1024 equal steps below the maximum; the last one holds everything further down.
-    int b = buf;
-    clear(b, BY_MASS);
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = xs[i];
-      if (x == -INFINITY || key(x) <= base) continue;
-      unsigned long long w = 0;
-      if constexpr (BY_MASS) {
-        w = wt(x);
-        if (w == 0) continue;
-      }
-      add(b, coarse(x), w, BY_MASS);
-    }
-    cl.sync();
-    find_bin<BY_MASS>(cl, b, need);
-    buf ^= 1;
-    const int cb = (int)S.found_bin;
-    need -= S.found_m;
-    unsigned int cnt = S.found_n;
-    // The keys of that step: coarse() falls as the key grows, so its bounds come by bisection.
     if (tid < 64 && (tid & 31) == 0) {
-      // warp 0: smallest key with coarse <= cb; warp 1: smallest key with coarse <= cb - 1 (then minus 1).
-      const int want = cb - (tid >> 5);
-      unsigned int lo = order_bits(-3.402823466e38f) >> kDrop, hi = key(top) + 1;  // answer in [lo, hi]
+      const int want = bin - (tid >> 5);
+      unsigned int lo = key(-3.402823466e38f), hi = key(m) + 1;  // answer in [lo, hi]
       while (lo < hi) {
         const unsigned int mid = lo + ((hi - lo) >> 1);
-        if (coarse(from_order((mid << kDrop) | (kDrop && !(mid & 0x8000u) ? 0xFFFFu : 0u))) <= want) hi = mid;
+        if (coarse(value(mid)) <= want) hi = mid;
         else lo = mid + 1;
       }
       if (tid == 0) S.lo = lo;
       else S.hi = lo - 1;
     }
     __syncthreads();
-    unsigned int lo = max(S.lo, base + 1), hi = S.hi;
+  }
+
+  // Threshold inside the keys lo..hi, which hold cnt entries: by count the
+  // `need` largest stay, by mass the shortest prefix with mass >= need.
+  template <bool BY_MASS>
+  __device__ __forceinline__ Keep refine(unsigned int lo, unsigned int hi, unsigned int cnt, unsigned long long need, const Weigher& wt) {
     while (true) {
-      if (BY_MASS ? cnt == 1 : need == cnt) return Keep{lo - 1, 0};  // the whole bin stays
+      if (BY_MASS ? cnt == 1 : need == cnt) return Keep{lo - 1, 0};  // all of them stay
       if (lo == hi) break;
-      const unsigned int range = hi - lo;
-      const int shift = max(0, 32 - __clz(range) - 10);  // (range >> shift) < kBins
-      b = buf;
-      clear(b, BY_MASS);
+      const int shift = max(0, 32 - __clz(hi - lo) - 10);  // ((hi - lo) >> shift) < kBins
+      const int b = buf;
+      clear(b, BY_MASS ? 4 : 1);
       __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        const float x = xs[i];
-        if (x == -INFINITY) continue;
+      each([&](float x) {
         const unsigned int k = key(x);
-        if (k < lo || k > hi) continue;
-        unsigned long long w = 0;
+        if (k < lo || k > hi) return;  // -inf too
         if constexpr (BY_MASS) {
-          w = wt(x);
-          if (w == 0) continue;
+          if (const unsigned long long w = wt(x)) add_mass(b, (int)((hi - k) >> shift), w);
+        } else {
+          atomicAdd(&S.hist[b][0][(hi - k) >> shift], 1u);
         }
-        add(b, (int)((hi - k) >> shift), w, BY_MASS);
-      }
+      });
       cl.sync();
-      find_bin<BY_MASS>(cl, b, need);
+      find_bin<BY_MASS>(b, need);
       buf ^= 1;
       need -= S.found_m;
       cnt = S.found_n;
-      const unsigned int bin = S.found_bin;
-      const unsigned int nh = hi - (bin << shift), width = (1u << shift) - 1;
+      const unsigned int width = (1u << shift) - 1, nh = hi - (S.found_bin << shift);
       lo = nh - lo > width ? nh - width : lo;
       hi = nh;
       __syncthreads();  // S.found_* are read before the next step writes them
     }
     if constexpr (!BY_MASS) return Keep{lo, (unsigned int)need};
-    const unsigned long long each = wt(from_order((lo << kDrop) | (kDrop && !(lo & 0x8000u) ? 0xFFFFu : 0u)));
-    return Keep{lo, (unsigned int)((need + each - 1) / each)};
+    const unsigned long long each_w = wt(value(lo));
+    return Keep{lo, (unsigned int)((need + each_w - 1) / each_w)};
+  }
+
+  // The threshold of the `need` largest logits (there are more above -inf).
+  __device__ __forceinline__ Keep largest(unsigned int need, float span, const Weigher& wt) {
+    const float top = m, step = span > 0.f ? (float)kBins / span : 0.f;
+    auto coarse = [&](float x) { return min(kBins - 1, (int)((top - x) * step)); };
+    // The `need` largest of the threads' own maxima are as many logits, so the
+    // wanted ones lie no lower: a histogram of one value per thread rules out
+    // most of the row, and the next one meets few entries.
+    int bound = kBins - 1;
+    if (need <= (unsigned int)(nc * kThreads) / 2) {
+      const int b = buf;
+      clear(b, 1);
+      __syncthreads();
+      if (own_max > -INFINITY) atomicAdd(&S.hist[b][0][coarse(own_max)], 1u);
+      cl.sync();
+      find_bin<false>(b, need);
+      buf ^= 1;
+      bound = min(bound, (int)S.found_bin);
+    }
+    const int b = buf;
+    clear(b, 1);
+    __syncthreads();
+    each([&](float x) {
+      if (x == -INFINITY) return;
+      const int c = coarse(x);
+      if (c <= bound) atomicAdd(&S.hist[b][0][c], 1u);
+    });
+    cl.sync();
+    find_bin<false>(b, need);
+    buf ^= 1;
+    const int bin = (int)S.found_bin;
+    const unsigned long long rest = need - S.found_m;
+    const unsigned int cnt = S.found_n;
+    bin_keys(bin, coarse);
+    return refine<false>(S.lo, S.hi, cnt, rest, wt);
   }
 };
+
+// Sums that each CTA tells the others (the values of all warps, added up).
+__device__ __forceinline__ void tell(cg::cluster_group& cl, Shared& S, int rank, int nc, unsigned long long mass,
+                                     unsigned long long in, unsigned long long below, unsigned int ties,
+                                     unsigned int cnt) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    in += __shfl_xor_sync(0xffffffffu, in, o);
+    below += __shfl_xor_sync(0xffffffffu, below, o);
+  }
+  ties = __reduce_add_sync(0xffffffffu, ties);
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
+  __syncthreads();  // S.wm and its neighbours are free
+  if (lane == 0) S.wm[warp] = mass, S.wi[warp] = in, S.wb[warp] = below, S.wc[warp] = ties, S.wn[warp] = cnt;
+  __syncthreads();
+  if (tid < nc) {
+    Tail t = {};
+    for (int w = 0; w < kWarps; ++w) t.mass += S.wm[w], t.in += S.wi[w], t.below += S.wb[w], t.ties += S.wc[w], t.cnt += S.wn[w];
+    cl.map_shared_rank(&S, tid)->tail[rank] = t;
+  }
+  cl.sync();
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     k_sample(SampleRows a, int slice) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& S = *reinterpret_cast<Shared*>(raw);
-  float* xs = reinterpret_cast<float*>(raw + sizeof(Shared));
+  Vec<T>* xs = reinterpret_cast<Vec<T>*>(raw + sizeof(Shared));
+  using R_ = Row<T>;
+  constexpr int E = R_::E;
   cg::cluster_group cl = cg::this_cluster();
   const int nc = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int row = blockIdx.x / nc;
@@ -370,26 +461,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   // One read of the row: NaN counts as -inf, -0 as 0 (so that equal logits have equal keys).
   float mx = -INFINITY, mn = INFINITY;
   int fi = 0x7FFFFFFF;
-  auto take = [&](int i, float x) {
-    x = x != x ? -INFINITY : x + 0.f;
-    xs[i] = x;
-    if (x > mx) mx = x, fi = lo + i;
-    if (x > -INFINITY) mn = fminf(mn, x);
-  };
-  constexpr int E = Chunk<T>::N;
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    const int nv = n / E;
+  const int nv = (n + 32 * E - 1) / (32 * E) * 32;  // whole warps of vectors, the last ones filled up with -inf
+  const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
 #pragma unroll 4
-    for (int i = tid; i < nv; i += kThreads) {
-      float v[E];
-      Chunk<T>::load(src + (size_t)i * E, v);
+  for (int i = tid; i < nv; i += kThreads) {
+    Vec<T> v;
+    if (wide && (i + 1) * E <= n) {
+      v.v = *reinterpret_cast<const decltype(v.v)*>(src + (size_t)i * E);
+    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) take(i * E + e, v[e]);
+      for (int e = 0; e < E; ++e) v.set(e, i * E + e < n ? to_f(src[i * E + e]) : -INFINITY);
     }
-    for (int i = nv * E + tid; i < n; i += kThreads) take(i, to_f(src[i]));
-  } else {
-    for (int i = tid; i < n; i += kThreads) take(i, to_f(src[i]));
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float x = v.get(e);
+      x = x != x ? -INFINITY : x + 0.f;
+      v.set(e, x);
+      top = fmaxf(top, x);
+      if (x > -INFINITY) mn = fminf(mn, x);
+    }
+    if (top > mx) {
+      mx = top;
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (v.get(e) == top) fi = lo + i * E + e;
+    }
+    xs[i] = v;
   }
+  const float own_max = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float om = __shfl_xor_sync(0xffffffffu, mx, o);
@@ -398,7 +498,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   if (lane == 0) S.fmx[warp] = mx, S.fmn[warp] = mn, S.fi[warp] = fi;
-  if (tid == 0) S.token = -1;
   cl.barrier_wait();
   __syncthreads();
   if (tid < nc) {  // thread i tells CTA i
@@ -423,118 +522,154 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     return;
   }
+  R_ R{S, cl, xs, nv, rank, nc};
+  R.own_max = own_max;
   if (mx == INFINITY) {  // the +inf entries share the mass
-    for (int i = tid; i < n; i += kThreads) xs[i] = xs[i] == INFINITY ? 0.f : -INFINITY;
+    for (int i = tid; i < nv; i += kThreads) {
+      Vec<T> v = xs[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v.set(e, v.get(e) == INFINITY ? 0.f : -INFINITY);
+      xs[i] = v;
+    }
+    R.own_max = own_max == INFINITY ? 0.f : -INFINITY;
     mx = mn = 0.f;
     __syncthreads();
   }
+  R.m = mx;
   // 1 / T in two parts.
-  const float Tc = fmaxf(T_, 1.17549435e-38f);
+  const float Tc = fminf(fmaxf(T_, 0x1p-126f), 0x1p126f);
   Weigher wt;
   wt.m = mx;
   wt.ch = __frcp_rn(Tc);
   wt.cl = __fmaf_rn(-Tc, wt.ch, 1.f) * wt.ch;
   wt.tab = S.tab;
   wt.tab30 = S.tab30;
-  Row<T> R{S, xs, n, rank, nc};
-  R.m = mx;
+  unsigned long long floor_w = 1;  // smallest weight that stays
+  if (mp > 0.f) floor_w = mp >= 1.f ? 1ull << kUnit : mul_ceil(mp, 1ull << kUnit);
+  // Logits at or below `cut` weigh nothing, or less than min_p allows: a
+  // comparison instead of a weight (with a margin for its own rounding).
+  float cut = mx - 31.75f * Tc;
+  if (mp > 0.f) cut = fmaxf(cut, mx + (mp < 1.f ? logf(mp) * 1.0001f - 1e-4f : -1e-4f) * Tc);
+  cut -= 1e-6f * fabsf(mx);
 
   Keep keep{0, 0};
   if (tk > 0 && tk < a.vocab) {
-    // Fewer than top_k tokens above -inf: all stay.
-    unsigned int have = 0;
-    for (int i = tid; i < n; i += kThreads) have += xs[i] != -INFINITY;
-    have = __reduce_add_sync(0xffffffffu, have);
-    if (lane == 0) S.wc[warp] = have;
-    __syncthreads();
-    if (tid < nc) {
-      unsigned int s = 0;
-      for (int w = 0; w < kWarps; ++w) s += S.wc[w];
-      cl.map_shared_rank(&S, tid)->tail[rank].ties = s;
-    }
-    cl.sync();
+    unsigned int have = 0;  // fewer than top_k tokens above -inf: all stay
+    R.each([&](float x) { have += x != -INFINITY; });
+    tell(cl, S, rank, nc, 0, 0, 0, have, 0);
     unsigned int all = 0;
     for (int i = 0; i < nc; ++i) all += S.tail[i].ties;
-    const float span = mx - mn;
-    if ((unsigned int)tk < all)
-      keep = R.template search<false>(cl, 0u, (unsigned long long)tk, span > 0.f ? (float)kBins / span : 0.f, wt);
-    else
-      cl.sync();  // S.tail is free for the sums below
+    cl.sync();  // S.tail is free for the sums below
+    if ((unsigned int)tk < all) keep = R.largest((unsigned int)tk, mx - mn, wt);
   }
-  // Mass of what is above the threshold, and of its kept ties.
-  const unsigned int drop_fill = (Row<T>::kDrop && !(keep.t & 0x8000u)) ? 0xFFFFu : 0u;
-  unsigned long long tie_w = keep.r ? wt(from_order((keep.t << Row<T>::kDrop) | drop_fill)) : 0ull;
+  // This warp's segment of the slice: the sums below go by it.
+  const int seg = (nv / 32 + kWarps - 1) / kWarps * 32;
+  const int s0 = min(nv, warp * seg), s1 = min(nv, s0 + seg);
+  unsigned long long tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
+  unsigned long long sum = 0;             // this lane's kept mass above keys `counted`
+  unsigned int counted = 0xFFFFFFFFu;     // keys above it are in `sum` already
   if (tp < 1.f) {
-    unsigned long long s = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = xs[i];
-      if (x > -INFINITY && R.key(x) > keep.t) s += wt(x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) S.wm[warp] = s;
+    // A first guess of the bin, 1024 equal steps of the logits that have mass,
+    // from sums of fp32 weights; then the exact mass above it, in it and below
+    // decides (and moves the bin, should the guess be off).
+    const float step = (float)kBins / 31.5f * wt.ch;
+    auto coarse = [&](float x) { return min(kBins - 1, (int)((mx - x) * step)); };
+    const float c2 = wt.ch * 1.4426950408889634f, zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);
+    const int b = R.buf;
+    float* fh = reinterpret_cast<float*>(S.hist[b][0]);
+    R.clear(b, 1);
     __syncthreads();
-    if (tid < nc) {
-      s = 0;
-      for (int w = 0; w < kWarps; ++w) s += S.wm[w];
-      cl.map_shared_rank(&S, tid)->tail[rank].mass = s;
-    }
+    R.each([&](float x) {
+      if (x > zero && R.key(x) > keep.t) atomicAdd(&fh[coarse(x)], exp2f((x - mx) * c2));
+    });
     cl.sync();
-    unsigned long long above = 0;
-    for (int i = 0; i < nc; ++i) above += S.tail[i].mass;
-    unsigned long long need = mul_ceil(tp, above + tie_w * keep.r);
-    if (need == 0) need = 1;
-    cl.sync();  // every CTA has read S.tail
-    if (need <= above)
-      keep = R.template search<true>(cl, keep.t, need, (float)kBins / 31.5f * wt.ch, wt);
-    else
-      keep.r = min(keep.r, (unsigned int)((need - above + tie_w - 1) / tie_w));
-    const unsigned int fill = (Row<T>::kDrop && !(keep.t & 0x8000u)) ? 0xFFFFu : 0u;
-    tie_w = keep.r ? wt(from_order((keep.t << Row<T>::kDrop) | fill)) : 0ull;
+    float fv[2] = {0.f, 0.f};
+    for (int i = 0; i < nc; ++i) {
+      const float2 o = *reinterpret_cast<const float2*>(&cl.map_shared_rank(&S, i)->hist[b][0][2 * tid]);
+      fv[0] += o.x, fv[1] += o.y;
+    }
+    R.buf ^= 1;
+    float ft = fv[0] + fv[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ft += __shfl_xor_sync(0xffffffffu, ft, o);
+    if (lane == 0) S.fmx[warp] = ft;
+    __syncthreads();
+    ft = 0.f;
+    for (int w = 0; w < kWarps; ++w) ft += S.fmx[w];
+    const unsigned int none[2] = {0, 0};
+    const float with_ties = ft + (float)tie_w * 0x1p-44f * (float)keep.r;
+    R.template find<float>(fv, none, fmaxf(fminf(tp * with_ties, 0.999998f * ft), 1e-30f));
+    int bin = min((int)S.found_bin, kBins - 1);
+    while (true) {
+      unsigned long long above = 0, in = 0, below = 0;
+      unsigned int cnt = 0;
+      R.each_of(s0, s1, [&](float x) {
+        if (!(x > zero) || R.key(x) <= keep.t) return;
+        const unsigned long long w = wt(x);
+        const int c = coarse(x);
+        above += c < bin ? w : 0ull;
+        in += c == bin ? w : 0ull;
+        below += c > bin ? w : 0ull;
+        cnt += c == bin && w != 0;
+      });
+      tell(cl, S, rank, nc, above, in, below, 0, cnt);
+      unsigned long long A = 0, B = 0, C = 0;
+      cnt = 0;
+      for (int i = 0; i < nc; ++i) A += S.tail[i].mass, B += S.tail[i].in, C += S.tail[i].below, cnt += S.tail[i].cnt;
+      cl.sync();
+      unsigned long long need = mul_ceil(tp, A + B + C + tie_w * keep.r);
+      if (need == 0) need = 1;
+      if (need > A + B + C) {  // into the ties of top_k
+        keep.r = min(keep.r, (unsigned int)((need - (A + B + C) + tie_w - 1) / tie_w));
+        sum = above + in + below;
+        counted = keep.t;
+        break;
+      }
+      if (need > A && need <= A + B) {
+        R.bin_keys(bin, coarse);
+        const unsigned int hi = S.hi;
+        keep = R.template refine<true>(max(S.lo, keep.t + 1), hi, cnt, need - A, wt);
+        sum = above;
+        counted = hi;
+        break;
+      }
+      // Off (a border within the guess's rounding): the bin from exact masses.
+      const int h = R.buf;
+      R.clear(h, 4);
+      __syncthreads();
+      R.each([&](float x) {
+        if (!(x > zero) || R.key(x) <= keep.t) return;
+        if (const unsigned long long w = wt(x)) R.add_mass(h, coarse(x), w);
+      });
+      cl.sync();
+      R.template find_bin<true>(h, need);
+      R.buf ^= 1;
+      bin = min((int)S.found_bin, kBins - 1);
+    }
+    tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   }
-  unsigned long long floor_w = 1;  // smallest weight that stays
   if (mp > 0.f) {
-    floor_w = mp >= 1.f ? 1ull << kUnit : mul_ceil(mp, 1ull << kUnit);
+    sum = 0, counted = 0xFFFFFFFFu;  // some of it may fall below the floor
     if (tie_w < floor_w) keep.r = 0;
   }
-
   // With u = 0 the first kept token wins however small its mass: weights that
   // the fixed-point unit rounds to none count as one unit there.
   const bool zero_u = !(u > 0.f) && floor_w == 1;
+  if (zero_u) sum = 0, counted = 0xFFFFFFFFu, cut = -INFINITY;
   auto kept_weight = [&](float x) {
     const unsigned long long w = wt(x);
     if (w >= floor_w) return w;
     return zero_u && (x - mx) * wt.ch > -700.f ? 1ull : 0ull;
   };
 
-  // Kept mass of each warp's segment of the slice, in index order.
-  const int seg = ((n + kWarps * 32 - 1) / (kWarps * 32)) * 32;
-  const int s0 = min(n, warp * seg), s1 = min(n, s0 + seg);
-  unsigned long long sum = 0;
+  // Kept mass of each warp's segment, in index order from warp to warp.
   unsigned int ties = 0;
-  for (int i = s0 + lane; i < s1; i += 32) {
-    const float x = xs[i];
-    if (x == -INFINITY) continue;
+  R.each_of(s0, s1, [&](float x) {
     const unsigned int k = R.key(x);
-    if (k > keep.t) {
-      sum += kept_weight(x);
-    } else if (k == keep.t) {
-      ++ties;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  ties = __reduce_add_sync(0xffffffffu, ties);
-  __syncthreads();
-  if (lane == 0) S.wm[warp] = sum, S.wc[warp] = ties;
-  __syncthreads();
-  if (tid < nc) {
-    unsigned long long s = 0;
-    unsigned int t = 0;
-    for (int w = 0; w < kWarps; ++w) s += S.wm[w], t += S.wc[w];
-    cl.map_shared_rank(&S, tid)->tail[rank] = Tail{s, t, 0};
-  }
-  cl.sync();
+    if (k == keep.t) ++ties;
+    if (x > cut && k > keep.t && k <= counted) sum += kept_weight(x);
+  });
+  tell(cl, S, rank, nc, sum, 0, 0, ties, 0);
   // Ties and mass before this CTA and in total; a CTA's ties count while fewer than keep.r came before.
   unsigned long long total = 0, mine0 = 0;
   unsigned int tied = 0, mytied0 = 0;
@@ -559,23 +694,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     tb += S.wc[w];
   }
   if (hit >= 0) {  // uniform in this CTA; no other CTA of the cluster has it
-    // The segment again, cut into one run of 32-entry chunks per warp.
+    // The segment again, cut into one run of vectors per warp.
     __syncthreads();  // S.wm and S.wc are read
-    const int g0 = min(n, hit * seg), g1 = min(n, g0 + seg);
-    const int sub = ((g1 - g0 + kWarps * 32 - 1) / (kWarps * 32)) * 32;
+    const int g0 = min(nv, hit * seg), g1 = min(nv, g0 + seg);
+    const int sub = (g1 - g0 + kWarps - 1) / kWarps;
     const int a0 = min(g1, g0 + warp * sub), a1 = min(g1, a0 + sub);
     unsigned long long s = 0;
     unsigned int tt = 0;
-    for (int i = a0 + lane; i < a1; i += 32) {
-      const float x = xs[i];
-      if (x == -INFINITY) continue;
+    R.each_of(a0, a1, [&](float x) {
       const unsigned int k = R.key(x);
-      if (k > keep.t) {
-        s += kept_weight(x);
-      } else if (k == keep.t) {
-        ++tt;
-      }
-    }
+      if (k == keep.t) ++tt;
+      if (x > cut && k > keep.t) s += kept_weight(x);
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     tt = __reduce_add_sync(0xffffffffu, tt);
@@ -587,22 +717,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const unsigned long long end = before + S.wm[warp] + tie_w * min(S.wc[warp], keep.r - min(keep.r, tb));
     if (before <= goal && goal < end) {
-      for (int i0 = a0; i0 < a1; i0 += 32) {  // in index order, 32 entries at a time
+      for (int i0 = a0 * E; i0 < a1 * E; i0 += 32) {  // in index order, 32 entries at a time
         const int i = i0 + lane;
-        const float x = i < a1 ? xs[i] : -INFINITY;
-        const unsigned int k = x > -INFINITY ? R.key(x) : 0u;
-        const bool tie = x > -INFINITY && k == keep.t;
+        const float x = i < a1 * E ? xs[i / E].get(i % E) : -INFINITY;
+        const unsigned int k = R.key(x);
+        const bool tie = k == keep.t;
         const unsigned int tm = __ballot_sync(0xffffffffu, tie);
         unsigned long long w = 0;
         if (tie) {
           if (tb + __popc(tm & ((1u << lane) - 1u)) < keep.r) w = tie_w;
-        } else if (x > -INFINITY && k > keep.t) {
+        } else if (x > cut && k > keep.t) {
           w = kept_weight(x);
         }
         unsigned long long inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long up = shfl_up64(inc, o);
+          const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= o) inc += up;
         }
         const unsigned int past = __ballot_sync(0xffffffffu, before + inc > goal);
@@ -628,11 +758,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 }  // namespace smp
 
 // Cluster size: CTAs hold their slice beside 34 KB of tables, two CTAs per SM
-// up to a 64 KB slice; small batches spread a row over more CTAs as long as
+// up to a slice of 72 KB; small batches spread a row over more CTAs as long as
 // all of them are resident at once.  The result does not depend on it.
 template <typename T>
 static cudaError_t sample_t(cudaStream_t s, const SampleRows& a) {
-  constexpr int kTwoPerSm = 16384, kMost = 45056;  // slice entries for two CTAs per SM, for one
+  constexpr int kTwoPerSm = 72 * 1024 / sizeof(T), kStep = 32 * 16 / sizeof(T);  // entries of such a slice; of a warp's vectors
+  constexpr int kMost = 176 * 1024;  // bytes of the largest slice
   static int sms[kMaxDevices] = {};
   const int dev = current_device();
   if (!sms[dev]) {
@@ -640,18 +771,18 @@ static cudaError_t sample_t(cudaStream_t s, const SampleRows& a) {
     cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(smp::k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(smp::Shared) + (size_t)kMost * 4));
+                             (int)(sizeof(smp::Shared) + kMost));
     if (e != cudaSuccess) return e;
     sms[dev] = n;
   }
   int nc = 1;
   while (nc < smp::kMaxCluster && a.vocab > nc * kTwoPerSm) nc *= 2;
   while (nc < smp::kMaxCluster && (long long)a.rows * nc * 2 <= 2ll * sms[dev] && a.vocab >= 2 * nc * 2048) nc *= 2;
-  const int slice = (((a.vocab + nc - 1) / nc) + 31) / 32 * 32;
+  const int slice = (((a.vocab + nc - 1) / nc) + kStep - 1) / kStep * kStep;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * nc);
   cfg.blockDim = dim3(smp::kThreads);
-  cfg.dynamicSmemBytes = sizeof(smp::Shared) + (size_t)slice * 4;
+  cfg.dynamicSmemBytes = sizeof(smp::Shared) + (size_t)slice * sizeof(T);
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
