@@ -19,7 +19,7 @@
 // works on its slice in its own shared memory, all CTAs of the cluster then
 // read one another's histograms or sums (distributed shared memory) and come to
 // the same decision; two histogram buffers leave one cluster barrier per step.
-// What bounds it: the instructions of the weights (about 45 for each logit that
+// What bounds it: the instructions of the weights (about 50 for each logit that
 // has mass) and, with few rows, the barriers.
 #include <cooperative_groups.h>
 
@@ -41,31 +41,31 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;       // two per thread
 constexpr int kMaxCluster = 8;
 constexpr int kUnit = 44;         // fixed-point weights: 2^kUnit is weight 1
-constexpr int kTab = 64;          // 2^(j/64), j = 0..63
+constexpr int kTab = 64;          // 2^(-j/64), j = 0..63
 
-// 2^(j/64) in units of 2^-44, rounded.
+// 2^(-j/64) in units of 2^-44, rounded.
 __constant__ unsigned long long kExp2[kTab] = {
-    17592186044416ull, 17783752390528ull, 17977404757381ull, 18173165860252ull,
-    18371058661769ull, 18571106374610ull, 18773332464219ull, 18977760651566ull,
-    19184414915921ull, 19393319497675ull, 19604498901178ull, 19817977897613ull,
-    20033781527906ull, 20251935105661ull, 20472464220127ull, 20695394739203ull,
-    20920752812471ull, 21148564874263ull, 21378857646762ull, 21611658143136ull,
-    21846993670708ull, 22084891834158ull, 22325380538761ull, 22568487993661ull,
-    22814242715178ull, 23062673530157ull, 23313809579344ull, 23567680320808ull,
-    23824315533396ull, 24083745320225ull, 24346000112214ull, 24611110671650ull,
-    24879108095804ull, 25150023820570ull, 25423889624159ull, 25700737630824ull,
-    25980600314626ull, 26263510503246ull, 26549501381838ull, 26838606496915ull,
-    27130859760289ull, 27426295453047ull, 27724948229574ull, 28026853121614ull,
-    28332045542385ull, 28640561290725ull, 28952436555301ull, 29267707918846ull,
-    29586412362452ull, 29908587269910ull, 30234270432094ull, 30563500051394ull,
-    30896314746195ull, 31232753555409ull, 31572855943056ull, 31916661802889ull,
-    32264211463077ull, 32615545690931ull, 32970705697691ull, 33329733143360ull,
-    33692670141585ull, 34059559264602ull, 34430443548229ull, 34805366496913ull,
+    17592186044416ull, 17402683248456ull, 17215221774115ull, 17029779632301ull,
+    16846335070792ull, 16664866571680ull, 16485352848846ull, 16307772845465ull,
+    16132105731538ull, 15958330901445ull, 15786427971528ull, 15616376777705ull,
+    15448157373097ull, 15281750025697ull, 15117135216047ull, 14954293634955ull,
+    14793206181226ull, 14633853959423ull, 14476218277651ull, 14320280645363ull,
+    14166022771192ull, 14013426560807ull, 13862474114787ull, 13713147726524ull,
+    13565429880144ull, 13419303248457ull, 13274750690919ull, 13131755251623ull,
+    12990300157313ull, 12850368815412ull, 12711944812080ull, 12575011910285ull,
+    12439554047902ull, 12305555335825ull, 12173000056107ull, 12041872660113ull,
+    11912157766698ull, 11783840160404ull, 11656904789672ull, 11531336765078ull,
+    11407121357589ull, 11284243996830ull, 11162690269381ull, 11042445917079ull,
+    10923496835354ull, 10805829071568ull, 10689428823381ull, 10574282437131ull,
+    10460376406236ull, 10347697369602ull, 10236232110063ull, 10125967552830ull,
+    10016890763953ull, 9908988948806ull, 9802249450589ull, 9696659748838ull,
+    9592207457961ull, 9488880325783ull, 9386666232110ull, 9285553187305ull,
+    9185529330885ull, 9086582930126ull, 8988702378691ull, 8891876195264ull,
 };
 
 // What each CTA tells the others (one record per CTA, written remotely).
 struct Note {
-  float mx, mn;  // largest logit, smallest above -inf
+  float mx, mn;  // largest logit, smallest above -inf of the threads' largest
   int first;     // lowest index of mx
   int pad;
 };
@@ -76,8 +76,7 @@ struct Tail {
 
 struct alignas(16) Shared {
   unsigned int hist[2][4][kBins];  // count, then the low, middle and high 16 bits of the masses
-  uint2 tab[kTab];                 // 2^(j/64) * 2^44 (low, high words)
-  int tab30[kTab];                 // 2^(j/64) * 2^30
+  uint4 tab[kTab];                 // 2^(-j/64): in units of 2^-44 (low, high word), in units of 2^-30
   Note note[kMaxCluster];
   Tail tail[kMaxCluster];
   unsigned long long wm[kWarps], wi[kWarps], wb[kWarps];  // per-warp values of the scans and sums
@@ -98,46 +97,43 @@ __device__ __forceinline__ float from_order(unsigned int k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// exp((x - m) c) 2^kUnit as an integer, c = ch + cl = 1 / T.  d = x - m as an
-// exact sum of two floats (Knuth's two-sum), y = d c to about 2^-46 of its
-// value; y = t ln2/64 + r with t an integer (Cody and Waite's two-part
-// constant) and |r| < 0.0055; exp(r) - 1 = r + r^2/2 + r^3/6 + r^4/24 (the next
-// term is below 2^-44) in units of 2^-36, times 2^(j/64) from the table,
-// shifted by the integer part.  About 45 fp32 and integer instructions: fp64
-// ones run at 1/64 of the fp32 rate here.
+// exp((x - m) c) 2^kUnit as an integer, c = ch + cl = 1 / T, x <= m.  d = x - m
+// as an exact sum of two floats (Knuth's two-sum), y = d c = p + pl to about
+// 2^-46 of its value; y = r - t ln2/64 with t an integer and |r| < 0.0055
+// (Cody and Waite's constants: t C1 and t C2 are exact products).  exp(r) - 1 =
+// r + r^2/2 + r^3/6 + r^4/24 (the next term is below 2^-44) is an integer in
+// units of 2^-38; times 2^(-j/64) from the table, shifted by the integer part.
+// 45 fp32 and integer instructions: fp64 ones run at 1/64 of the fp32 rate.
 struct Weigher {
   float m, ch, cl;
-  const uint2* tab;
-  const int* tab30;
+  const uint4* tab;
   __device__ __forceinline__ unsigned long long operator()(float x) const {
     const float d = __fsub_rn(x, m);
-    if (d == 0.f) return 1ull << kUnit;
     const float db = __fsub_rn(d, x);
     const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(d, db)), __fsub_rn(-m, db));
     const float p = __fmul_rn(d, ch);
-    if (!(p > -31.5f)) return 0;
-    const float pl = __fmaf_rn(d, ch, -p) + __fmaf_rn(d, cl, dl * ch);
-    constexpr float kMagic = 12582912.f;                   // 1.5 * 2^23: the sum's low bits are the rounded integer
-    constexpr float kInv = 92.332482616893657f;            // 64 / ln 2
-    constexpr float kC1 = 2839.f / 262144.f;               // ln2/64 to 12 bits: t C1 is exact (|t| < 2^12)
-    constexpr float kC2 = 4.9915913977005e-07f;            // ln2/64 - kC1
-    const float tm = __fmaf_rn(p, kInv, kMagic);
-    const int t = __float_as_int(tm) - 0x4B400000;
+    const float pl = __fmaf_rn(dl, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, -p)));
+    constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: the sum's low bits are the rounded integer
+    constexpr float kInv = 92.332482616893657f;  // 64 / ln 2
+    constexpr float kC1 = 2839.f / 262144.f;     // ln2/64 = C1 + C2 + C3: 12 bits, 12 bits, the rest
+    constexpr float kC2 = 2144.f / 4294967296.f;
+    constexpr float kC3 = -2.9760223437e-11f;
+    constexpr float k37 = 137438953472.f, k38 = 2.f * k37;  // 2^37, 2^38
+    const float tm = __fmaf_rn(p, -kInv, kMagic);
+    const unsigned int t = __float_as_uint(tm) - 0x4B400000u;
     const float tf = __fsub_rn(tm, kMagic);
-    const float r1 = __fmaf_rn(-tf, kC1, p);               // exact
-    const float u2 = __fmul_rn(tf, kC2);
-    const float rh = __fsub_rn(r1, u2);
-    const float rb = __fsub_rn(rh, r1);
-    const float re = __fadd_rn(__fsub_rn(r1, __fsub_rn(rh, rb)), __fsub_rn(-u2, rb));
-    const float rl = re - __fmaf_rn(tf, kC2, -u2) + pl;    // r = rh + rl
-    const float q = rh * rh * (0.5f + rh * (0.16666667f + rh * 0.041666668f));
-    constexpr float k36 = 68719476736.f;                   // 2^36
-    const int is = __float2int_rn(rh * k36) + (__float_as_int(__fmaf_rn(rl + rh * rl + q, k36, kMagic)) - 0x4B400000);
-    const int j = t & (kTab - 1), n = -(t >> 6);
-    const uint2 tv = tab[j];
-    // 2^30 * 2^36 units to 2^-44 units: a shift by 22.
-    const long long w = (long long)(((unsigned long long)tv.y << 32) | tv.x) + (((long long)tab30[j] * is) >> 22);
-    return n > 45 ? 0ull : (unsigned long long)w >> n;
+    const float r1 = __fmaf_rn(tf, kC1, p);      // exact
+    const float rr = __fmaf_rn(tf, kC2, r1);
+    const float low = __fmaf_rn(tf, kC3, pl);
+    const float q = rr * rr * __fmaf_rn(rr, __fmaf_rn(rr, 0.041666668f, 0.16666667f), 0.5f);
+    const float s = __fmaf_rn(rr, low, low) + q;
+    const int is = __float2int_rn(r1 * k38) + __float2int_rn(tf * (kC2 * k38)) +
+                   2 * (__float_as_int(__fmaf_rn(s, k37, kMagic)) - 0x4B400000);
+    const uint4 e = tab[t & (kTab - 1)];
+    // 2^30 * 2^38 / 2^32 = 2^36 units, times 2^8.
+    const unsigned long long w = (unsigned long long)((long long)__mulhi((int)e.z, is) * 256 +
+                                                      (long long)(((unsigned long long)e.y << 32) | e.x));
+    return p > -31.5f ? w >> (t >> 6) : 0ull;
   }
 };
 
@@ -185,6 +181,13 @@ struct Vec<float> {
   float4 v;
   __device__ __forceinline__ float get(int i) const { return reinterpret_cast<const float*>(&v)[i]; }
   __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<float*>(&v)[i] = x; }
+  // NaN to -inf, -0 to 0; the largest.
+  __device__ __forceinline__ float clean() {
+    float* x = reinterpret_cast<float*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], -INFINITY) + 0.f;
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
 };
 template <>
 struct Vec<__nv_bfloat16> {
@@ -197,6 +200,14 @@ struct Vec<__nv_bfloat16> {
   __device__ __forceinline__ void set(int i, float x) {
     unsigned int& w = reinterpret_cast<unsigned int*>(&v)[i >> 1];
     w = (i & 1) ? (w & 0xFFFFu) | __float_as_uint(x) : (w & 0xFFFF0000u) | (__float_as_uint(x) >> 16);
+  }
+  __device__ __forceinline__ float clean() {
+    __nv_bfloat162* x = reinterpret_cast<__nv_bfloat162*>(&v);
+    const __nv_bfloat162 low = __floats2bfloat162_rn(-INFINITY, -INFINITY), zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __hadd2(__hmax2(x[i], low), zero);
+    const __nv_bfloat162 t = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
+    return fmaxf(__low2float(t), __high2float(t));
   }
 };
 
@@ -330,13 +341,14 @@ struct Row {
       const int b = buf;
       clear(b, BY_MASS ? 4 : 1);
       __syncthreads();
+      const float xlo = value(lo), xhi = value(hi);
       each([&](float x) {
-        const unsigned int k = key(x);
-        if (k < lo || k > hi) return;  // -inf too
+        if (x < xlo || x > xhi) return;
+        const int bin = (int)((hi - key(x)) >> shift);
         if constexpr (BY_MASS) {
-          if (const unsigned long long w = wt(x)) add_mass(b, (int)((hi - k) >> shift), w);
+          if (const unsigned long long w = wt(x)) add_mass(b, bin, w);
         } else {
-          atomicAdd(&S.hist[b][0][(hi - k) >> shift], 1u);
+          atomicAdd(&S.hist[b][0][bin], 1u);
         }
       });
       cl.sync();
@@ -354,15 +366,17 @@ struct Row {
     return Keep{lo, (unsigned int)((need + each_w - 1) / each_w)};
   }
 
-  // The threshold of the `need` largest logits (there are more above -inf).
-  __device__ __forceinline__ Keep largest(unsigned int need, float span, const Weigher& wt) {
-    const float top = m, step = span > 0.f ? (float)kBins / span : 0.f;
-    auto coarse = [&](float x) { return min(kBins - 1, (int)((top - x) * step)); };
+  // The threshold of the `need` largest logits; all of them, where there are no more above -inf.
+  __device__ __forceinline__ Keep largest(unsigned int need, float lowest_own, const Weigher& wt) {
+    const float top = m;
     // The `need` largest of the threads' own maxima are as many logits, so the
     // wanted ones lie no lower: a histogram of one value per thread rules out
     // most of the row, and the next one meets few entries.
-    int bound = kBins - 1;
+    float step = 0.f, least = -INFINITY;
+    int bound = kBins;
+    auto coarse = [&](float x) { return min(kBins - 1, (int)((top - x) * step)); };
     if (need <= (unsigned int)(nc * kThreads) / 2) {
+      step = (float)kBins / (top - lowest_own);  // infinite where all are equal: the maximum in bin 0, the rest in the last
       const int b = buf;
       clear(b, 1);
       __syncthreads();
@@ -370,13 +384,44 @@ struct Row {
       cl.sync();
       find_bin<false>(b, need);
       buf ^= 1;
-      bound = min(bound, (int)S.found_bin);
+      bound = (int)S.found_bin;
+      if (bound < kBins - 1) least = top - (float)(bound + 1) * (top - lowest_own) * (1.00001f / kBins) - 1e-6f * fabsf(top);
+    }
+    if (bound == kBins) {  // more are wanted: the range and the number of all logits
+      float mn = INFINITY;
+      unsigned int have = 0;
+      each([&](float x) {
+        if (x == -INFINITY) return;
+        mn = fminf(mn, x);
+        ++have;
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      have = __reduce_add_sync(0xffffffffu, have);
+      const int tid = threadIdx.x;
+      __syncthreads();
+      if ((tid & 31) == 0) S.fmn[tid >> 5] = mn, S.wc[tid >> 5] = have;
+      __syncthreads();
+      if (tid < nc) {
+        have = 0;
+        for (int w = 0; w < kWarps; ++w) mn = fminf(mn, S.fmn[w]), have += S.wc[w];
+        Shared* o = cl.map_shared_rank(&S, tid);
+        o->tail[rank].ties = have;
+        o->note[rank].mn = mn;
+      }
+      cl.sync();
+      have = 0;
+      for (int i = 0; i < nc; ++i) mn = fminf(mn, S.note[i].mn), have += S.tail[i].ties;
+      cl.sync();  // S.tail is free again
+      if (need >= have) return Keep{0, 0};
+      step = top > mn ? (float)kBins / (top - mn) : 0.f;
+      bound = kBins - 1;
     }
     const int b = buf;
     clear(b, 1);
     __syncthreads();
     each([&](float x) {
-      if (x == -INFINITY) return;
+      if (x == -INFINITY || x < least) return;
       const int c = coarse(x);
       if (c <= bound) atomicAdd(&S.hist[b][0][c], 1u);
     });
@@ -430,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   cl.barrier_arrive();  // waited for before the first access to another CTA's shared memory
   if (tid < kTab) {
     const unsigned long long f = kExp2[tid];
-    S.tab[tid] = make_uint2((unsigned int)f, (unsigned int)(f >> 32));
-    S.tab30[tid] = (int)((f + (1u << 13)) >> 14);
+    S.tab[tid] = make_uint4((unsigned int)f, (unsigned int)(f >> 32), (unsigned int)((f + (1u << 13)) >> 14), 0u);
   }
   pdl_wait();
   pdl_trigger();
@@ -459,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const T* src = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.ld + lo;
 
   // One read of the row: NaN counts as -inf, -0 as 0 (so that equal logits have equal keys).
-  float mx = -INFINITY, mn = INFINITY;
+  float mx = -INFINITY;
   int fi = 0x7FFFFFFF;
   const int nv = (n + 32 * E - 1) / (32 * E) * 32;  // whole warps of vectors, the last ones filled up with -inf
   const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
@@ -472,15 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int e = 0; e < E; ++e) v.set(e, i * E + e < n ? to_f(src[i * E + e]) : -INFINITY);
     }
-    float top = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float x = v.get(e);
-      x = x != x ? -INFINITY : x + 0.f;
-      v.set(e, x);
-      top = fmaxf(top, x);
-      if (x > -INFINITY) mn = fminf(mn, x);
-    }
+    const float top = v.clean();
     if (top > mx) {
       mx = top;
 #pragma unroll
@@ -489,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     xs[i] = v;
   }
+  float mn = mx > -INFINITY ? mx : INFINITY;
   const float own_max = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -543,7 +580,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   wt.ch = __frcp_rn(Tc);
   wt.cl = __fmaf_rn(-Tc, wt.ch, 1.f) * wt.ch;
   wt.tab = S.tab;
-  wt.tab30 = S.tab30;
   unsigned long long floor_w = 1;  // smallest weight that stays
   if (mp > 0.f) floor_w = mp >= 1.f ? 1ull << kUnit : mul_ceil(mp, 1ull << kUnit);
   // Logits at or below `cut` weigh nothing, or less than min_p allows: a
@@ -553,21 +589,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   cut -= 1e-6f * fabsf(mx);
 
   Keep keep{0, 0};
-  if (tk > 0 && tk < a.vocab) {
-    unsigned int have = 0;  // fewer than top_k tokens above -inf: all stay
-    R.each([&](float x) { have += x != -INFINITY; });
-    tell(cl, S, rank, nc, 0, 0, 0, have, 0);
-    unsigned int all = 0;
-    for (int i = 0; i < nc; ++i) all += S.tail[i].ties;
-    cl.sync();  // S.tail is free for the sums below
-    if ((unsigned int)tk < all) keep = R.largest((unsigned int)tk, mx - mn, wt);
-  }
+  if (tk > 0 && tk < a.vocab) keep = R.largest((unsigned int)tk, mn, wt);
   // This warp's segment of the slice: the sums below go by it.
   const int seg = (nv / 32 + kWarps - 1) / kWarps * 32;
   const int s0 = min(nv, warp * seg), s1 = min(nv, s0 + seg);
   unsigned long long tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   unsigned long long sum = 0;             // this lane's kept mass above keys `counted`
-  unsigned int counted = 0xFFFFFFFFu;     // keys above it are in `sum` already
+  float counted = INFINITY;               // logits above it are in `sum` already
   if (tp < 1.f) {
     // A first guess of the bin, 1024 equal steps of the logits that have mass,
     // from sums of fp32 weights; then the exact mass above it, in it and below
@@ -575,12 +603,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float step = (float)kBins / 31.5f * wt.ch;
     auto coarse = [&](float x) { return min(kBins - 1, (int)((mx - x) * step)); };
     const float c2 = wt.ch * 1.4426950408889634f, zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);
+    const float least = fmaxf(zero, R.value(keep.t));  // above it is what top_k keeps whole and has mass
     const int b = R.buf;
     float* fh = reinterpret_cast<float*>(S.hist[b][0]);
     R.clear(b, 1);
     __syncthreads();
     R.each([&](float x) {
-      if (x > zero && R.key(x) > keep.t) atomicAdd(&fh[coarse(x)], exp2f((x - mx) * c2));
+      if (x > least) atomicAdd(&fh[coarse(x)], exp2f((x - mx) * c2));
     });
     cl.sync();
     float fv[2] = {0.f, 0.f};
@@ -604,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       unsigned long long above = 0, in = 0, below = 0;
       unsigned int cnt = 0;
       R.each_of(s0, s1, [&](float x) {
-        if (!(x > zero) || R.key(x) <= keep.t) return;
+        if (!(x > least)) return;
         const unsigned long long w = wt(x);
         const int c = coarse(x);
         above += c < bin ? w : 0ull;
@@ -622,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (need > A + B + C) {  // into the ties of top_k
         keep.r = min(keep.r, (unsigned int)((need - (A + B + C) + tie_w - 1) / tie_w));
         sum = above + in + below;
-        counted = keep.t;
+        counted = R.value(keep.t);
         break;
       }
       if (need > A && need <= A + B) {
@@ -630,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const unsigned int hi = S.hi;
         keep = R.template refine<true>(max(S.lo, keep.t + 1), hi, cnt, need - A, wt);
         sum = above;
-        counted = hi;
+        counted = R.value(hi);
         break;
       }
       // Off (a border within the guess's rounding): the bin from exact masses.
@@ -638,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       R.clear(h, 4);
       __syncthreads();
       R.each([&](float x) {
-        if (!(x > zero) || R.key(x) <= keep.t) return;
+        if (!(x > least)) return;
         if (const unsigned long long w = wt(x)) R.add_mass(h, coarse(x), w);
       });
       cl.sync();
@@ -649,13 +678,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   }
   if (mp > 0.f) {
-    sum = 0, counted = 0xFFFFFFFFu;  // some of it may fall below the floor
+    sum = 0, counted = INFINITY;  // some of it may fall below the floor
     if (tie_w < floor_w) keep.r = 0;
   }
   // With u = 0 the first kept token wins however small its mass: weights that
   // the fixed-point unit rounds to none count as one unit there.
   const bool zero_u = !(u > 0.f) && floor_w == 1;
-  if (zero_u) sum = 0, counted = 0xFFFFFFFFu, cut = -INFINITY;
+  if (zero_u) sum = 0, counted = INFINITY, cut = -INFINITY;
   auto kept_weight = [&](float x) {
     const unsigned long long w = wt(x);
     if (w >= floor_w) return w;
@@ -663,11 +692,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 
   // Kept mass of each warp's segment, in index order from warp to warp.
+  // The threshold as a value; a tie of it counts only if some of them stay.
+  const float at = R.value(keep.t), least = fmaxf(cut, at), tie_x = keep.r ? at : NAN;
   unsigned int ties = 0;
   R.each_of(s0, s1, [&](float x) {
-    const unsigned int k = R.key(x);
-    if (k == keep.t) ++ties;
-    if (x > cut && k > keep.t && k <= counted) sum += kept_weight(x);
+    ties += x == tie_x;
+    if (x > least && x <= counted) sum += kept_weight(x);
   });
   tell(cl, S, rank, nc, sum, 0, 0, ties, 0);
   // Ties and mass before this CTA and in total; a CTA's ties count while fewer than keep.r came before.
@@ -702,9 +732,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     unsigned long long s = 0;
     unsigned int tt = 0;
     R.each_of(a0, a1, [&](float x) {
-      const unsigned int k = R.key(x);
-      if (k == keep.t) ++tt;
-      if (x > cut && k > keep.t) s += kept_weight(x);
+      tt += x == tie_x;
+      if (x > least) s += kept_weight(x);
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -720,13 +749,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i0 = a0 * E; i0 < a1 * E; i0 += 32) {  // in index order, 32 entries at a time
         const int i = i0 + lane;
         const float x = i < a1 * E ? xs[i / E].get(i % E) : -INFINITY;
-        const unsigned int k = R.key(x);
-        const bool tie = k == keep.t;
+        const bool tie = x == tie_x;
         const unsigned int tm = __ballot_sync(0xffffffffu, tie);
         unsigned long long w = 0;
         if (tie) {
           if (tb + __popc(tm & ((1u << lane) - 1u)) < keep.r) w = tie_w;
-        } else if (x > cut && k > keep.t) {
+        } else if (x > least) {
           w = kept_weight(x);
         }
         unsigned long long inc = w;

@@ -40,9 +40,9 @@ const char *cdb_ops_last_error(void);
  * logprob 0.  A logit of -inf or NaN is never chosen; a row without any other
  * gives token -1 and logprob -inf.  If a row holds +inf, its +inf entries
  * share the whole mass.  u is clamped to [0, 1); u = 0 takes the lowest kept
- * token whose weight is above e^-700.  T is clamped
- * to 2^-126..2^126.  Masses are exact sums of 64-bit fixed-point weights (unit 2^-44 of
- * the largest, each within 2^-35 of its value), so a row's token depends on nothing but the row. */
+ * token whose weight is above e^-700.  T is clamped to 2^-126..2^126.  Masses
+ * are exact sums of 64-bit fixed-point weights (unit 2^-44 of the largest, each
+ * within 2^-33 of its value), so a row's token depends on nothing but the row. */
 #define CDB_SAMPLE_MAX_VOCAB 262144
 typedef struct {
   int rows, vocab;           /* vocab <= CDB_SAMPLE_MAX_VOCAB */

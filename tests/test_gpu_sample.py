@@ -1,8 +1,8 @@
 """Sampling (include/cdb_ops.h) against a float64 restatement of its definition.
 
-Tokens must be equal: the kernel's weights are within 2^-35 of their values, so
+Tokens must be equal: the kernel's weights are within 2^-33 of their values, so
 over every row of this file (below 4000) a running sum is on the wrong side of
-its border with probability below 4000 * 2 * sqrt(262144) * 2^-35 = 1.2e-4.
+its border with probability below 4000 * 2 * sqrt(262144) * 2^-33 = 4.8e-4.
 logprob: a float32 sum of a quotient and a logarithm, each within 2^-22 of its
 value, the quotient's operand below 90 in magnitude: 90 * 2^-22 + 2^-22 * |log|.
 The reference rounds each weight to the operator's unit and adds integers: with
