@@ -49,6 +49,10 @@ class SchedCfg(C.Structure):
                 ("prep_stream", C.c_void_p), ("attn_split", C.c_int)]
 
 
+class Sampling(C.Structure):
+    _fields_ = [("temperature", C.c_float), ("top_k", C.c_int), ("top_p", C.c_float), ("min_p", C.c_float)]
+
+
 class StepInfo(C.Structure):
     _fields_ = [("stage", C.c_int), ("batch", C.c_int), ("prefill_tokens", C.c_int), ("stage2", C.c_int),
                 ("batch2", C.c_int), ("exits", C.c_int), ("q_r", C.c_int), ("q_c", C.c_int), ("q_p", C.c_int),
@@ -102,6 +106,7 @@ def lib(path: str | None = None) -> C.CDLL:
     L.cdb_init.argtypes = [C.POINTER(ModelDesc), C.POINTER(Weights), C.POINTER(SchedCfg), C.POINTER(C.c_void_p)]
     L.cdb_admit.argtypes = [C.c_void_p, C.c_int64, C.POINTER(C.c_int32), C.c_int, C.c_int,
                             C.POINTER(C.c_int8), C.POINTER(C.c_int32)]
+    L.cdb_admit_sampled.argtypes = L.cdb_admit.argtypes + [C.POINTER(Sampling), C.POINTER(C.c_float)]
     L.cdb_step_boundary.argtypes = [C.c_void_p, C.POINTER(StepInfo)]
     L.cdb_step_core.argtypes = [C.c_void_p, C.POINTER(StepInfo)]
     L.cdb_drain.argtypes = [C.c_void_p, C.POINTER(Result), C.c_int, C.POINTER(C.c_int)]
@@ -244,14 +249,25 @@ class Engine:
             raise CdbError(rc, self.L.cdb_last_error(self.ctx).decode())
         return rc
 
-    def admit(self, seq_id, prompt, max_new, force_exit=None, force_token=None):
+    def admit(self, seq_id, prompt, max_new, force_exit=None, force_token=None, sampling=None, u=None):
+        """Queue a request (cdb_admit).  sampling: a Sampling, or a dict of its fields (temperature, top_k,
+        top_p, min_p; absent filters are off), with u the max_new uniform numbers its tokens are drawn
+        with (cdb_admit_sampled); None: greedy."""
         p, pp = _i32(prompt)
         fe = fp = ft = ftp = None
         if force_exit is not None:
             fe, fp = _i8(force_exit)
         if force_token is not None:
             ft, ftp = _i32(force_token)
-        return self._check(self.L.cdb_admit(self.ctx, int(seq_id), pp, len(p), int(max_new), fp, ftp))
+        if sampling is None:
+            return self._check(self.L.cdb_admit(self.ctx, int(seq_id), pp, len(p), int(max_new), fp, ftp))
+        if not isinstance(sampling, Sampling):
+            sampling = Sampling(**{"temperature": 1.0, "top_p": 1.0, **sampling})
+        un = np.ascontiguousarray(u, dtype=np.float32)
+        if un.shape != (int(max_new),):
+            raise ValueError(f"u: expected {max_new} numbers, got shape {un.shape}")
+        return self._check(self.L.cdb_admit_sampled(self.ctx, int(seq_id), pp, len(p), int(max_new), fp, ftp,
+                                                    C.byref(sampling), un.ctypes.data_as(C.POINTER(C.c_float))))
 
     def step_boundary(self):
         info = StepInfo()

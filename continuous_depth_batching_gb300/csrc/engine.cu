@@ -18,7 +18,9 @@
 #include <vector>
 
 #include "../../include/cdb.h"
+#include "../../include/cdb_ops.h"
 #include "kernels.cuh"
+#include "sample.h"
 #include "sched.h"
 
 namespace cdb {
@@ -38,6 +40,7 @@ struct Layout {
   size_t pend_new, ring, status;
   size_t Xp, Ep, rslot, rpos, rtok, ptiles, done_idx, Cp, Cp_meta;
   size_t lslot, lt, lpos;
+  size_t samp, samp_u;  // sampling settings [W], uniform numbers [W][max_new_cap]
   size_t A, QKV, Q, O, Mid, logits, part_o, part_ml, gpart;
   size_t gpart_floats;
   // dims
@@ -113,6 +116,8 @@ static bool plan_layout(const cdb_model_desc* m, const cdb_sched_cfg* c, Layout*
   // narrow weights (at most kWideMaxSplits splits) from kWideBatch on.
   L->gpart_floats = (size_t)(W < kWideBatch ? kGemmMaxSplits : kWideMaxSplits) * W * std::max(3 * d, 2 * f);
   L->gpart = take(L->gpart_floats * 4);
+  L->samp = take(W * sizeof(SampleParams));
+  L->samp_u = take(W * cap * 4);
   L->total = o;
   return true;
 }
@@ -163,6 +168,7 @@ struct cdb_ctx {
   std::unique_ptr<cdb::Scheduler> sched;
   std::string err;
   bool dead = false;
+  bool sampling = false;  // a sampled sequence was admitted: settings of every slot are kept current
   int64_t io_h2d = 0, io_d2h = 0;
   // kernel timing (cdb_profile_enable, cdb_profile_repeat)
   bool prof_on = false;
@@ -314,6 +320,17 @@ class GpuExecutor : public Executor {
     for (size_t i = 0; i < s.force_tok.size(); ++i) ft[i] = s.force_tok[i];
     rc = upload(x, at<int>(x, L.ftok) + (size_t)s.slot * cap, ft.data(), cap * 4);
     if (rc < 0) return rc;
+    if (x->sampling) {
+      // A slot's settings until its first sequence are the arena's zeros (off).
+      const bool on = !s.u.empty();
+      const SampleParams sp = {on, s.sampling.temperature, s.sampling.top_k, s.sampling.top_p, s.sampling.min_p};
+      rc = upload(x, at<SampleParams>(x, L.samp) + s.slot, &sp, sizeof(sp));
+      if (rc < 0) return rc;
+      if (on) {
+        rc = upload(x, at<float>(x, L.samp_u) + (size_t)s.slot * cap, s.u.data(), s.u.size() * 4);
+        if (rc < 0) return rc;
+      }
+    }
     if (x->c.trace_gate)
       CK(cudaMemsetAsync(at<float>(x, L.gtrace) + (size_t)s.slot * cap * x->m.r_max, 0xFF,
                          (size_t)cap * x->m.r_max * 4, x->cs));
@@ -494,6 +511,21 @@ class GpuExecutor : public Executor {
     const bool tr = x->c.trace_tokens > 0;
     launch_argmax(x->cs, lg, n, V, m, at<int>(x, L.ftok), cap, at<int>(x, L.out_tok), tr ? at<float>(x, L.ltrace) : nullptr,
                   x->c.trace_tokens, Hrows, tr ? at<float>(x, L.htrace) : nullptr, d, at<int>(x, L.status));
+    if (x->sampling) {  // rows of sampled sequences get their token instead of the argmax
+      SampleRows r = {};
+      r.rows = n;
+      r.vocab = V;
+      r.logits = lg;
+      r.ld = V;
+      r.u = at<float>(x, L.samp_u);
+      r.token = at<int>(x, L.out_tok);
+      r.slot = m.slot;
+      r.t = m.t;
+      r.params = at<SampleParams>(x, L.samp);
+      r.forced = at<int>(x, L.ftok);
+      r.cap = cap;
+      CK(launch_sample(x->cs, r, false));
+    }
     return CDB_OK;
   }
 
@@ -944,8 +976,9 @@ int cdb_init(const cdb_model_desc* m, const cdb_weights* w, const cdb_sched_cfg*
   return CDB_OK;
 }
 
-int cdb_admit(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int prompt_len, int max_new_tokens,
-              const int8_t* force_exit, const int32_t* force_token) {
+static int admit_impl(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int prompt_len, int max_new_tokens,
+                      const int8_t* force_exit, const int32_t* force_token, const cdb_sampling* sampling,
+                      const float* u) {
   if (!x) return CDB_ERR_ARG;
   if (x->dead) return CDB_ERR_STATE;
   if (!prompt) {
@@ -963,8 +996,35 @@ int cdb_admit(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int prompt_len,
         x->err = "force_token out of range";
         return CDB_ERR_ARG;
       }
-  int rc = x->sched->admit(seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token);
+  int rc = x->sched->admit(seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token, sampling, u);
   if (rc < 0) x->err = x->sched->err;
+  return rc;
+}
+
+int cdb_admit(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int prompt_len, int max_new_tokens,
+              const int8_t* force_exit, const int32_t* force_token) {
+  return admit_impl(x, seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token, nullptr, nullptr);
+}
+
+int cdb_admit_sampled(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int prompt_len, int max_new_tokens,
+                      const int8_t* force_exit, const int32_t* force_token, const cdb_sampling* sampling,
+                      const float* u) {
+  if (!x) return CDB_ERR_ARG;
+  if (x->dead) return CDB_ERR_STATE;
+  const char* why = nullptr;
+  if (!sampling || !u) why = "sampling and u are needed";
+  else if (x->m.vocab > CDB_SAMPLE_MAX_VOCAB) why = "the vocabulary is too large to sample from";
+  else if (std::isnan(sampling->temperature) || std::isnan(sampling->top_p) || std::isnan(sampling->min_p))
+    why = "a sampling setting is NaN";
+  else
+    for (int i = 0; i < max_new_tokens; ++i)
+      if (!(u[i] >= 0.f && u[i] < 1.f)) why = "a uniform number is outside [0, 1)";
+  if (why) {
+    x->err = why;
+    return CDB_ERR_ARG;
+  }
+  const int rc = admit_impl(x, seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token, sampling, u);
+  if (rc >= 0) x->sampling = true;
   return rc;
 }
 

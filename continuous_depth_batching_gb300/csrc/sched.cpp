@@ -21,7 +21,8 @@ int Scheduler::blocks_per_seq_max() const { return (c_.max_ctx + c_.kv_block - 1
 static int ctx_positions(const Seq& s) { return s.P + s.max_new - 1; }
 
 int Scheduler::admit(int64_t id, const int32_t* prompt, int P, int max_new,
-                     const int8_t* force_exit, const int32_t* force_tok) {
+                     const int8_t* force_exit, const int32_t* force_tok, const cdb_sampling* sampling,
+                     const float* u) {
   if (P < 1 || max_new < 1) return fail(CDB_ERR_ARG, "prompt_len and max_new_tokens must be >= 1");
   if (max_new > c_.max_new_cap) return fail(CDB_ERR_ARG, "max_new_tokens exceeds max_new_cap");
   if (P + max_new - 1 > c_.max_ctx) return fail(CDB_ERR_ARG, "prompt_len + max_new_tokens - 1 exceeds max_ctx");
@@ -38,6 +39,10 @@ int Scheduler::admit(int64_t id, const int32_t* prompt, int P, int max_new,
         return fail(CDB_ERR_ARG, "force_exit entries must be 0 or in [r_min, r_max]");
   }
   if (force_tok) s.force_tok.assign(force_tok, force_tok + max_new);
+  if (sampling) {
+    s.sampling = *sampling;
+    s.u.assign(u, u + max_new);
+  }
   int need = (ctx_positions(s) + c_.kv_block - 1) / c_.kv_block;
   if (need > c_.kv_blocks) return fail(CDB_ERR_KV_FULL, "sequence needs more KV blocks than the pool holds");
   seqs_.push_back(std::move(s));

@@ -44,6 +44,8 @@ struct Seq {
   int P = 0, max_new = 0;
   std::vector<int8_t> force_exit;  // empty: live gate
   std::vector<int32_t> force_tok;  // empty: live argmax
+  cdb_sampling sampling = {0.f, 0, 1.f, 0.f};
+  std::vector<float> u;            // uniform numbers of a sampled sequence, one per token; empty: greedy
   int state = kWaiting;
   int slot = -1;        // sequence slot (0..W-1) while active
   int prefilled = 0;    // prompt tokens already prefilled
@@ -102,7 +104,7 @@ class Scheduler {
   Scheduler(const SchedCfg& c, Executor* ex);
 
   int admit(int64_t id, const int32_t* prompt, int P, int max_new, const int8_t* force_exit,
-            const int32_t* force_tok);
+            const int32_t* force_tok, const cdb_sampling* sampling = nullptr, const float* u = nullptr);
   int step_boundary(cdb_step_info* info);
   int step_core(cdb_step_info* info);
 

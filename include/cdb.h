@@ -193,6 +193,26 @@ int cdb_init(const cdb_model_desc *m, const cdb_weights *w, const cdb_sched_cfg 
 int cdb_admit(cdb_ctx *ctx, int64_t seq_id, const int32_t *prompt, int prompt_len,
               int max_new_tokens, const int8_t *force_exit, const int32_t *force_token);
 
+/* How a sequence's tokens are chosen from their logits; see cdb_sample
+ * (cdb_ops.h) for the filters and their order. */
+typedef struct {
+  float temperature; /* not > 0: greedy argmax */
+  int top_k;         /* <= 0: off */
+  float top_p;       /* >= 1: off */
+  float min_p;       /* <= 0: off */
+} cdb_sampling;
+
+/* cdb_admit for a sequence whose tokens are sampled: token t (the first one,
+ * which prefill produces, is token 0) is drawn with the uniform number u[t]
+ * (HOST array of max_new_tokens numbers in [0, 1), copied).  The given numbers
+ * decide: the same request gives the same tokens in every mode and batch.
+ * force_token entries >= 0 take precedence.  A row of logits with nothing but
+ * -inf and NaN gives token 0, as the argmax does.  CDB_ERR_ARG for a vocabulary
+ * above CDB_SAMPLE_MAX_VOCAB, a NaN setting or a number outside [0, 1). */
+int cdb_admit_sampled(cdb_ctx *ctx, int64_t seq_id, const int32_t *prompt, int prompt_len,
+                      int max_new_tokens, const int8_t *force_exit, const int32_t *force_token,
+                      const cdb_sampling *sampling, const float *u);
+
 /* Run the next non-core stage the mode's priority rule selects (Alg. 1 / 2):
  * coda (+prelude), prefill (+prelude in refill mode), or a cohort prelude.
  * Returns CDB_IDLE when the next stage is a core step, CDB_DONE when all
