@@ -709,17 +709,17 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 // owns columns 4j..4j+3.
 template <int HD>
 __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
-  pdl_wait();
-  pdl_trigger();
+  // Before the wait: only what the caller gave.  The attention kernels let this
+  // one start after their own wait, so earlier kernels' writes are visible.
   const cdb_attention_args& a = A.a;
   const int lane = threadIdx.x & 31;
   const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int row = item / a.n_heads, h = item % a.n_heads;
-  if (row >= a.rows) return;
-  const int seq = a.seq[row], pos = a.pos[row];
-  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
-  if (seq < 0 || seq >= a.cache.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= a.cache.n_kv_slots) return;
-  if (A.chunks > 0 && h == 0) {  // does the row name the prefix's blocks?
+  const bool in = row < a.rows;
+  const int seq = in ? a.seq[row] : -1, pos = in ? a.pos[row] : -1;
+  const int slot = a.slot_base + (in && a.depth ? a.depth[row] : 0);
+  const bool live = seq >= 0 && seq < a.cache.n_seqs && pos < a.max_ctx && slot >= 0 && slot < a.cache.n_kv_slots;
+  if (A.chunks > 0 && h == 0 && live) {  // does the row name the prefix's blocks?
     int base = -1;
     for (int r0 = 0; base < 0; r0 += 32) {  // ends: this row has a sequence
       const int s = r0 + lane < a.rows ? a.seq[r0 + lane] : -1;
@@ -734,29 +734,49 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
     for (int p = lane; p < pages; p += 32) differ |= t0[p] ^ t1[p];
     if (differ) report(a.status, CDB_OPS_NOT_SHARED);
   }
+  pdl_wait();
+  pdl_trigger();
+  if (!live) return;
   const int L = pos + 1;
   const int parts = A.chunks + row_parts(L, A.first, A.split, A.wph);
   if (A.chunks == 0 && parts <= 1) return;  // written by the attention kernel
   const size_t pi = ((size_t)row * a.n_heads + h) * A.parts;
+  const bool cols = 4 * lane < HD;
+  const float* po = A.part_o + pi * HD + 4 * lane;
+  // The first eight partials are in flight while the weights are worked out.
+  constexpr int kAhead = 8;
+  float4 x[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    x[k] = cols && k < parts ? *reinterpret_cast<const float4*>(po + (size_t)k * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY;
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, A.part_ml[pi + s].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const bool cols = 4 * lane < HD;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
+  auto add = [&](const float4& p, float wk) {
+    if (wk != 0.f) v.x = fmaf(p.x, wk, v.x), v.y = fmaf(p.y, wk, v.y), v.z = fmaf(p.z, wk, v.z), v.w = fmaf(p.w, wk, v.w);
+  };
   for (int s0 = 0; s0 < parts; s0 += 32) {
     const int s = s0 + lane, n = min(32, parts - s0);
     const float2 ml = s < parts ? A.part_ml[pi + s] : make_float2(-INFINITY, 0.f);
     const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m), ls = ml.y * w;
+    int k0 = 0;
+    if (s0 == 0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);  // 0 behind the last partial
+        l += __shfl_sync(0xffffffffu, ls, k);
+        add(x[k], wk);
+      }
+      k0 = kAhead;
+    }
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
+    for (int k = k0; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       l += __shfl_sync(0xffffffffu, ls, k);
-      if (cols && wk != 0.f) {
-        const float4 x = *reinterpret_cast<const float4*>(A.part_o + (pi + s0 + k) * HD + 4 * lane);
-        v.x = fmaf(x.x, wk, v.x), v.y = fmaf(x.y, wk, v.y), v.z = fmaf(x.z, wk, v.z), v.w = fmaf(x.w, wk, v.w);
-      }
+      if (cols) add(*reinterpret_cast<const float4*>(po + (size_t)(s0 + k) * HD), wk);
     }
   }
   if (!cols) return;

@@ -35,7 +35,10 @@
 //                   would take four instructions).  A key's scale multiplies
 //                   its fp32 score, a value's scale its weight, relative to
 //                   the largest value scale so far (fp16's range); q becomes
-//                   fp16, each row divided by a power of two.
+//                   fp16, each row divided by a power of two.  (Scaled by the
+//                   converters instead, rounded to fp16: 163 us where this takes
+//                   129, 256 rows x 32/8 heads behind 16384 tokens: the
+//                   converters then hold the others up.)
 // Waits and issues of one block cost a warp some 500 cycles (a commit about
 // 140, a wait 100), as much as the products themselves: hence two issuing warps,
 // one commit per product, and pairs of barriers that two lanes wait for at once.
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t to = trow + G::O_COL + g * HD;
     float m = -INFINITY, l = 0.f;
-    float ref = 0x1p-126f, iref = 0x1p126f;  // e4m3: value scale the weights are relative to, its reciprocal
+    float ref = 0x1p-60f, lref = -60.f;      // e4m3: value scale the weights are relative to, its logarithm
     float up = 1.f;                          // e4m3: what q was divided by
     bool ok = true;
     {
@@ -456,12 +459,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
             tmem_st32(to + c0, reinterpret_cast<const uint32_t*>(v));
           }
         }
-        if (Q8 && rnew != ref) ref = rnew, iref = 1.f / rnew;
+        if (Q8 && rnew != ref) ref = rnew, lref = log2f(rnew);
       }
-      const float mm = m == -INFINITY ? 0.f : m;
+      // e4m3: the weights come out of the exponential divided by ref (their sum is multiplied back; ref is at
+      // least 2^-60, so none overflows, and a weight that this flushes is no weight beside the maximum's).
+      const float mm = (m == -INFINITY ? 0.f : m) + (Q8 ? lref : 0.f);
       uint32_t p[32];
-      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm), i2 = pair(iref, iref);
-      uint64_t l2[2] = {pair(l, 0.f), pair(0.f, 0.f)};
+      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+      uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
         float x0, x1, x2, x3;
@@ -473,8 +478,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         if constexpr (Q8) {
           const float4 f = ks[kKeys / 4 + e / 2];
           // Keys behind the chunk may have any scale, NaN too, but their pages are not multiplied.
-          unpair(mul2(mul2(pair(f.x, f.y), i2), pair(x0, x1)), x0, x1);
-          unpair(mul2(mul2(pair(f.z, f.w), i2), pair(x2, x3)), x2, x3);
+          unpair(mul2(pair(f.x, f.y), pair(x0, x1)), x0, x1);
+          unpair(mul2(pair(f.z, f.w), pair(x2, x3)), x2, x3);
           p[e] = pack_f16(x0, x1);
           p[e + 1] = pack_f16(x2, x3);
         } else {
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       float la, lb, lc, ld;
       unpair(l2[0], la, lb);
       unpair(l2[1], lc, ld);
-      l = (la + lb) + (lc + ld);
+      l += ((la + lb) + (lc + ld)) * (Q8 ? ref : 1.f);
       tmem_st32(ts, p);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
