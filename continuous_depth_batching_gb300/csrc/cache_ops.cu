@@ -809,8 +809,10 @@ cudaError_t launch_as(cudaStream_t s, const Args& A) {
 }
 
 template <int HD, bool Q8>
-cudaError_t launch(cudaStream_t s, const Args& A) {
-  const cudaError_t e = A.group > 4 ? launch_as<HD, Q8, true>(s, A) : launch_as<HD, Q8, false>(s, A);
+cudaError_t launch(cudaStream_t s, const Args& A, const SharedPlan& sh) {
+  cudaError_t e = A.group > 4 ? launch_as<HD, Q8, true>(s, A) : launch_as<HD, Q8, false>(s, A);
+  // The prefix after the rows' own keys: its CTAs move in as the others drain.
+  if (e == cudaSuccess && A.chunks > 0) e = launch_shared_prefix(s, A.a, sh, A.parts, A.part_o, A.part_ml);
   if (e != cudaSuccess || (A.chunks == 0 && A.parts <= 1)) return e;
   count_launch();
   const long long items = (long long)A.a.rows * A.a.n_heads;
@@ -881,16 +883,12 @@ cudaError_t launch_decode_attention(cudaStream_t s, const cdb_attention_args& a)
   const size_t cells = (size_t)a.rows * a.n_heads * A.parts;
   A.part_o = static_cast<float*>(a.workspace);
   A.part_ml = reinterpret_cast<float2*>(A.part_o + cells * a.cache.head_dim);
-  if (sh.chunks) {
-    const cudaError_t e = launch_shared_prefix(s, a, sh, A.parts, A.part_o, A.part_ml);
-    if (e != cudaSuccess) return e;
-  }
   const bool q8 = a.cache.dtype == CDB_E4M3;
   switch (a.cache.head_dim) {
-    case 32: return q8 ? da::launch<32, true>(s, A) : da::launch<32, false>(s, A);
-    case 64: return q8 ? da::launch<64, true>(s, A) : da::launch<64, false>(s, A);
-    case 96: return q8 ? da::launch<96, true>(s, A) : da::launch<96, false>(s, A);
-    case 128: return q8 ? da::launch<128, true>(s, A) : da::launch<128, false>(s, A);
+    case 32: return q8 ? da::launch<32, true>(s, A, sh) : da::launch<32, false>(s, A, sh);
+    case 64: return q8 ? da::launch<64, true>(s, A, sh) : da::launch<64, false>(s, A, sh);
+    case 96: return q8 ? da::launch<96, true>(s, A, sh) : da::launch<96, false>(s, A, sh);
+    case 128: return q8 ? da::launch<128, true>(s, A, sh) : da::launch<128, false>(s, A, sh);
     default: return cudaErrorInvalidValue;
   }
 }

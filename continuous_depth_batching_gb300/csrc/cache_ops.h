@@ -28,7 +28,8 @@ struct SharedPlan {
   int chunks;     // partials per (row, head)
 };
 // The prefix's partials (shared_prefix.cu): [row][head][parts], the first
-// p.chunks of each; head_dim 64 or 128.
+// p.chunks of each; head_dim 64 or 128.  Launched right after the kernel for the
+// rows' own keys, beside which it runs; its end is the end of both.
 cudaError_t launch_shared_prefix(cudaStream_t s, const cdb_attention_args& a, const SharedPlan& p, int parts, float* part_o,
                                  float2* part_ml);
 

@@ -175,8 +175,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_trigger();
+  pdl_trigger();  // no wait yet: see the end
   const int k_lo = chunk * A.chunk, k_hi = min(a.shared_len, k_lo + A.chunk);
   const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;  // >= 1
   const int npg = (k_hi - k_lo) / 16;
@@ -537,6 +536,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::TMEM_COLS));
   }
+  // This kernel follows the one for the rows' own keys and shares no data with
+  // it, so it starts as soon as every CTA of that one has started, which is
+  // after its own wait for whatever came before.  Waiting here makes the end of
+  // this grid the end of both, which is what the join waits for.
+  pdl_wait();
 }
 
 template <int HD, bool Q8>
