@@ -19,192 +19,255 @@ namespace cdb {
 // Cache write.
 //
 // A streaming kernel: every element of qkv is read once and written once, so
-// HBM bounds it.  One CTA per row; groups of GW lanes take one head at a time,
-// 8 elements per lane (16-byte loads for bf16, two for fp32; the rotation's
-// partner elements sit rot_dim / 16 lanes away), so the sums of the norm and
-// the maximum of the quantisation are shuffles inside the group and a head is
-// never staged in memory.  Each lane keeps the (cos, sin) of its 8 elements in
-// registers over all heads of the row.
+// HBM bounds it.  Persistent CTAs, three per SM: a producer warp looks up 32
+// rows at a time (sequence, position, block) and copies each row, or a part of
+// at most 24 KB of it, and its line of the rotation table into a three-stage
+// ring with bulk copies, so that lookups and loads run two rows ahead of the
+// arithmetic (one CTA per row, loading for itself, reached 3.8 TB/s where this
+// reaches 5.8, 8192 rows of 16 heads fp32 to e4m3).  Eight warps do the
+// arithmetic: groups of GW lanes take one head at a time, 8 elements per lane,
+// four of the rotation's lower half and their four partners of the upper one
+// (or, behind rot_dim, 8 in a row), so a rotation stays in the lane and the
+// sums of the norm and the maximum of the quantisation are shuffles inside the
+// group.
 // ---------------------------------------------------------------------------
 namespace cw {
 
-constexpr int kThreads = 256;
+constexpr int kConsumers = 256;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kStages = 3;
+constexpr int kData = 24 * 1024;  // bytes of a row part
+constexpr int kTable = 512;       // bytes of a table line (128 elements)
+
+// What the producer found out about a stage's row.
+struct Meta {
+  int row, h0, heads, in_page;  // in_page: position in the page, -1: nothing to do
+  long long cell;               // cached heads before this position's block and slot
+};
+struct Stage {
+  alignas(16) uint8_t data[kData];
+  float2 table[kTable / 8];
+  Meta meta;
+};
+struct Shared {
+  Stage stage[kStages];
+  uint64_t full[kStages], empty[kStages];
+};
 
 template <int HD>
 struct Geo {
   static constexpr int GW = HD / 8 <= 4 ? 4 : HD / 8 <= 8 ? 8 : 16;  // lanes of a group (hd 96: 12 of 16 work)
-  static constexpr int NG = kThreads / GW;
+  static constexpr int NG = kConsumers / GW;
 };
 
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  Chunk<float>::load(p, v);
-  Chunk<float>::load(p + 4, v + 4);
+// Four elements as fp32.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  uint4 u;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return u;
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float* v) {
+  return make_uint2(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]));
+}
+__device__ __forceinline__ uint32_t code4(const float* v, float f) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * f, v[1] * f), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * f, v[3] * f), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 
-// Heads of a group whose elements are loaded together: their bytes are in
-// flight while the row's sequence, position and block are looked up.
-constexpr int kAhead = 3;
-
-// 8 elements as loaded.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-};
-template <>
-struct Raw<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float* v) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-};
-
+// unit_heads: heads of a part; parts: parts of a row.
 template <typename T, int HD, bool Q8>
-__global__ void __launch_bounds__(kThreads, 4) k_cache_write(const __grid_constant__ cdb_cache_write_args a) {
+__global__ void __launch_bounds__(kThreads, 3)
+    k_cache_write(const __grid_constant__ cdb_cache_write_args a, int unit_heads, int parts) {
   using G = Geo<HD>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& S = *reinterpret_cast<Shared*>(raw);
+  const cdb_paged_cache& c = a.cache;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&S.full[i], 1);
+      tc::mbar_init(&S.empty[i], kConsumers / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x;
-  const int g = threadIdx.x / G::GW, l = threadIdx.x % G::GW;
-  const cdb_paged_cache& c = a.cache;
-  const int seq = a.seq[row], pos = a.pos[row], dep = a.depth ? a.depth[row] : 0;
-  const bool on = l * 8 < HD;
   const int H = a.n_heads, Hk = c.n_kv_heads, total = H + 2 * Hk;
-  const T* src = reinterpret_cast<const T*>(a.qkv) + (size_t)row * a.ldqkv + l * 8;
-  Raw<T> raw[kAhead] = {};
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (on && g + i * G::NG < total) raw[i].load(src + (size_t)(g + i * G::NG) * HD);
-  if (seq < 0) return;  // padding
-  if (seq >= c.n_seqs || pos < 0 || pos >= c.max_blocks * 16 || (a.rope && pos >= a.rope_positions)) {
-    if (threadIdx.x == 0) report(a.status, CDB_OPS_BAD_ROW);
-    return;
-  }
-  const int slot = a.slot_base + dep;
-  const int blk = c.block_table[(size_t)seq * c.max_blocks + (pos >> 4)];
-  // Groups of a warp may be at different kinds of heads: shuffles name their group's lanes only.
-  const uint32_t peers = (0xffffffffu >> (32 - G::GW)) << ((threadIdx.x & 31) / G::GW * G::GW);
-  // Rotation: x' = x cos + y sn, y the element rot_dim / 2 away, sn = -sin in the lower half and sin in
-  // the upper one.
-  const int rl = a.rope ? a.rot_dim / 16 : 0;  // lanes of one half
-  const bool low = l < rl, turned = l < 2 * rl;
-  float cs[8], sn[8];
-  if (turned) {
-    const float4* t = reinterpret_cast<const float4*>(a.rope + ((size_t)pos * (a.rot_dim / 2) + (low ? l : l - rl) * 8) * 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = t[i];
-      cs[2 * i] = v.x, sn[2 * i] = low ? -v.y : v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = low ? -v.w : v.w;
-    }
-  }
-  const int peer = (low ? l + rl : l - rl) & (G::GW - 1);  // lane holding the rotation's other element
-  if (slot < 0 || slot >= c.n_kv_slots || blk < 0 || blk >= c.kv_blocks) {
-    if (threadIdx.x == 0) report(a.status, blk < 0 || blk >= c.kv_blocks ? CDB_OPS_BAD_BLOCK : CDB_OPS_BAD_SLOT);
-    return;
-  }
-  // Cached element (kv half, head j) of this position starts at ((cell + kv Hk + j) 16 + pos % 16).
-  const size_t cell = ((size_t)blk * c.n_kv_slots + slot) * 2 * Hk;
+  const long long units = (long long)a.rows * parts;
+  const int n = (int)((units - blockIdx.x + gridDim.x - 1) / gridDim.x);  // of this CTA; >= 1
 
-  for (int h0 = g; h0 < total; h0 += kAhead * G::NG) {
-    if (h0 != g) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (on && h0 + i * G::NG < total) raw[i].load(src + (size_t)(h0 + i * G::NG) * HD);
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int h = h0 + i * G::NG;
-      if (h >= total) break;
-      float v[8];
-      raw[i].get(v);  // zeros in the idle lanes of a 96-element head
-      if (h < H + Hk) {
-        if (a.q_gain) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-#pragma unroll
-          for (int o = G::GW / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o, G::GW);
-          const float r = rsqrtf(ss * (1.f / HD) + a.eps);
-          if (on) {
-            float w[8];
-            load8((h < H ? a.q_gain : a.k_gain) + l * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
-          }
-        }
-        if (rl) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float o = __shfl_sync(peers, v[e], peer, G::GW);
-            if (turned) v[e] = __fadd_rn(__fmul_rn(v[e], cs[e]), __fmul_rn(o, sn[e]));
+  if (tid >= kConsumers) {
+    // ---------------- producer ----------------
+    bool ok = true;
+    int issued = 0, in_page = -1, row_l = 0, pos_l = 0;
+    long long cell_l = 0;
+    for (int i = 0; i < n; ++i) {
+      if ((i & 31) == 0) {  // this lane looks up unit i + lane
+        in_page = -1;
+        const long long u = blockIdx.x + (long long)(i + lane) * gridDim.x;
+        if (u < units) {
+          row_l = (int)(u / parts);
+          const int seq = a.seq[row_l];
+          if (seq >= 0) {
+            pos_l = a.pos[row_l];
+            const int slot = a.slot_base + (a.depth ? a.depth[row_l] : 0);
+            if (seq >= c.n_seqs || pos_l < 0 || pos_l >= c.max_blocks * 16 || (a.rope && pos_l >= a.rope_positions)) {
+              report(a.status, CDB_OPS_BAD_ROW);
+            } else {
+              const int blk = c.block_table[(size_t)seq * c.max_blocks + (pos_l >> 4)];
+              if (blk < 0 || blk >= c.kv_blocks) {
+                report(a.status, CDB_OPS_BAD_BLOCK);
+              } else if (slot < 0 || slot >= c.n_kv_slots) {
+                report(a.status, CDB_OPS_BAD_SLOT);
+              } else {
+                cell_l = ((long long)blk * c.n_kv_slots + slot) * 2 * Hk;
+                in_page = pos_l & 15;
+              }
+            }
           }
         }
       }
-      if (h < H) {
-        if (on)
-          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + (size_t)row * a.ldq + (size_t)h * HD + l * 8) =
-              pack8(v);
-        continue;
-      }
-      const size_t at = (cell + (h - H)) * 16 + (pos & 15);  // K heads, then V heads
-      if constexpr (Q8) {
-        // Scale of this (position, head): the largest magnitude maps to 448; the
-        // floor keeps the scale and its reciprocal normal numbers.
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-#pragma unroll
-        for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
-        const float s = fmaxf(m * (1.f / 448.f), 0x1p-126f);
-        const float inv = __frcp_rn(s);
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j] * inv, v[4 * j + 1] * inv), __NV_SATFINITE,
-                                                       __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2] * inv, v[4 * j + 3] * inv),
-                                                       __NV_SATFINITE, __NV_E4M3);
-          w[j] = lo | (hi << 16);
+      const int s = i % kStages;
+      const int row = __shfl_sync(0xffffffffu, row_l, i & 31), pos = __shfl_sync(0xffffffffu, pos_l, i & 31);
+      const int where = __shfl_sync(0xffffffffu, in_page, i & 31);
+      const long long cell = __shfl_sync(0xffffffffu, cell_l, i & 31);
+      if (i >= kStages && !(ok = __all_sync(0xffffffffu, tc::mbar_wait(&S.empty[s], ((i / kStages) - 1) & 1)))) break;
+      const int part = (int)((blockIdx.x + (long long)i * gridDim.x) % parts);
+      const int h0 = part * unit_heads, heads = min(unit_heads, total - h0);
+      if (tc::elect_one()) {
+        Stage& st = S.stage[s];
+        st.meta = Meta{row, h0, heads, where, cell};
+        const uint32_t bytes = (uint32_t)heads * HD * sizeof(T), line = a.rope ? (uint32_t)a.rot_dim * 4 : 0u;
+        tc::mbar_arrive_tx(&S.full[s], where >= 0 ? bytes + line : 0u);
+        if (where >= 0) {
+          tc::bulk_1d(tc::su32(st.data), reinterpret_cast<const T*>(a.qkv) + (size_t)row * a.ldqkv + (size_t)h0 * HD, bytes,
+                      &S.full[s]);
+          if (line) tc::bulk_1d(tc::su32(st.table), a.rope + (size_t)pos * a.rot_dim, line, &S.full[s]);
         }
-        if (on) *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(c.pool) + at * HD + l * 8) = make_uint2(w[0], w[1]);
-        if (l == 0) c.scales[at] = s;
-      } else if (on) {
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.pool) + at * HD + l * 8) = pack8(v);
       }
+      __syncwarp();
+      issued = i + 1;
     }
+    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    // Copies in flight land before the CTA may leave (at once when the consumers took every stage).
+    for (int i = max(0, issued - kStages); i < issued; ++i) tc::mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
+    return;
   }
+
+  // ---------------- arithmetic ----------------
+  const int g = tid / G::GW, l = tid % G::GW;
+  const bool on = l * 8 < HD;
+  // Groups of a warp may be at different kinds of heads: shuffles name their group's lanes only.
+  const uint32_t peers = (0xffffffffu >> (32 - G::GW)) << (lane / G::GW * G::GW);
+  // This lane's elements e0..e0+3 and e1..e1+3: partners of the rotation, or 8 in a row.
+  const int rl = a.rope ? a.rot_dim / 8 : 0;
+  const bool turned = l < rl;
+  const int e0 = turned ? 4 * l : 8 * l, e1 = turned ? a.rot_dim / 2 + 4 * l : 8 * l + 4;
+  float wq[8] = {}, wk[8] = {};
+  if (a.q_gain && on) {
+    load4(a.q_gain + e0, wq), load4(a.q_gain + e1, wq + 4);
+    load4(a.k_gain + e0, wk), load4(a.k_gain + e1, wk + 4);
+  }
+  bool ok = true;
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kStages;
+    if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&S.full[s], (i / kStages) & 1)))) break;
+    const Stage& st = S.stage[s];
+    const Meta meta = st.meta;
+    if (meta.in_page >= 0) {
+      float2 cs[4];
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = st.table[e0 + e];
+      }
+      const T* src = reinterpret_cast<const T*>(st.data);
+      for (int r = g; r < meta.heads; r += G::NG) {
+        const int h = meta.h0 + r;
+        float v[8] = {};  // zeros in the idle lanes of a 96-element head
+        if (on) load4(src + r * HD + e0, v), load4(src + r * HD + e1, v + 4);
+        if (h < H + Hk) {
+          if (a.q_gain) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+            for (int o = G::GW / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(peers, ss, o, G::GW);
+            const float f = rsqrtf(ss * (1.f / HD) + a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * f * (h < H ? wq[e] : wk[e]);
+          }
+          if (turned) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rope_pair(v[e], v[e + 4], cs[e], v[e], v[e + 4]);
+          }
+        }
+        if (h < H) {
+          if (on) {
+            __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(a.q) + (size_t)meta.row * a.ldq + (size_t)h * HD;
+            *reinterpret_cast<uint2*>(q + e0) = pack4(v);
+            *reinterpret_cast<uint2*>(q + e1) = pack4(v + 4);
+          }
+          continue;
+        }
+        const size_t at = (size_t)(meta.cell + (h - H)) * 16 + meta.in_page;  // K heads, then V heads
+        if constexpr (Q8) {
+          // Scale of this (position, head): the largest magnitude maps to 448; the
+          // floor keeps the scale and its reciprocal normal numbers.
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+#pragma unroll
+          for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
+          const float f = fmaxf(m * (1.f / 448.f), 0x1p-126f);
+          const float inv = __frcp_rn(f);
+          uint8_t* dst = reinterpret_cast<uint8_t*>(c.pool) + at * HD;
+          if (on) {
+            *reinterpret_cast<uint32_t*>(dst + e0) = code4(v, inv);
+            *reinterpret_cast<uint32_t*>(dst + e1) = code4(v + 4, inv);
+          }
+          if (l == 0) c.scales[at] = f;
+        } else if (on) {
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(c.pool) + at * HD;
+          *reinterpret_cast<uint2*>(dst + e0) = pack4(v);
+          *reinterpret_cast<uint2*>(dst + e1) = pack4(v + 4);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&S.empty[s]);
+  }
+  if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+}
+
+template <typename T, int HD, bool Q8>
+cudaError_t launch_as(cudaStream_t s, const cdb_cache_write_args& a) {
+  static int sms[kMaxDevices] = {};
+  const int dev = current_device();
+  if (!sms[dev]) {
+    int n = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_cache_write<T, HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    sms[dev] = n;
+  }
+  const int total = a.n_heads + 2 * a.cache.n_kv_heads, most = kData / (HD * (int)sizeof(T));
+  const int parts = (total + most - 1) / most, unit_heads = (total + parts - 1) / parts;
+  const long long units = (long long)a.rows * parts;
+  count_launch();
+  return launch_pdl(k_cache_write<T, HD, Q8>, dim3((unsigned)std::min(units, 3ll * sms[dev])), dim3(kThreads), sizeof(Shared), s,
+                    a, unit_heads, parts);
 }
 
 template <typename T, int HD>
 cudaError_t launch(cudaStream_t s, const cdb_cache_write_args& a) {
-  count_launch();
-  if (a.cache.dtype == CDB_E4M3)
-    return launch_pdl(k_cache_write<T, HD, true>, dim3(a.rows), dim3(kThreads), 0, s, a);
-  return launch_pdl(k_cache_write<T, HD, false>, dim3(a.rows), dim3(kThreads), 0, s, a);
+  return a.cache.dtype == CDB_E4M3 ? launch_as<T, HD, true>(s, a) : launch_as<T, HD, false>(s, a);
 }
 
 }  // namespace cw
