@@ -768,21 +768,26 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   }
 }
 
-// Join a row's partials in split order: one warp per (row, query head), lane j
-// owns columns 4j..4j+3.
-template <int HD>
+// Join a row's partials: lane j owns columns 4j..4j+3.  Up to kAhead partials
+// are one warp's work, in order; of more, warp w of four takes w, w + 4, ...,
+// and the four sums are added in order (few rows of long contexts have more
+// partials than warps: 63 of them took one warp 9 us).  Which of the two goes by
+// the row's own partials.  TEAM: four warps per (row, query head), else one.
+constexpr int kAhead = 8;
+
+template <int HD, bool TEAM>
 __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   // Before the wait: only what the caller gave.  The attention kernels let this
   // one start after their own wait, so earlier kernels' writes are visible.
   const cdb_attention_args& a = A.a;
   const int lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, item = TEAM ? blockIdx.x : blockIdx.x * 4 + warp;
   const int row = item / a.n_heads, h = item % a.n_heads;
   const bool in = row < a.rows;
   const int seq = in ? a.seq[row] : -1, pos = in ? a.pos[row] : -1;
   const int slot = a.slot_base + (in && a.depth ? a.depth[row] : 0);
   const bool live = seq >= 0 && seq < a.cache.n_seqs && pos < a.max_ctx && slot >= 0 && slot < a.cache.n_kv_slots;
-  if (A.chunks > 0 && h == 0 && live) {  // does the row name the prefix's blocks?
+  if (A.chunks > 0 && h == 0 && live && (!TEAM || warp == 0)) {  // does the row name the prefix's blocks?
     int base = -1;
     for (int r0 = 0; base < 0; r0 += 32) {  // ends: this row has a sequence
       const int s = r0 + lane < a.rows ? a.seq[r0 + lane] : -1;
@@ -806,12 +811,15 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   const size_t pi = ((size_t)row * a.n_heads + h) * A.parts;
   const bool cols = 4 * lane < HD;
   const float* po = A.part_o + pi * HD + 4 * lane;
-  // The first eight partials are in flight while the weights are worked out.
-  constexpr int kAhead = 8;
+  const bool team = TEAM && parts > kAhead;
+  if (TEAM && !team && warp > 0) return;
+  const int step = team ? 4 : 1, k0 = team ? warp : 0;  // this warp's partials: k0, k0 + step, ...
+  // The first ones are in flight while the weights are worked out.
   float4 x[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
-    x[k] = cols && k < parts ? *reinterpret_cast<const float4*>(po + (size_t)k * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[k] = cols && k0 + k * step < parts ? *reinterpret_cast<const float4*>(po + (size_t)(k0 + k * step) * HD)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY;
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, A.part_ml[pi + s].x);
 #pragma unroll
@@ -821,11 +829,12 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   auto add = [&](const float4& p, float wk) {
     if (wk != 0.f) v.x = fmaf(p.x, wk, v.x), v.y = fmaf(p.y, wk, v.y), v.z = fmaf(p.z, wk, v.z), v.w = fmaf(p.w, wk, v.w);
   };
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    const int s = s0 + lane, n = min(32, parts - s0);
-    const float2 ml = s < parts ? A.part_ml[pi + s] : make_float2(-INFINITY, 0.f);
+  const int mine = (parts - k0 + step - 1) / step;
+  for (int s0 = 0; s0 < mine; s0 += 32) {  // 32 of this warp's partials at a time, a weight per lane
+    const int s = s0 + lane, n = min(32, mine - s0);
+    const float2 ml = s < mine ? A.part_ml[pi + k0 + s * step] : make_float2(-INFINITY, 0.f);
     const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m), ls = ml.y * w;
-    int k0 = 0;
+    int k1 = 0;
     if (s0 == 0) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -833,13 +842,31 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
         l += __shfl_sync(0xffffffffu, ls, k);
         add(x[k], wk);
       }
-      k0 = kAhead;
+      k1 = kAhead;
     }
 #pragma unroll 4
-    for (int k = k0; k < n; ++k) {
+    for (int k = k1; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       l += __shfl_sync(0xffffffffu, ls, k);
-      if (cols) add(*reinterpret_cast<const float4*>(po + (size_t)(s0 + k) * HD), wk);
+      if (cols) add(*reinterpret_cast<const float4*>(po + (size_t)(k0 + (s0 + k) * step) * HD), wk);
+    }
+  }
+  if constexpr (TEAM) {
+    if (team) {  // uniform in the block
+      __shared__ float4 sv[3][32];
+      __shared__ float sl[3];
+      if (warp > 0) {
+        sv[warp - 1][lane] = v;
+        if (lane == 0) sl[warp - 1] = l;
+      }
+      __syncthreads();
+      if (warp > 0) return;
+#pragma unroll
+      for (int w = 0; w < 3; ++w) {
+        const float4 o = sv[w][lane];
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        l += sl[w];
+      }
     }
   }
   if (!cols) return;
@@ -879,7 +906,8 @@ cudaError_t launch(cudaStream_t s, const Args& A, const SharedPlan& sh) {
   if (e != cudaSuccess || (A.chunks == 0 && A.parts <= 1)) return e;
   count_launch();
   const long long items = (long long)A.a.rows * A.a.n_heads;
-  return launch_pdl(k_join<HD>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, s, A);
+  if (A.parts > kAhead) return launch_pdl(k_join<HD, true>, dim3((unsigned)items), dim3(128), 0, s, A);
+  return launch_pdl(k_join<HD, false>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, s, A);
 }
 
 }  // namespace da
