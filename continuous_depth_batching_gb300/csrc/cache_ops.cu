@@ -429,7 +429,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const cdb_attention_args& a = A.a;
   const cdb_paged_cache& c = a.cache;
-  const int row = blockIdx.x / A.nhg, hg = blockIdx.x % A.nhg, sp = blockIdx.y;
+  // Last splits first: they are the partly filled ones and, of the longest rows, the ones a launch in
+  // ascending order would end with (64 rows of 128 to 1280 keys, e4m3: 38.7 us ascending, 35.4 so).
+  const int row = blockIdx.x / A.nhg, hg = blockIdx.x % A.nhg, sp = gridDim.y - 1 - blockIdx.y;
   const int qb = hg % A.qblocks, k0 = hg / A.qblocks * A.hpc;  // first KV head
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");

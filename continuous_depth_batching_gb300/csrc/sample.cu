@@ -14,7 +14,7 @@
 // equal steps of m - x, then histograms over the ordered bit patterns of the
 // chosen bin, until the bin holds exactly what is needed or a single value.
 // top_k counts, after the maxima of single threads have ruled out most of the
-// row.  top_p guesses its bin from fp32 weights and then adds up the exact mass
+// row.  top_p guesses its bin from counts and mean offsets and adds up the exact mass
 // above and in it, so each logit's exact weight is computed once.  Each CTA
 // works on its slice in its own shared memory, all CTAs of the cluster then
 // read one another's histograms or sums (distributed shared memory) and come to
@@ -312,20 +312,29 @@ struct Row {
   }
 
   // The keys with coarse(value) == bin into S.lo, S.hi: coarse() falls as the key grows, so its bounds come
-  // by bisection (warp 0: the smallest key with coarse <= bin, warp 1: with coarse <= bin - 1).
+  // by bisection, 32 keys at a time (warp 0: the smallest key with coarse <= bin, warp 1: with coarse <= bin - 1).
   template <typename F>
   __device__ __forceinline__ void bin_keys(int bin, F coarse) {
-    const int tid = threadIdx.x;
-    if (tid < 64 && (tid & 31) == 0) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < 64) {
       const int want = bin - (tid >> 5);
       unsigned int lo = key(-3.402823466e38f), hi = key(m) + 1;  // answer in [lo, hi]
       while (lo < hi) {
-        const unsigned int mid = lo + ((hi - lo) >> 1);
-        if (coarse(value(mid)) <= want) hi = mid;
-        else lo = mid + 1;
+        const unsigned int step = (hi - lo) / 32 + 1, mid = lo + lane * step;
+        const bool below = mid >= hi || coarse(value(mid)) <= want;  // the answer is not above mid
+        const unsigned int first = __ffs(__ballot_sync(0xffffffffu, below)) - 1;  // 32 if none
+        const unsigned int l = lo;
+        if (first == 0) {
+          hi = lo;
+        } else {
+          lo = l + (first > 32 ? 31 : first - 1) * step + 1;
+          if (first <= 31) hi = min(hi, l + first * step);
+        }
       }
-      if (tid == 0) S.lo = lo;
-      else S.hi = lo - 1;
+      if (lane == 0) {
+        if (tid == 0) S.lo = lo;
+        else S.hi = lo - 1;
+      }
     }
     __syncthreads();
   }
@@ -593,31 +602,43 @@ __global__ void __launch_bounds__(kThreads, 2)
   // This warp's segment of the slice: the sums below go by it.
   const int seg = (nv / 32 + kWarps - 1) / kWarps * 32;
   const int s0 = min(nv, warp * seg), s1 = min(nv, s0 + seg);
+  // Where most logits have a weight, weights without a branch around them overlap.
+  const bool dense = keep.t == 0 && !(mp > 1e-4f);
   unsigned long long tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   unsigned long long sum = 0;             // this lane's kept mass above keys `counted`
   float counted = INFINITY;               // logits above it are in `sum` already
   if (tp < 1.f) {
     // A first guess of the bin, 1024 equal steps of the logits that have mass,
-    // from sums of fp32 weights; then the exact mass above it, in it and below
-    // decides (and moves the bin, should the guess be off).
+    // from each bin's count and mean offset (its mass to 1e-4); then the exact
+    // mass above it, in it and below decides.
     const float step = (float)kBins / 31.5f * wt.ch;
     auto coarse = [&](float x) { return min(kBins - 1, (int)((mx - x) * step)); };
-    const float c2 = wt.ch * 1.4426950408889634f, zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);
+    const float zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);
     const float least = fmaxf(zero, R.value(keep.t));  // above it is what top_k keeps whole and has mass
     const int b = R.buf;
-    float* fh = reinterpret_cast<float*>(S.hist[b][0]);
-    R.clear(b, 1);
+    R.clear(b, 2);
     __syncthreads();
     R.each([&](float x) {
-      if (x > least) atomicAdd(&fh[coarse(x)], exp2f((x - mx) * c2));
+      if (!(x > least)) return;
+      const float y = (mx - x) * step;
+      const int c = min(kBins - 1, (int)y);
+      atomicAdd(&S.hist[b][0][c], 1u);
+      atomicAdd(&S.hist[b][1][c], (unsigned int)((y - (float)c) * 4096.f) & 0x1FFFu);
     });
     cl.sync();
-    float fv[2] = {0.f, 0.f};
+    unsigned int hc[2] = {0, 0}, ho[2] = {0, 0};
     for (int i = 0; i < nc; ++i) {
-      const float2 o = *reinterpret_cast<const float2*>(&cl.map_shared_rank(&S, i)->hist[b][0][2 * tid]);
-      fv[0] += o.x, fv[1] += o.y;
+      const Shared* o = cl.map_shared_rank(&S, i);
+      const uint2 x = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]), y = *reinterpret_cast<const uint2*>(&o->hist[b][1][2 * tid]);
+      hc[0] += x.x, hc[1] += x.y, ho[0] += y.x, ho[1] += y.y;
     }
     R.buf ^= 1;
+    float fv[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float mean = hc[e] ? (float)ho[e] / (4096.f * (float)hc[e]) : 0.f;
+      fv[e] = (float)hc[e] * exp2f(-((float)(2 * tid + e) + mean) * (31.5f * 1.4426950408889634f / kBins));
+    }
     float ft = fv[0] + fv[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ft += __shfl_xor_sync(0xffffffffu, ft, o);
@@ -625,22 +646,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     ft = 0.f;
     for (int w = 0; w < kWarps; ++w) ft += S.fmx[w];
-    const unsigned int none[2] = {0, 0};
     const float with_ties = ft + (float)tie_w * 0x1p-44f * (float)keep.r;
-    R.template find<float>(fv, none, fmaxf(fminf(tp * with_ties, 0.999998f * ft), 1e-30f));
+    R.template find<float>(fv, hc, fmaxf(fminf(tp * with_ties, 0.999998f * ft), 1e-30f));
     int bin = min((int)S.found_bin, kBins - 1);
     while (true) {
       unsigned long long above = 0, in = 0, below = 0;
       unsigned int cnt = 0;
-      R.each_of(s0, s1, [&](float x) {
-        if (!(x > least)) return;
-        const unsigned long long w = wt(x);
+      auto put = [&](float x, unsigned long long w) {
         const int c = coarse(x);
         above += c < bin ? w : 0ull;
         in += c == bin ? w : 0ull;
         below += c > bin ? w : 0ull;
         cnt += c == bin && w != 0;
-      });
+      };
+      if (dense) {
+        R.each_of(s0, s1, [&](float x) {
+          const unsigned long long w = wt(x);
+          put(x, x > least ? w : 0ull);
+        });
+      } else {
+        R.each_of(s0, s1, [&](float x) {
+          if (x > least) put(x, wt(x));
+        });
+      }
       tell(cl, S, rank, nc, above, in, below, 0, cnt);
       unsigned long long A = 0, B = 0, C = 0;
       cnt = 0;
@@ -695,10 +723,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   // The threshold as a value; a tie of it counts only if some of them stay.
   const float at = R.value(keep.t), least = fmaxf(cut, at), tie_x = keep.r ? at : NAN;
   unsigned int ties = 0;
-  R.each_of(s0, s1, [&](float x) {
-    ties += x == tie_x;
-    if (x > least && x <= counted) sum += kept_weight(x);
-  });
+  if (dense && counted == INFINITY && !zero_u) {  // no threshold but the floor
+    R.each_of(s0, s1, [&](float x) {
+      const unsigned long long w = wt(x);
+      sum += x > least && w >= floor_w ? w : 0ull;
+    });
+  } else {
+    R.each_of(s0, s1, [&](float x) {
+      ties += x == tie_x;
+      if (x > least && x <= counted) sum += kept_weight(x);
+    });
+  }
   tell(cl, S, rank, nc, sum, 0, 0, ties, 0);
   // Ties and mass before this CTA and in total; a CTA's ties count while fewer than keep.r came before.
   unsigned long long total = 0, mine0 = 0;
