@@ -1023,9 +1023,13 @@ int cdb_admit_sampled(cdb_ctx* x, int64_t seq_id, const int32_t* prompt, int pro
     x->err = why;
     return CDB_ERR_ARG;
   }
-  const int rc = admit_impl(x, seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token, sampling, u);
-  if (rc >= 0) x->sampling = true;
-  return rc;
+  try {
+    const int rc = admit_impl(x, seq_id, prompt, prompt_len, max_new_tokens, force_exit, force_token, sampling, u);
+    if (rc >= 0) x->sampling = true;
+    return rc;
+  } catch (...) {  // no exception crosses the C boundary
+    return CDB_ERR_STATE;
+  }
 }
 
 int cdb_step_boundary(cdb_ctx* x, cdb_step_info* info) {

@@ -49,7 +49,7 @@ const char* bad_cache(const cdb_paged_cache& c) {
 #define CDB_ENTRY_END                \
   }                                  \
   catch (...) {                      \
-    return CDB_ERR_STATE;            \
+    return CDB_ERR_STATE; /* out of host memory */ \
   }
 
 extern "C" {
@@ -63,6 +63,7 @@ int cdb_sample(const cdb_sample_args* a, void* stream) {
   if (a->vocab < 1 || a->vocab > CDB_SAMPLE_MAX_VOCAB) return refuse("vocab must be in 1..262144");
   if (a->ld < a->vocab) return refuse("ld is smaller than vocab");
   if (a->dtype != CDB_FP32 && a->dtype != CDB_BF16) return refuse("logits must be fp32 or bf16");
+  if (a->rows == 0) return CDB_OK;
   if (!a->logits || !a->u || !a->temperature || !a->token) return refuse("logits, u, temperature and token are needed");
   if ((uintptr_t)a->logits % (a->dtype == CDB_FP32 ? 4 : 2)) return refuse("logits are not aligned to their type");
   cdb::SampleRows r = {};
@@ -92,6 +93,7 @@ int cdb_cache_write(const cdb_cache_write_args* a, void* stream) {
   if (a->dtype != CDB_FP32 && a->dtype != CDB_BF16) return refuse("qkv must be fp32 or bf16");
   const int64_t es = a->dtype == CDB_FP32 ? 4 : 2;
   if (a->ldqkv < ((int64_t)a->n_heads + 2 * a->cache.n_kv_heads) * hd) return refuse("ldqkv is smaller than a row");
+  if (a->rows == 0) return CDB_OK;
   if (!a->qkv || !aligned(a->qkv, 16) || a->ldqkv * es % 16) return refuse("qkv is missing or its rows are not 16-byte aligned");
   if (!a->q || !aligned(a->q, 16) || a->ldq % 8 || a->ldq < (int64_t)a->n_heads * hd)
     return refuse("q is missing, too narrow, or its rows are not 16-byte aligned");
@@ -133,6 +135,7 @@ int cdb_attention(const cdb_attention_args* a, void* stream) {
   if ((uint64_t)c.kv_blocks * c.n_kv_slots * 2 * c.n_kv_heads * 16 >= (1ull << 31) - 64)
     return refuse("the pool has more than 2^31 key rows");
   if (a->max_ctx > (int64_t)c.max_blocks * 16) return refuse("max_ctx is longer than the block table");
+  if (a->rows == 0) return CDB_OK;
   const int64_t width = (int64_t)a->n_heads * c.head_dim;
   if (!a->q || !aligned(a->q, 16) || a->ldq % 8 || a->ldq < width)
     return refuse("q is missing, too narrow, or its rows are not 16-byte aligned");

@@ -4,8 +4,9 @@ For programs that drive the model themselves instead of through
 ``binding.Engine``.  Each class checks its arguments, keeps the argument
 structure and the output buffers of its operator, and enqueues one call on the
 current CUDA stream; nothing synchronizes, and every call can be captured into
-a CUDA graph.  An object's default outputs are overwritten by its next call,
-so one object serves one stream at a time.
+a CUDA graph.  An object's default outputs and its workspace are overwritten by
+its next call, so one object serves one stream at a time.  An object works on
+the device that was current when it was made; no gradients are recorded.
 """
 
 from __future__ import annotations
@@ -75,6 +76,8 @@ class _Op:
         self.dev = torch.cuda.current_device()
 
     def _stream(self):
+        if self._t.cuda.current_device() != self.dev:
+            raise ValueError(f"made on cuda:{self.dev}, the current device is cuda:{self._t.cuda.current_device()}")
         return self._t.cuda.current_stream(self.dev).cuda_stream
 
     def _vec(self, name, t, dtype, n):

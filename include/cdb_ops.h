@@ -6,11 +6,15 @@
  * with cdb_admit_sampled use the sampler below.
  *
  * Conventions.  All pointers inside the argument structs are device pointers
- * on the current device unless marked otherwise; nothing is allocated, nothing
- * is kept between calls, no call synchronizes.  Work is enqueued on `stream`
- * (cudaStream_t, NULL: the legacy default stream) and can be captured into a
- * CUDA graph.  Calls return CDB_OK, CDB_ERR_ARG (refused before any launch;
- * cdb_ops_last_error() says why) or CDB_ERR_CUDA (a launch failed).
+ * on the current device unless marked otherwise, inputs and outputs do not
+ * overlap; nothing is allocated, nothing is kept between calls, no call
+ * synchronizes.  Work is enqueued on `stream` (cudaStream_t, NULL: the legacy
+ * default stream) and can be captured into a CUDA graph (with CUDA's lazy
+ * loading, make the first call of an operator outside of the capture).  Calls
+ * of several host threads or streams may run at once if they share no output,
+ * workspace or status.  rows = 0 does nothing.  Calls return CDB_OK,
+ * CDB_ERR_ARG (refused before any launch; cdb_ops_last_error() says why),
+ * CDB_ERR_CUDA (a launch failed) or CDB_ERR_STATE (out of host memory).
  */
 #ifndef CDB_OPS_H
 #define CDB_OPS_H

@@ -314,6 +314,124 @@ def test_shared_prefix_of_other_blocks_is_reported():
     assert int(at.status.item()) == 128
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [1.0, 0.0, -0.3])
+def test_shared_prefix_scales(dtype, scale):
+    # Sharp scores, none, and turned-round ones.
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    cs = attention_case(dtype, 4, 2, 64, [30, 7, 1, 90], shared=320, seed=11)
+    at = ops.DecodeAttention(cs["cache"], 4, 4, scale=scale)
+    out = at(cs["q"], cs["seq"], cs["pos"], shared_len=320)
+    at.check()
+    v = cs["vals"][:, :, 1].nan_to_num().abs().max()
+    for i in range(4):
+        o, tol = expected(cs, i, scale)
+        assert bool(((out[i].double().view(4, 64) - o).abs() <= tol + 2.0 ** -8 * v).all())
+
+
+def test_shared_value_scales_over_many_orders():
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    cs = attention_case("e4m3", 4, 4, 128, [30, 40], shared=1024, seed=12)
+    sc = cs["cache"].scales
+    g = torch.Generator(device="cuda").manual_seed(1)
+    f = torch.exp2(torch.randint(-20, 21, sc[:, :, 1].shape, generator=g, device="cuda").float())
+    sc[:, :, 1] *= f
+    cs["vals"][:, :, 1] *= f.double()[..., None]
+    at = ops.DecodeAttention(cs["cache"], 4, 2)
+    out = at(cs["q"], cs["seq"], cs["pos"], shared_len=1024)
+    at.check()
+    v = cs["vals"][:, :, 1].nan_to_num().abs().max()
+    for i in range(2):
+        o, tol = expected(cs, i, 128 ** -0.5)
+        assert bool(((out[i].double().view(4, 128) - o).abs() <= tol + 2.0 ** -8 * v).all())
+
+
+def test_zero_values_in_the_cache():
+    # Pages of zeros: codes 0 with the smallest scale; the output of such keys alone is 0.
+    import torch
+    for shared in (0, 64):
+        cs = attention_case("e4m3", 4, 4, 64, [20, 33], shared=shared, seed=13)
+        cs["cache"].pool.view(torch.uint8)[:, :, 1] = 0
+        cs["cache"].scales[:, :, 1] = 2.0 ** -126
+        from continuous_depth_batching_gb300 import ops
+        at = ops.DecodeAttention(cs["cache"], 4, 2)
+        out = at(cs["q"], cs["seq"], cs["pos"], shared_len=shared)
+        at.check()
+        assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_shared_prefix_in_a_graph_and_on_a_side_stream(dtype):
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    cs = attention_case(dtype, 8, 4, 128, [40, 300, 7, 19, 120], shared=528, seed=14)
+    plain = ops.DecodeAttention(cs["cache"], 8, 5)
+    at = ops.DecodeAttention(cs["cache"], 8, 5)
+    q, out = cs["q"].clone(), torch.zeros_like(cs["q"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        at(q, cs["seq"], cs["pos"], shared_len=528, out=out)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(3):  # back to back on one workspace
+                at(q, cs["seq"], cs["pos"], shared_len=528, out=out)
+    torch.cuda.synchronize()
+    for seed in range(5):
+        q.copy_(torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
+        g.replay()
+        got = out.clone()
+        assert torch.equal(got, plain(q, cs["seq"], cs["pos"], shared_len=528))
+    at.check()
+
+
+def test_a_decode_step_of_all_operators():
+    # Project, write, attend behind a shared prompt, project to logits, sample: against the same step in float64.
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    from tests.test_gpu_sample import reference
+    H, hk, hd, d, vocab, rows, shared = 8, 4, 64, 256, 1000, 6, 64
+    g = torch.Generator(device="cuda").manual_seed(21)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    cs = attention_case("e4m3", H, hk, hd, [5, 17, 1, 40, 16, 33], shared=shared, seed=22)
+    cache, vals = cs["cache"], cs["vals"]
+    h, wqkv, head = rnd(rows, d), rnd((H + 2 * hk) * hd, d) / 16, rnd(vocab, H * hd) / 8
+    rope, gain = ops.rope_table(256, hd), 1 + 0.1 * rnd(hd)
+    seq, pos = cs["seq"], cs["pos"]  # the last position of each sequence is this step's
+    w = ops.CacheWriter(cache, H, rope, gain, gain)
+    at, s = ops.DecodeAttention(cache, H, rows), ops.Sampler(rows, vocab)
+    u, t = torch.rand(rows, generator=g, device="cuda"), torch.full((rows,), 0.9, device="cuda")
+    p = torch.full((rows,), 0.8, device="cuda")
+    qkv = h @ wqkv.T
+    q = w(qkv, seq, pos)
+    o = at(q, seq, pos, shared_len=shared)
+    logits = o.float() @ head.T
+    token, _ = s(logits, u, t, top_p=p)
+    w.check()
+    at.check()
+    # Reference: the written row's key and value from the cache they went to, everything before it as it was.
+    blk, off = cache.block_table[seq.long(), pos.long() // 16].long(), pos.long() % 16
+    vals[blk, 0, :, :, off] = cache.pool[blk, 0, :, :, off].double() * cache.scales[blk, 0, :, :, off].double()[..., None]
+    x = qkv.double().view(rows, H + 2 * hk, hd)
+    y = x[:, :H + hk] / torch.sqrt((x[:, :H + hk] ** 2).mean(-1, keepdim=True) + 1e-6) * gain.double()
+    c = torch.view_as_complex(rope.double().contiguous())[pos.long()][:, None]
+    z = torch.complex(y[..., :hd // 2].contiguous(), y[..., hd // 2:].contiguous()) * c
+    y = torch.cat([z.real, z.imag], -1)
+    assert bool(((q.double().view(rows, H, hd) - y[:, :H]).abs() <= 2.0 ** -8 * y[:, :H].abs() + 2.0 ** -18).all())
+    new = vals[blk, 0, :, :, off]
+    want = torch.stack([y[:, H:], x[:, H + hk:]], 1)
+    big = want.abs().amax(-1, keepdim=True)
+    assert bool(((new - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * big / 448 + 2.0 ** -18 * big).all())
+    cs = dict(cs, q=q)
+    for i in range(rows):
+        e, tol = expected(cs, i, hd ** -0.5)
+        tol = tol + 2.0 ** -8 * vals[:, :, 1].nan_to_num().abs().max()
+        assert bool(((o[i].double().view(H, hd) - e).abs() <= tol).all())
+        assert int(token[i]) == reference(logits[i].cpu().numpy(), float(u[i]), np.float32(0.9), None, np.float32(0.8))[0]
+
+
 def write_reference(cs):
     """Float64 queries [rows, H, hd], keys and values [rows, 2, hk, hd]."""
     import torch

@@ -94,6 +94,8 @@ def test_attention_refuses(L, bad):
 
 
 def test_empty_batches(L):
+    assert L.cdb_sample(C.byref(sample_args(rows=0, logits=None, u=None, token=None)), None) == 0
+    assert L.cdb_attention(C.byref(attention_args(rows=0, q=None, seq=None, workspace=None, workspace_bytes=0)), None) == 0
     assert L.cdb_cache_write(C.byref(write_args(rows=0)), None) == 0
     assert L.cdb_attention(C.byref(attention_args(rows=0)), None) == 0
 
