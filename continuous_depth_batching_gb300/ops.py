@@ -93,10 +93,10 @@ class _Op:
         """Device pointer and row stride of a [>= rows, >= cols] matrix with contiguous rows."""
         shape, stride = t.shape, t.stride()
         if (t.dtype not in dtypes or t.get_device() != self.dev or len(shape) != 2 or shape[0] < rows or
-                shape[1] < cols or (stride[1] != 1 and shape[1] > 1)):
-            raise ValueError(f"{name}: expected [{rows}, {cols}] with contiguous rows of {dtypes} on cuda:{self.dev}, "
-                             f"got {tuple(shape)} {t.dtype} on {t.device}")
-        return t.data_ptr(), max(stride[0], shape[1])
+                shape[1] < cols or (stride[1] != 1 and shape[1] > 1) or (stride[0] < shape[1] and shape[0] > 1)):
+            raise ValueError(f"{name}: expected [{rows}, {cols}] with contiguous rows, one behind another, of {dtypes} "
+                             f"on cuda:{self.dev}, got {tuple(shape)} with strides {tuple(stride)} {t.dtype} on {t.device}")
+        return t.data_ptr(), max(stride[0], shape[1])  # one row: its stride says nothing
 
 
 class Sampler(_Op):

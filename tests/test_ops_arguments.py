@@ -109,3 +109,17 @@ def test_attention_workspace_sizes(L):
     for rows in (1, 2, 3, 31, 32, 33, 64):
         for shared in range(0, 4097, 16):
             assert L.cdb_attention_workspace(rows, 16, 4, 128, 4096, shared) <= any_prefix
+
+
+def test_matrices_whose_rows_overlap_are_refused():
+    """A broadcast row has stride 0, which the operators' row stride cannot say."""
+    import torch
+    op = object.__new__(ops._Op)
+    op.dev = -1  # where CPU tensors are
+    x = torch.zeros(4, 32)
+    assert op._mat("x", x, (torch.float32,), 4, 32) == (x.data_ptr(), 32)
+    assert op._mat("x", x[:, :24], (torch.float32,), 4, 24) == (x.data_ptr(), 32)
+    assert op._mat("x", x[:1].expand(1, 32), (torch.float32,), 1, 32)[1] == 32
+    for bad in (x[:1].expand(4, 32), x.as_strided((4, 32), (16, 1)), x.t(), x[0], x[:, ::2]):
+        with pytest.raises(ValueError):
+            op._mat("x", bad, (torch.float32,), bad.shape[0], bad.shape[-1])
