@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     const bool in = r < A.group * A.tile_rows && br < a.rows;
     const int seq = in ? a.seq[br] : -1, pos = in ? a.pos[br] : -1;
     const bool live = in && seq >= 0 && seq < c.n_seqs && pos < a.max_ctx;
-    const int lim = min(pos, k_hi - 1) - k_lo;  // last key of this row, from the chunk's first
+    const int lim = min(max(pos, -1), k_hi - 1) - k_lo;  // last key of this row, from the chunk's first
     // Scores in the log2 domain; a negative factor turns the scores around first, so that the
     // maximum can be taken before the factor is applied.
     const bool turn_round = a.scale < 0.f;

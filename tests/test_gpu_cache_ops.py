@@ -296,6 +296,18 @@ def test_shared_prefix_rows_inside_it_and_padding(dtype):
     assert bool((out == 3).all())
 
 
+@pytest.mark.parametrize("shared", [0, 208])
+def test_rows_without_keys_at_any_negative_position(shared):
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    cs = attention_case("bf16", 8, 2, 64, [20, 30, 3, 90], shared=208, seed=4)
+    cs["pos"][1], cs["pos"][2] = -2 ** 31, -1000
+    at = ops.DecodeAttention(cs["cache"], 8, 4)
+    out = at(cs["q"], cs["seq"], cs["pos"], shared_len=shared)
+    at.check()
+    assert bool((out[1:3] == 0).all()) and bool((out[[0, 3]] != 0).any(1).all())
+
+
 def test_shared_prefix_exactly_the_context():
     # No row has keys of its own.
     cs = attention_case("bf16", 4, 4, 128, [1, 1, 1], shared=128, seed=2)
