@@ -1,6 +1,7 @@
 // C entry points of the decode-step operators (include/cdb_ops.h): argument
 // checks and launches.
 #include <climits>
+#include <cmath>
 #include <string>
 
 #include "../../include/cdb.h"
@@ -142,6 +143,7 @@ int cdb_attention(const cdb_attention_args* a, void* stream) {
   if (!a->out || !aligned(a->out, 16) || a->ldo % 8 || a->ldo < width)
     return refuse("out is missing, too narrow, or its rows are not 16-byte aligned");
   if (!a->seq || !a->pos) return refuse("seq and pos are needed");
+  if (!std::isfinite(a->scale)) return refuse("scale must be finite");
   if (a->shared_len && (a->depth || a->slot_base < 0 || a->slot_base >= c.n_kv_slots))
     return refuse("a shared prefix needs all rows in one slot (depth NULL, slot_base a slot of the cache)");
   if (!a->workspace || !aligned(a->workspace, 256) ||

@@ -81,7 +81,8 @@ typedef struct {
 } cdb_paged_cache;
 
 /* Device status bits that the cache operators OR into *status (a device int32
- * the caller zeroes; NULL: not reported).  The row concerned is skipped. */
+ * the caller zeroes; NULL: not reported).  The row concerned is skipped; where
+ * attention meets a bad block (a shared prefix: all rows), outputs are undefined. */
 #define CDB_OPS_BAD_BLOCK 1   /* block table entry out of range */
 #define CDB_OPS_BAD_SLOT 2    /* slot_base + depth out of range */
 #define CDB_OPS_BAD_ROW 8     /* sequence or position out of range */
@@ -129,7 +130,7 @@ int cdb_cache_write(const cdb_cache_write_args *a, void *stream);
  * other rows.
  * shared_len > 0 (a multiple of 16) says that every row's sequence names the
  * same blocks for positions 0..shared_len-1 (a common prompt, all of it
- * written): those keys are then read once for all rows (head_dim 64 and 128,
+ * written, its values finite): those keys are then read once for all rows (head_dim 64 and 128,
  * two rows or more, at most 128 query heads per KV head; else the prefix is
  * read per row), and cut by the number of rows, which changes a row's roundings.
  * The sequence of the first row with seq >= 0 names the blocks that are read; a
@@ -145,7 +146,7 @@ typedef struct {
   const int32_t *seq, *pos;
   const int32_t *depth;
   int slot_base;
-  float scale;
+  float scale;            /* finite */
   int max_ctx;            /* every pos < max_ctx (checked on the device), <= max_blocks * 16 */
   int shared_len;
   void *out;              /* bf16 [rows][ldo]; 16-byte aligned rows */

@@ -93,6 +93,12 @@ def test_attention_refuses(L, bad):
     assert L.cdb_ops_last_error()
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_refuses_scales_that_are_not_finite(L, scale):
+    assert L.cdb_attention(C.byref(attention_args(scale=scale)), None) == ARG
+    assert b"scale" in L.cdb_ops_last_error()
+
+
 def test_empty_batches(L):
     assert L.cdb_sample(C.byref(sample_args(rows=0, logits=None, u=None, token=None)), None) == 0
     assert L.cdb_attention(C.byref(attention_args(rows=0, q=None, seq=None, workspace=None, workspace_bytes=0)), None) == 0
