@@ -12,6 +12,8 @@ the device that was current when it was made; no gradients are recorded.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
+import os
 
 from .binding import CdbError, lib
 
@@ -62,8 +64,22 @@ def _lib():
     return L
 
 
-def _fail(L, rc, what):
-    raise CdbError(rc, f"{what}: {L.cdb_ops_last_error().decode()}")
+_calls = None
+
+
+def _tensor_calls():
+    """The module of csrc/tensor_calls.cpp: checks of tensors and calls."""
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (its libraries have to be loaded)
+
+        from .build import CALLS
+        if not os.path.exists(CALLS):
+            raise RuntimeError(f"CDB library not built ({CALLS}); run continuous_depth_batching_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("cdb_tensor_calls", CALLS)
+        _calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_calls)
+    return _calls
 
 
 class _Op:
@@ -74,15 +90,28 @@ class _Op:
         self._t = torch
         self.L = _lib()
         self.dev = torch.cuda.current_device()
+        self._device, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+    def _bind(self, what, call):
+        """The C entry point and the argument structure that self._call fills in."""
+        self._what, self._call = what, getattr(_tensor_calls(), call)
+        self._fn, self._ref = C.cast(getattr(self.L, what), C.c_void_p).value, C.addressof(self.args)
 
     def _stream(self):
-        if self._t.cuda.current_device() != self.dev:
-            raise ValueError(f"made on cuda:{self.dev}, the current device is cuda:{self._t.cuda.current_device()}")
-        return self._t.cuda.current_stream(self.dev).cuda_stream
+        if self._device() != self.dev:
+            raise ValueError(f"made on cuda:{self.dev}, the current device is cuda:{self._device()}")
+        return self._raw_stream(self.dev)
 
-    def _vec(self, name, t, dtype, n):
+    def _fail(self, rc):
+        if rc is None:
+            raise ValueError(f"{self._what}: a tensor has no memory or is a view that negates its values")
+        raise CdbError(rc, f"{self._what}: {self.L.cdb_ops_last_error().decode()}")
+
+    def _vec(self, name, t, dtype, n, needed=False):
         """Device pointer of a contiguous vector of at least n elements."""
         if t is None:
+            if needed:
+                raise ValueError(f"{name} is needed")
             return None
         if t.dtype is not dtype or t.get_device() != self.dev or t.numel() < n or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous {dtype} vector of at least {n} on cuda:{self.dev}, got "
@@ -116,27 +145,32 @@ class Sampler(_Op):
         self.max_rows, self.vocab = int(max_rows), int(vocab)
         self.token = t.empty(self.max_rows, dtype=t.int32, device=f"cuda:{self.dev}")
         self.logprob = t.empty(self.max_rows, dtype=t.float32, device=f"cuda:{self.dev}")
-        self.args = SampleArgs(vocab=self.vocab)
-        self._ref = C.byref(self.args)
+        self.args = SampleArgs(vocab=self.vocab, token=self.token.data_ptr(), logprob=self.logprob.data_ptr())
+        self._bind("cdb_sample", "sample")
+        self._out = self.token, self.logprob  # of the last number of rows
 
     def __call__(self, logits, u, temperature, top_k=None, top_p=None, min_p=None):
-        t, a = self._t, self.args
-        rows = logits.shape[0]
+        rc = self._call(self._fn, self._ref, self._stream(), self.dev, self.max_rows, logits, u, temperature, top_k,
+                        top_p, min_p)
+        if rc != 0:
+            if rc is None:
+                self._explain(logits, u, temperature, top_k, top_p, min_p)
+            self._fail(rc)
+        rows = self.args.rows
+        if self._out[0].shape[0] != rows:
+            self._out = self.token[:rows], self.logprob[:rows]
+        return self._out
+
+    def _explain(self, logits, u, temperature, top_k, top_p, min_p):
+        t, rows = self._t, logits.shape[0]
         if rows > self.max_rows or logits.shape[-1] != self.vocab:
             raise ValueError(f"logits {tuple(logits.shape)}: at most {self.max_rows} rows of {self.vocab}")
-        a.rows = rows
-        a.logits, a.ld = self._mat("logits", logits, (t.float32, t.bfloat16), rows, self.vocab)
-        a.dtype = BF16 if logits.dtype == t.bfloat16 else FP32
-        a.u = self._vec("u", u, t.float32, rows)
-        a.temperature = self._vec("temperature", temperature, t.float32, rows)
-        a.top_k = self._vec("top_k", top_k, t.int32, rows)
-        a.top_p = self._vec("top_p", top_p, t.float32, rows)
-        a.min_p = self._vec("min_p", min_p, t.float32, rows)
-        a.token, a.logprob = self.token.data_ptr(), self.logprob.data_ptr()
-        rc = self.L.cdb_sample(self._ref, self._stream())
-        if rc != 0:
-            _fail(self.L, rc, "cdb_sample")
-        return self.token[:rows], self.logprob[:rows]
+        self._mat("logits", logits, (t.float32, t.bfloat16), rows, self.vocab)
+        self._vec("u", u, t.float32, rows, True)
+        self._vec("temperature", temperature, t.float32, rows, True)
+        self._vec("top_k", top_k, t.int32, rows)
+        self._vec("top_p", top_p, t.float32, rows)
+        self._vec("min_p", min_p, t.float32, rows)
 
 
 class PagedCache:
@@ -183,6 +217,10 @@ class _CacheOp(_Op):
         self.width = self.n_heads * cache.head_dim
         self.status = self._t.zeros(1, dtype=self._t.int32, device=cache.pool.device)
 
+    def _rows(self, rows, seq, pos, depth):
+        for name, v, needed in (("seq", seq, True), ("pos", pos, True), ("depth", depth, False)):
+            self._vec(name, v, self._t.int32, rows, needed)
+
     def check(self):
         """Wait for the device and raise if a call found an index out of range."""
         st = int(self.status.item())
@@ -215,23 +253,20 @@ class CacheWriter(_CacheOp):
             a.rope, a.rope_positions, a.rot_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
         self._keep = (rope, q_gain, k_gain)
         a.status = self.status.data_ptr()
-        self._ref = C.byref(a)
+        self._bind("cdb_cache_write", "cache_write")
 
     def __call__(self, qkv, seq, pos, depth=None, slot_base=0, q_out=None):
-        t, a = self._t, self.args
-        rows = qkv.shape[0]
         if q_out is None:
-            q_out = t.zeros(rows, self.width, dtype=t.bfloat16, device=qkv.device)
-        a.rows, a.slot_base = rows, slot_base
-        a.qkv, a.ldqkv = self._mat("qkv", qkv, (t.float32, t.bfloat16), rows,
-                                   self.width + 2 * self.cache.n_kv_heads * self.cache.head_dim)
-        a.dtype = BF16 if qkv.dtype == t.bfloat16 else FP32
-        a.seq, a.pos = self._vec("seq", seq, t.int32, rows), self._vec("pos", pos, t.int32, rows)
-        a.depth = self._vec("depth", depth, t.int32, rows)
-        a.q, a.ldq = self._mat("q_out", q_out, (t.bfloat16,), rows, self.width)
-        rc = self.L.cdb_cache_write(self._ref, self._stream())
+            q_out = self._t.zeros(qkv.shape[0], self.width, dtype=self._t.bfloat16, device=qkv.device)
+        rc = self._call(self._fn, self._ref, self._stream(), self.dev, qkv, seq, pos, depth, slot_base, q_out)
         if rc != 0:
-            _fail(self.L, rc, "cdb_cache_write")
+            if rc is None:
+                t, rows = self._t, qkv.shape[0]
+                self._mat("qkv", qkv, (t.float32, t.bfloat16), rows,
+                          self.width + 2 * self.cache.n_kv_heads * self.cache.head_dim)
+                self._rows(rows, seq, pos, depth)
+                self._mat("q_out", q_out, (t.bfloat16,), rows, self.width)
+            self._fail(rc)
         return q_out
 
 
@@ -258,23 +293,22 @@ class DecodeAttention(_CacheOp):
         self.args = AttentionArgs(cache=cache.desc, n_heads=self.n_heads, scale=hd ** -0.5 if scale is None else scale,
                                   max_ctx=self.max_ctx, status=self.status.data_ptr(), workspace=base,
                                   workspace_bytes=n)
-        self._ref = C.byref(self.args)
+        self._bind("cdb_attention", "attention")
 
     def __call__(self, q, seq, pos, depth=None, slot_base=0, shared_len=0, out=None):
-        t, a = self._t, self.args
-        rows = q.shape[0]
-        if rows > self.max_rows:
-            raise ValueError(f"{rows} rows, the workspace holds {self.max_rows}")
         if out is None:
-            out = t.zeros(rows, self.width, dtype=t.bfloat16, device=q.device)
-        a.rows, a.slot_base, a.shared_len = rows, slot_base, shared_len
-        a.q, a.ldq = self._mat("q", q, (t.bfloat16,), rows, self.width)
-        a.seq, a.pos = self._vec("seq", seq, t.int32, rows), self._vec("pos", pos, t.int32, rows)
-        a.depth = self._vec("depth", depth, t.int32, rows)
-        a.out, a.ldo = self._mat("out", out, (t.bfloat16,), rows, self.width)
-        rc = self.L.cdb_attention(self._ref, self._stream())
+            out = self._t.zeros(q.shape[0], self.width, dtype=self._t.bfloat16, device=q.device)
+        rc = self._call(self._fn, self._ref, self._stream(), self.dev, self.max_rows, q, seq, pos, depth, slot_base,
+                        shared_len, out)
         if rc != 0:
-            _fail(self.L, rc, "cdb_attention")
+            if rc is None:
+                t, rows = self._t, q.shape[0]
+                if rows > self.max_rows:
+                    raise ValueError(f"{rows} rows, the workspace holds {self.max_rows}")
+                self._mat("q", q, (t.bfloat16,), rows, self.width)
+                self._rows(rows, seq, pos, depth)
+                self._mat("out", out, (t.bfloat16,), rows, self.width)
+            self._fail(rc)
         return out
 
 

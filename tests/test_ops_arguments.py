@@ -129,3 +129,88 @@ def test_matrices_whose_rows_overlap_are_refused():
     for bad in (x[:1].expand(4, 32), x.as_strided((4, 32), (16, 1)), x.t(), x[0], x[:, ::2]):
         with pytest.raises(ValueError):
             op._mat("x", bad, (torch.float32,), bad.shape[0], bad.shape[-1])
+
+
+def on_cpu(cls, args, **attrs):
+    """An operator object whose device is the CPU; its argument structure is one that the C call refuses."""
+    op = object.__new__(cls)
+    import torch
+    op._t, op.L, op.dev, op.args = torch, ops._lib(), -1, args
+    op._device, op._raw_stream = lambda: -1, lambda dev: 0
+    for k, v in attrs.items():
+        setattr(op, k, v)
+    return op
+
+
+def test_sampler_checks_its_tensors():
+    import torch
+    op = on_cpu(ops.Sampler, ops.SampleArgs(vocab=64), max_rows=8, vocab=64)  # no output: refused
+    op._bind("cdb_sample", "sample")
+    f, i = torch.zeros(8), torch.zeros(8, dtype=torch.int32)
+    x = torch.zeros(8, 80)[:, :64]
+    for logits in (x, x.bfloat16(), x[:5], x[7:]):
+        with pytest.raises(ops.CdbError, match="are needed"):
+            op(logits, f, f, i, f, None)
+        a = op.args
+        assert (a.rows, a.logits, a.ld) == (logits.shape[0], logits.data_ptr(), max(logits.stride(0), 64))
+        assert a.dtype == (logits.dtype is torch.bfloat16)
+        assert (a.u, a.temperature, a.top_k, a.top_p, a.min_p) == (f.data_ptr(),) * 2 + (i.data_ptr(), f.data_ptr(), None)
+    for bad in (x[:, :63], torch.zeros(9, 64), x.half(), x[0], x[:1].expand(4, 64), x.t().contiguous().t(), torch.zeros(8, 65)):
+        with pytest.raises(ValueError):
+            op(bad, f, f)
+    for bad in (f[:7], f.double(), f.repeat(2)[::2], i, None):
+        for args in ((bad, f), (f, bad), (f, f, i, bad) if bad is not None else (bad, f)):
+            with pytest.raises(ValueError):
+                op(x, *args)
+    for bad in (f, i[:3], i.long()):
+        with pytest.raises(ValueError):
+            op(x, f, f, bad)
+    with pytest.raises(ValueError):
+        op(torch._neg_view(x), f, f)
+    with pytest.raises((TypeError, AttributeError)):
+        op([1.0], f, f)
+
+
+def test_cache_operators_check_their_tensors():
+    import torch
+    cache = ops._CacheOp.__new__(ops._CacheOp)
+    cache.n_kv_heads, cache.head_dim = 4, 64
+    wr = on_cpu(ops.CacheWriter, write_args(eps=-1.0), cache=cache, width=512)  # refused behind the tensors' checks
+    at = on_cpu(ops.DecodeAttention, attention_args(workspace=None), cache=cache, width=512, max_rows=8)
+    wr._bind("cdb_cache_write", "cache_write")
+    at._bind("cdb_attention", "attention")
+    qkv, q, v = torch.zeros(8, 1032), torch.zeros(8, 520, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int32)
+    for n in (8, 5, 1):
+        with pytest.raises(ops.CdbError, match="eps"):
+            wr(qkv[:n], v, v, None, 3, q)
+        a = wr.args
+        assert (a.rows, a.qkv or 0, a.ldqkv, a.dtype) == (n, qkv[:n].data_ptr(), 1032, 0)
+        assert (a.seq, a.pos, a.depth, a.slot_base, a.q, a.ldq) == (v.data_ptr(), v.data_ptr(), None, 3, q.data_ptr(), 520)
+    for n in (8, 5, 1):
+        with pytest.raises(ops.CdbError, match="workspace"):
+            at(q[:n, :512], v, v, None, 0, 32, q)
+        a = at.args
+        assert (a.rows, a.q, a.ldq, a.seq, a.pos, a.depth) == (n, q.data_ptr(), 520, v.data_ptr(), v.data_ptr(), None)
+        assert (a.slot_base, a.shared_len, a.out, a.ldo) == (0, 32, q.data_ptr(), 520)
+    for bad in (qkv[:, :1023], qkv.double(), qkv[:1].expand(8, 1032), qkv[0], torch.zeros(1032, 8).t()):
+        with pytest.raises(ValueError):
+            wr(bad, v, v, q_out=q)
+    for bad in (q[:, :511], q.float(), q[:1].expand(8, 520), q[:7]):
+        with pytest.raises(ValueError):
+            wr(qkv, v, v, q_out=bad)
+        with pytest.raises(ValueError):
+            at(q, v, v, out=bad)
+    for bad in (q[:, :511], q.float(), q[:1].expand(8, 520), torch.zeros(9, 512, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            at(bad, v, v, out=torch.zeros(9, 512, dtype=torch.bfloat16))
+    for bad in (v[:7], v.long(), v.repeat(2)[::2], v.float()):
+        for args in ((bad, v), (v, bad), (v, v, bad)):
+            with pytest.raises(ValueError):
+                wr(qkv, *args, q_out=q)
+            with pytest.raises(ValueError):
+                at(q, *args, out=q)
+    with pytest.raises(ValueError, match="seq is needed"):
+        wr(qkv, None, v, q_out=q)
+    for call in (lambda: wr(qkv, v, v, None, 1 << 40, q), lambda: at(q, v, v, None, 0, 1 << 31, q)):
+        with pytest.raises(OverflowError):
+            call()
