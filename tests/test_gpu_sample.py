@@ -224,3 +224,21 @@ def test_replay_in_a_graph_and_side_stream():
     again = plain(x, u, t, top_p=p)
     torch.cuda.synchronize()
     assert torch.equal(out[0], again[0])
+
+
+@pytest.mark.parametrize("near", [1, 2, 127, 128, 129, 300])
+@pytest.mark.parametrize("vocab", [700, 20000])
+def test_many_logits_close_together(near, vocab):
+    """`near` logits a few ulps apart, some of them equal, behind a larger one: thresholds fall between and inside them."""
+    rng = np.random.default_rng(near * 7 + vocab)
+    rows = 16
+    x = rng.standard_normal((rows, vocab)) - 9
+    for i in range(rows):
+        at = rng.permutation(vocab)[:near + 1]
+        x[i, at[1:]] = 3.0 + rng.integers(0, max(1, near // 3), near) * 2.0 ** -21
+        x[i, at[0]] = 4.0
+    k = rng.integers(1, near + 2, rows)
+    k[::3] = 0
+    p = rng.uniform(0.1, 0.99, rows)
+    p[1::3] = 1.0
+    check(x, rng.random(rows), rng.uniform(0.5, 2.0, rows), k, p)
