@@ -15,12 +15,16 @@
 // chosen bin, until the bin holds exactly what is needed or a single value.
 // top_k counts, after the maxima of single threads have ruled out most of the
 // row.  top_p guesses its bin from counts and mean offsets and adds up the exact mass
-// above and in it, so each logit's exact weight is computed once.  Each CTA
+// above and in it, so each logit's exact weight is computed once; of bf16 rows in
+// one or two CTAs it counts every value by itself, and weighs values, not logits.  Each CTA
 // works on its slice in its own shared memory, all CTAs of the cluster then
 // read one another's histograms or sums (distributed shared memory) and come to
 // the same decision; two histogram buffers leave one cluster barrier per step.
 // What bounds it: the instructions of the weights (about 50 for each logit that
-// has mass) and, with few rows, the barriers.
+// has mass), shared atomics (some 20 cycles a warp) and, with few rows, the
+// barriers.  512 rows of 65536 bf16 logits (9.9 us of HBM traffic): argmax 22 us,
+// temperature alone 104, top_k 82, top_p 165, min_p 66; 64 rows of 49152 fp32: 5,
+// 18, 20, 33, 12; one row: 3.4, 9, 13, 22, 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -92,6 +96,7 @@ struct alignas(16) Shared {
   unsigned int found_bin, found_n;
   unsigned int lo, hi;
   unsigned int list_n;  // entries of this CTA's list
+  unsigned int small[4];  // by_value: mass of the values too small for a bin, 16 bits at a time
   float fmx[kWarps], fmn[kWarps];
   int fi[kWarps];
 };
@@ -216,6 +221,22 @@ struct Vec<__nv_bfloat16> {
     for (int i = 0; i < 4; ++i) x[i] = __hadd2(__hmax2(x[i], low), zero);
     const __nv_bfloat162 t = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
     return fmaxf(__low2float(t), __high2float(t));
+  }
+};
+
+// Bins of a histogram by value: bf16 has 128 values per sign and power of two, so
+// 15 powers of two have 3840 of them, in falling order 0..1919 for positive and
+// 1921..3840 for negative ones; those of smaller magnitude share bin 1920.
+struct ValueBins {
+  static constexpr int kSide = 15 * 128, kSmall = kSide, kAll = 4096;  // eight per thread
+  int low;  // smallest magnitude (15 bits) with a bin
+  __device__ __forceinline__ int bin(unsigned int bits) const {  // < 0 or >= kAll: none
+    const int d = (int)(bits & 0x7FFFu) - low;
+    if (d < 0) return kSmall;
+    return (bits & 0x8000u) ? (d < kSide ? kSmall + 1 + d : kAll) : kSide - 1 - d;
+  }
+  __device__ __forceinline__ unsigned int key(int b) const {  // b != kSmall
+    return b < kSide ? 0x8000u + low + (kSide - 1 - b) : 0x7FFFu - (low + b - kSmall - 1);
   }
 };
 
@@ -443,6 +464,122 @@ struct Row {
     return Keep{lo, (unsigned int)((need + each_w - 1) / each_w)};
   }
 
+  // Of v[0..7] of every thread: the sum before this thread's, and of all.
+  __device__ __forceinline__ unsigned long long scan8(const unsigned long long* v, unsigned long long* total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    unsigned long long inc = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inc += v[e];
+    const unsigned long long mine = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    __syncthreads();  // S.wm and S.found_* are free
+    if (lane == 31) S.wm[w] = inc;
+    if (threadIdx.x == 0) S.found_bin = ValueBins::kAll;
+    __syncthreads();
+    unsigned long long before = inc - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == w) before += all;
+      all += S.wm[i];
+    }
+    *total = all;
+    return before;
+  }
+  // bf16: the threshold of top_p among the logits that `keep` leaves, from one
+  // histogram with a bin per value, whose masses are counts times weights.  `zero`:
+  // logits at or below it have no mass.  False, and nothing done, where a threshold
+  // is among the values that share a bin or have none.  kept: the number that stay.
+  __device__ __forceinline__ bool by_value(float tp, float zero, const Weigher& wt, Keep& keep, unsigned int& kept) {
+    const int tid = threadIdx.x, lane = tid & 31, b = buf;
+    const float far = fmaxf(fabsf(m), fabsf(zero));  // no larger magnitude needs a bin
+    if (!(far < INFINITY)) return false;
+    const ValueBins vb{max((int)(__float_as_uint(far) >> 23) - 14, 1) << 7};
+    const int last = keep.r ? vb.bin(__float_as_uint(value(keep.t)) >> 16) : -1;  // bin of top_k's ties
+    if (last == ValueBins::kSmall) return false;
+    const float least = fmaxf(zero, value(keep.t));
+    clear(b, 4);
+    if (tid < 4) S.small[tid] = 0;
+    __syncthreads();
+    unsigned int* hist = S.hist[b][0];
+    each([&](float x) {
+      if (!(x > least)) return;
+      const int c = vb.bin(__float_as_uint(x) >> 16);
+      if (c >= ValueBins::kAll) return;
+      atomicAdd(&hist[c], 1u);
+      if (c == ValueBins::kSmall) {
+        const unsigned long long w = wt(x);
+        atomicAdd(&S.small[0], (unsigned int)w & 0xFFFFu);
+        atomicAdd(&S.small[1], (unsigned int)(w >> 16) & 0xFFFFu);
+        atomicAdd(&S.small[2], (unsigned int)(w >> 32));
+      }
+    });
+    cl.sync();
+    unsigned int c[8] = {};
+#pragma unroll 4
+    for (int i = 0; i < nc; ++i) {
+      const Shared* o = cl.map_shared_rank(&S, i);
+      const uint4 x = *reinterpret_cast<const uint4*>(&o->hist[b][0][8 * tid]), y = *reinterpret_cast<const uint4*>(&o->hist[b][0][8 * tid + 4]);
+      c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w, c[4] += y.x, c[5] += y.y, c[6] += y.z, c[7] += y.w;
+    }
+    buf ^= 1;
+    unsigned long long small = 0;
+    if (tid == ValueBins::kSmall / 8) {
+      for (int i = 0; i < nc; ++i) {
+        const unsigned int* o = cl.map_shared_rank(&S, i)->small;
+        small += o[0] + ((unsigned long long)o[1] << 16) + ((unsigned long long)o[2] << 32);
+      }
+    }
+    unsigned long long v[8], inc = 0;  // masses
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int bin = 8 * tid + e;
+      if (bin == last) c[e] = keep.r;
+      v[e] = c[e] == 0 ? 0ull : bin == ValueBins::kSmall ? small : wt(value(vb.key(bin))) * c[e];
+      inc += v[e];
+    }
+    const unsigned long long mine = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) S.wm[tid >> 5] = inc;
+    if (tid == 0) S.found_bin = ValueBins::kAll;
+    __syncthreads();
+    unsigned long long before = inc - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == tid >> 5) before += total;
+      total += S.wm[i];
+    }
+    const unsigned long long goal = max(mul_ceil(tp, total), 1ull);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (before < goal && goal <= before + v[e]) S.found_bin = 8 * tid + e, S.found_n = c[e], S.found_m = before;
+      before += v[e];
+    }
+    __syncthreads();
+    const int at = (int)S.found_bin;
+    if (at == ValueBins::kAll || at == ValueBins::kSmall) return false;
+    const unsigned int k = vb.key(at);
+    const unsigned long long w = wt(value(k));
+    const unsigned int r = (unsigned int)((goal - S.found_m + w - 1) / w);
+    keep = r == S.found_n && at != last ? Keep{k - 1, 0} : Keep{k, r};
+    unsigned int n = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n += 8 * tid + e <= at ? c[e] : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) S.wn[tid >> 5] = n;
+    __syncthreads();
+    kept = 0;
+    for (int i = 0; i < kWarps; ++i) kept += S.wn[i];
+    return true;
+  }
+
   // The threshold of the `need` largest logits; all of them, where there are no more above -inf.
   __device__ __forceinline__ Keep largest(unsigned int need, float lowest_own, const Weigher& wt) {
     const float top = m;
@@ -667,6 +804,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   Keep keep{0, 0};
   if (tk > 0 && tk < a.vocab) keep = R.largest((unsigned int)tk, mn, wt);
+  const float zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);  // logits below it have no mass
+  bool guess = tp < 1.f;
+  unsigned int kept = 0;  // logits that stay, where by_value() counted them
+  if constexpr (R_::kDrop == 16) {
+    // The histogram of all CTAs is 16 KB a CTA to each of them: up to two CTAs it is the quicker (512 rows of
+    // 65536 logits, top_p 165 us against 215, behind top_k 122 against 131), with eight the slower by half.
+    if (guess && nc <= 2) guess = !R.by_value(tp, zero, wt, keep, kept);
+  }
   // This warp's segment of the slice: the sums below go by it.
   const int seg = (nv / 32 + kWarps - 1) / kWarps * 32;
   const int s0 = min(nv, warp * seg), s1 = min(nv, s0 + seg);
@@ -675,37 +820,38 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned long long tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   unsigned long long sum = 0;             // this lane's kept mass above keys `counted`
   float counted = INFINITY;               // logits above it are in `sum` already
-  if (tp < 1.f) {
+  if (guess) {
     // A first guess of the bin, 1024 equal steps of the logits that have mass,
-    // from each bin's count and mean offset (its mass to 1e-4); then the exact
-    // mass above it, in it and below decides.
+    // from each bin's count and mean offset (its mass to 1e-4), in one word: 16 bits
+    // of count, 16 of the offsets' sum in 32nds (rounded up or down by lane, so that the
+    // roundings cancel; a bin of more than 2000 logits may get its mean wrong).  Then the exact mass above it, in it and
+    // below decides.
     const float step = (float)kBins / 31.5f * wt.ch;
     auto coarse = [&](float x) { return min(kBins - 1, (int)((mx - x) * step)); };
-    const float zero = mx - 31.75f * Tc - 1e-6f * fabsf(mx);
     const float least = fmaxf(zero, R.value(keep.t));  // above it is what top_k keeps whole and has mass
+    const float dither = ((float)(lane * 13 % 32) + 0.5f) / 32.f;
     const int b = R.buf;
-    R.clear(b, 2);
+    R.clear(b, 1);
     __syncthreads();
     R.each([&](float x) {
       if (!(x > least)) return;
       const float y = (mx - x) * step;
       const int c = min(kBins - 1, (int)y);
-      atomicAdd(&S.hist[b][0][c], 1u);
-      atomicAdd(&S.hist[b][1][c], (unsigned int)((y - (float)c) * 4096.f) & 0x1FFFu);
+      atomicAdd(&S.hist[b][0][c], 1u + ((unsigned int)fmaf(y - (float)c, 32.f, dither) << 16));
     });
     cl.sync();
     unsigned int hc[2] = {0, 0}, ho[2] = {0, 0};
 #pragma unroll 4
     for (int i = 0; i < nc; ++i) {
       const Shared* o = cl.map_shared_rank(&S, i);
-      const uint2 x = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]), y = *reinterpret_cast<const uint2*>(&o->hist[b][1][2 * tid]);
-      hc[0] += x.x, hc[1] += x.y, ho[0] += y.x, ho[1] += y.y;
+      const uint2 x = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]);
+      hc[0] += x.x & 0xFFFFu, hc[1] += x.y & 0xFFFFu, ho[0] += x.x >> 16, ho[1] += x.y >> 16;
     }
     R.buf ^= 1;
     float fv[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float mean = hc[e] ? (float)ho[e] / (4096.f * (float)hc[e]) : 0.f;
+      const float mean = hc[e] ? (float)ho[e] / (32.f * (float)hc[e]) : 0.f;
       fv[e] = (float)hc[e] * exp2f(-((float)(2 * tid + e) + mean) * (31.5f * 1.4426950408889634f / kBins));
     }
     float ft = fv[0] + fv[1];
@@ -792,7 +938,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   // The threshold as a value; a tie of it counts only if some of them stay.
   const float at = R.value(keep.t), least = fmaxf(cut, at), tie_x = keep.r ? at : NAN;
   unsigned int ties = 0;
-  if (dense && counted == INFINITY && !zero_u) {  // no threshold but the floor
+  if ((dense || kept > (unsigned int)a.vocab / 32) && counted == INFINITY && !zero_u) {  // many stay
+    if (keep.r) R.each_of(s0, s1, [&](float x) { ties += x == tie_x; });
     R.each_of(s0, s1, [&](float x) {
       const unsigned long long w = wt(x);
       sum += x > least && w >= floor_w ? w : 0ull;
