@@ -242,3 +242,25 @@ def test_many_logits_close_together(near, vocab):
     p = rng.uniform(0.1, 0.99, rows)
     p[1::3] = 1.0
     check(x, rng.random(rows), rng.uniform(0.5, 2.0, rows), k, p)
+
+
+@pytest.mark.parametrize("vocab", [3000, 24001])
+def test_bf16_rows_of_every_scale(vocab):
+    """Rows in one or two thread blocks; thresholds among positive, negative, tiny, zero, equal and huge logits."""
+    rng = np.random.default_rng(vocab)
+    rows = 160
+    x = rng.standard_normal((rows, vocab)) * 10.0 ** rng.uniform(-7, 4, (rows, 1))
+    x += np.where(rng.random((rows, 1)) < 0.3, 10.0 ** rng.uniform(-2, 3, (rows, 1)) * rng.choice([-1, 1], (rows, 1)), 0)
+    x[::7] = np.round(x[::7])
+    x[3::11, ::2] = 0.0
+    x[5::13, 1::3] = -np.inf
+    x[6::17] = -1.25
+    t = np.maximum(np.abs(x[np.isfinite(x).all(1)]).mean(), 1e-6) * 10.0 ** rng.uniform(-3, 1, rows)
+    s = np.where(np.isfinite(x), x, 0).std(1) + 1e-3
+    t = np.where(rng.random(rows) < 0.8, s * rng.uniform(0.1, 3, rows), t)
+    p = rng.uniform(0.02, 0.999, rows)
+    k = np.where(rng.random(rows) < 0.5, 0, rng.integers(1, 2 * vocab // 3, rows))
+    k[1::5] = rng.integers(1, 60, len(k[1::5]))
+    mp = np.where(rng.random(rows) < 0.8, 0, rng.uniform(0, 0.3, rows))
+    check(x, rng.random(rows), t, k, p, mp, bf16=True)
+    check(x[:, :vocab // 2], rng.random(rows), t, None, p, None, bf16=True, pad=3)
