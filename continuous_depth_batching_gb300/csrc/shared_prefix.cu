@@ -37,7 +37,7 @@
 //                   the largest value scale so far (fp16's range); q becomes
 //                   fp16, each row divided by a power of two.  (Scaled by the
 //                   converters instead, rounded to fp16: 163 us where this takes
-//                   129, 256 rows x 32/8 heads behind 16384 tokens: the
+//                   125 (bf16: 90), 256 rows x 32/8 heads behind 16384 tokens: the
 //                   converters then hold the others up.)
 // Waits and issues of one block cost a warp some 500 cycles (a commit about
 // 140, a wait 100), as much as the products themselves: hence two issuing warps,
