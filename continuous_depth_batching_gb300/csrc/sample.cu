@@ -22,9 +22,9 @@
 // the same decision; two histogram buffers leave one cluster barrier per step.
 // What bounds it: the instructions of the weights (about 50 for each logit that
 // has mass), shared atomics (some 20 cycles a warp) and, with few rows, the
-// barriers.  512 rows of 65536 bf16 logits (9.9 us of HBM traffic): argmax 22 us,
-// temperature alone 104, top_k 82, top_p 165, min_p 66; 64 rows of 49152 fp32: 5,
-// 18, 20, 33, 12; one row: 3.4, 9, 13, 22, 8.
+// barriers.  512 rows of 65536 bf16 logits (9.9 us of HBM traffic): argmax 21 us,
+// temperature alone 99, top_k 79, top_p 160, min_p 61; 64 rows of 49152 fp32: 5,
+// 17, 19, 32, 11; one row: 3.3, 9, 13, 20, 7.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -77,6 +77,7 @@ struct Note {
 struct Tail {
   unsigned long long mass, in, below;  // kept mass above the threshold value; top_p: mass above the bin, in it, below it
   unsigned int ties, cnt;       // entries equal to the threshold value; top_p: entries of the bin
+  float mn;                     // largest(): smallest logit above -inf
 };
 
 // Entries in place of a histogram: one CTA's, or the cluster's.
@@ -89,7 +90,7 @@ struct alignas(16) Shared {
   unsigned int hist[2][4][kBins];  // count, then the low, middle and high 16 bits of the masses
   uint4 tab[kTab];                 // 2^(-j/64): in units of 2^-44 (low, high word), in units of 2^-30
   Note note[kMaxCluster];
-  Tail tail[kMaxCluster];
+  Tail tail[2][kMaxCluster];  // in turn
   unsigned long long wm[kWarps], wi[kWarps], wb[kWarps];  // per-warp values of the scans and sums
   unsigned int wc[kWarps], wn[kWarps];
   unsigned long long found_m;
@@ -252,6 +253,14 @@ struct Row {
   float m;           // largest logit
   float own_max;     // largest logit this thread loaded
   int buf = 0;       // histogram buffer of the next step
+  int tbuf = 0;      // tails of the next step
+
+  // Barrier of the cluster; the shared memory of its CTA i.
+  __device__ __forceinline__ void sync() const {
+    if (nc > 1) cl.sync();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ Shared* peer(int i) const { return i == rank ? &S : cl.map_shared_rank(&S, i); }
 
   static __device__ __forceinline__ unsigned int key(float x) { return order_bits(x) >> kDrop; }
   static __device__ __forceinline__ float value(unsigned int k) {  // of a key
@@ -306,7 +315,8 @@ struct Row {
     if (tid == 0) S.found_bin = kBins;  // none
     __syncthreads();
     V before = inc - mine;
-    for (int i = 0; i < w; ++i) before += part[i];
+#pragma unroll
+    for (int i = 0; i < kWarps - 1; ++i) before += i < w ? part[i] : V(0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (before < need && before + v[e] >= need) {
@@ -326,7 +336,7 @@ struct Row {
     unsigned long long v[2] = {0, 0};
 #pragma unroll (BY_MASS ? 2 : 4)  // reads of another CTA's memory in flight
     for (int i = 0; i < nc; ++i) {
-      const Shared* o = cl.map_shared_rank(&S, i);
+      const Shared* o = peer(i);
       const uint2 a = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]);
       c[0] += a.x, c[1] += a.y;
       if constexpr (BY_MASS) {
@@ -386,10 +396,10 @@ struct Row {
       const unsigned int at = atomicAdd(&S.list_n, 1u);
       if (at < kList) own.key[at] = key(x), own.w[at] = w;
     });
-    cl.sync();
+    sync();
     unsigned int n[kMaxCluster], total = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i) n[i] = i < nc ? cl.map_shared_rank(&S, i)->list_n : 0;
+    for (int i = 0; i < kMaxCluster; ++i) n[i] = i < nc ? peer(i)->list_n : 0;
     int from = 0;
     unsigned int first = 0;  // the list that holds entry tid, and the entries before it
 #pragma unroll
@@ -401,7 +411,7 @@ struct Row {
     unsigned int k = 0;
     unsigned long long w = 0;
     if ((unsigned int)tid < total) {
-      const List* l = reinterpret_cast<const List*>(cl.map_shared_rank(&S, from)->hist[buf]);
+      const List* l = reinterpret_cast<const List*>(peer(from)->hist[buf]);
       k = l->key[tid - first], w = l->w[tid - first];
       all.key[tid] = k, all.w[tid] = w;
     }
@@ -449,7 +459,7 @@ struct Row {
           atomicAdd(&S.hist[b][0][bin], 1u);
         }
       });
-      cl.sync();
+      sync();
       find_bin<BY_MASS>(b, need);
       buf ^= 1;
       need -= S.found_m;
@@ -517,11 +527,11 @@ struct Row {
         atomicAdd(&S.small[2], (unsigned int)(w >> 32));
       }
     });
-    cl.sync();
+    sync();
     unsigned int c[8] = {};
 #pragma unroll 4
     for (int i = 0; i < nc; ++i) {
-      const Shared* o = cl.map_shared_rank(&S, i);
+      const Shared* o = peer(i);
       const uint4 x = *reinterpret_cast<const uint4*>(&o->hist[b][0][8 * tid]), y = *reinterpret_cast<const uint4*>(&o->hist[b][0][8 * tid + 4]);
       c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w, c[4] += y.x, c[5] += y.y, c[6] += y.z, c[7] += y.w;
     }
@@ -529,7 +539,7 @@ struct Row {
     unsigned long long small = 0;
     if (tid == ValueBins::kSmall / 8) {
       for (int i = 0; i < nc; ++i) {
-        const unsigned int* o = cl.map_shared_rank(&S, i)->small;
+        const unsigned int* o = peer(i)->small;
         small += o[0] + ((unsigned long long)o[1] << 16) + ((unsigned long long)o[2] << 32);
       }
     }
@@ -580,6 +590,45 @@ struct Row {
     return true;
   }
 
+  // Sums that each CTA tells the others (the values of all warps, added up); the
+  // returned records stay until the call after the next.  BIN: top_p's sums.
+  template <bool BIN>
+  __device__ __forceinline__ const Tail* tell(unsigned long long mass, unsigned long long in, unsigned long long below,
+                                              unsigned int ties, unsigned int cnt) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      if constexpr (BIN) {
+        in += __shfl_xor_sync(0xffffffffu, in, o);
+        below += __shfl_xor_sync(0xffffffffu, below, o);
+      }
+    }
+    if constexpr (BIN) cnt = __reduce_add_sync(0xffffffffu, cnt);
+    else ties = __reduce_add_sync(0xffffffffu, ties);
+    __syncthreads();  // S.wm and its neighbours are free
+    if (lane == 0) {
+      S.wm[warp] = mass;
+      if constexpr (BIN) S.wi[warp] = in, S.wb[warp] = below, S.wn[warp] = cnt;
+      else S.wc[warp] = ties;
+    }
+    __syncthreads();
+    if (tid < nc) {
+      Tail t = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        t.mass += S.wm[w];
+        if constexpr (BIN) t.in += S.wi[w], t.below += S.wb[w], t.cnt += S.wn[w];
+        else t.ties += S.wc[w];
+      }
+      peer(tid)->tail[tbuf][rank] = t;
+    }
+    sync();
+    const Tail* r = S.tail[tbuf];
+    tbuf ^= 1;
+    return r;
+  }
+
   // The threshold of the `need` largest logits; all of them, where there are no more above -inf.
   __device__ __forceinline__ Keep largest(unsigned int need, float lowest_own, const Weigher& wt) {
     const float top = m;
@@ -595,7 +644,7 @@ struct Row {
       clear(b, 1);
       __syncthreads();
       if (own_max > -INFINITY) atomicAdd(&S.hist[b][0][coarse(own_max)], 1u);
-      cl.sync();
+      sync();
       find_bin<false>(b, need);
       buf ^= 1;
       bound = (int)S.found_bin;
@@ -619,14 +668,14 @@ struct Row {
       if (tid < nc) {
         have = 0;
         for (int w = 0; w < kWarps; ++w) mn = fminf(mn, S.fmn[w]), have += S.wc[w];
-        Shared* o = cl.map_shared_rank(&S, tid);
-        o->tail[rank].ties = have;
-        o->note[rank].mn = mn;
+        Tail& t = peer(tid)->tail[tbuf][rank];
+        t.ties = have;
+        t.mn = mn;
       }
-      cl.sync();
+      sync();
       have = 0;
-      for (int i = 0; i < nc; ++i) mn = fminf(mn, S.note[i].mn), have += S.tail[i].ties;
-      cl.sync();  // S.tail is free again
+      for (int i = 0; i < nc; ++i) mn = fminf(mn, S.tail[tbuf][i].mn), have += S.tail[tbuf][i].ties;
+      tbuf ^= 1;
       if (need >= have) return Keep{0, 0};
       step = top > mn ? (float)kBins / (top - mn) : 0.f;
       bound = kBins - 1;
@@ -639,7 +688,7 @@ struct Row {
       const int c = coarse(x);
       if (c <= bound) atomicAdd(&S.hist[b][0][c], 1u);
     });
-    cl.sync();
+    sync();
     find_bin<false>(b, need);
     buf ^= 1;
     const int bin = (int)S.found_bin;
@@ -649,30 +698,6 @@ struct Row {
     return refine<false>(S.lo, S.hi, cnt, rest, wt);
   }
 };
-
-// Sums that each CTA tells the others (the values of all warps, added up).
-__device__ __forceinline__ void tell(cg::cluster_group& cl, Shared& S, int rank, int nc, unsigned long long mass,
-                                     unsigned long long in, unsigned long long below, unsigned int ties,
-                                     unsigned int cnt) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    in += __shfl_xor_sync(0xffffffffu, in, o);
-    below += __shfl_xor_sync(0xffffffffu, below, o);
-  }
-  ties = __reduce_add_sync(0xffffffffu, ties);
-  cnt = __reduce_add_sync(0xffffffffu, cnt);
-  __syncthreads();  // S.wm and its neighbours are free
-  if (lane == 0) S.wm[warp] = mass, S.wi[warp] = in, S.wb[warp] = below, S.wc[warp] = ties, S.wn[warp] = cnt;
-  __syncthreads();
-  if (tid < nc) {
-    Tail t = {};
-    for (int w = 0; w < kWarps; ++w) t.mass += S.wm[w], t.in += S.wi[w], t.below += S.wb[w], t.ties += S.wc[w], t.cnt += S.wn[w];
-    cl.map_shared_rank(&S, tid)->tail[rank] = t;
-  }
-  cl.sync();
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -686,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nc = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int row = blockIdx.x / nc;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  cl.barrier_arrive();  // waited for before the first access to another CTA's shared memory
+  if (nc > 1) cl.barrier_arrive();  // waited for before the first access to another CTA's shared memory
   if (tid < kTab) {
     const unsigned long long f = kExp2[tid];
     S.tab[tid] = make_uint4((unsigned int)f, (unsigned int)(f >> 32), (unsigned int)((f + (1u << 13)) >> 14), 0u);
@@ -703,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const SampleParams P = a.params[sl];
     out = (size_t)sl * a.cap + t;
     if (!P.on || a.forced[out] >= 0) {
-      cl.barrier_wait();
+      if (nc > 1) cl.barrier_wait();
       return;
     }
     T_ = P.temperature, tk = P.top_k, tp = P.top_p, mp = P.min_p, u = a.u[out];
@@ -716,10 +741,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int lo = min(a.vocab, rank * slice), n = min(a.vocab, lo + slice) - lo;
   const T* src = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.ld + lo;
 
+  const int nv = (n + 32 * E - 1) / (32 * E) * 32;  // whole warps of vectors, the last ones filled up with -inf
+  R_ R{S, cl, xs, nv, rank, nc};
+
   // One read of the row: NaN counts as -inf, -0 as 0 (so that equal logits have equal keys).
   float mx = -INFINITY;
   int fi = 0x7FFFFFFF;
-  const int nv = (n + 32 * E - 1) / (32 * E) * 32;  // whole warps of vectors, the last ones filled up with -inf
   const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
 #pragma unroll 4
   for (int i = tid; i < nv; i += kThreads) {
@@ -749,16 +776,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   if (lane == 0) S.fmx[warp] = mx, S.fmn[warp] = mn, S.fi[warp] = fi;
-  cl.barrier_wait();
+  if (nc > 1) cl.barrier_wait();
   __syncthreads();
   if (tid < nc) {  // thread i tells CTA i
     for (int w = 0; w < kWarps; ++w) {
       if (S.fmx[w] > mx || (S.fmx[w] == mx && S.fi[w] < fi)) mx = S.fmx[w], fi = S.fi[w];
       mn = fminf(mn, S.fmn[w]);
     }
-    cl.map_shared_rank(&S, tid)->note[rank] = Note{mx, mn, fi, 0};
+    R.peer(tid)->note[rank] = Note{mx, mn, fi, 0};
   }
-  cl.sync();
+  R.sync();
   mx = -INFINITY, mn = INFINITY, fi = 0x7FFFFFFF;
   for (int i = 0; i < nc; ++i) {
     const Note o = S.note[i];
@@ -773,7 +800,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     return;
   }
-  R_ R{S, cl, xs, nv, rank, nc};
   R.own_max = own_max;
   if (mx == INFINITY) {  // the +inf entries share the mass
     for (int i = tid; i < nv; i += kThreads) {
@@ -809,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned int kept = 0;  // logits that stay, where by_value() counted them
   if constexpr (R_::kDrop == 16) {
     // The histogram of all CTAs is 16 KB a CTA to each of them: up to two CTAs it is the quicker (512 rows of
-    // 65536 logits, top_p 165 us against 215, behind top_k 122 against 131), with eight the slower by half.
+    // 65536 logits, top_p 160 us against 208, behind top_k 117 against 126), with eight the slower by half.
     if (guess && nc <= 2) guess = !R.by_value(tp, zero, wt, keep, kept);
   }
   // This warp's segment of the slice: the sums below go by it.
@@ -839,11 +865,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int c = min(kBins - 1, (int)y);
       atomicAdd(&S.hist[b][0][c], 1u + ((unsigned int)fmaf(y - (float)c, 32.f, dither) << 16));
     });
-    cl.sync();
+    R.sync();
     unsigned int hc[2] = {0, 0}, ho[2] = {0, 0};
 #pragma unroll 4
     for (int i = 0; i < nc; ++i) {
-      const Shared* o = cl.map_shared_rank(&S, i);
+      const Shared* o = R.peer(i);
       const uint2 x = *reinterpret_cast<const uint2*>(&o->hist[b][0][2 * tid]);
       hc[0] += x.x & 0xFFFFu, hc[1] += x.y & 0xFFFFu, ho[0] += x.x >> 16, ho[1] += x.y >> 16;
     }
@@ -864,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float with_ties = ft + (float)tie_w * 0x1p-44f * (float)keep.r;
     R.template find<float>(fv, hc, fmaxf(fminf(tp * with_ties, 0.999998f * ft), 1e-30f));
     int bin = min((int)S.found_bin, kBins - 1);
+    bool moved = false;
     while (true) {
       unsigned long long above = 0, in = 0, below = 0;
       unsigned int cnt = 0;
@@ -884,11 +911,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (x > least) put(x, wt(x));
         });
       }
-      tell(cl, S, rank, nc, above, in, below, 0, cnt);
+      const Tail* tail = R.template tell<true>(above, in, below, 0, cnt);
       unsigned long long A = 0, B = 0, C = 0;
       cnt = 0;
-      for (int i = 0; i < nc; ++i) A += S.tail[i].mass, B += S.tail[i].in, C += S.tail[i].below, cnt += S.tail[i].cnt;
-      cl.sync();
+      for (int i = 0; i < nc; ++i) A += tail[i].mass, B += tail[i].in, C += tail[i].below, cnt += tail[i].cnt;
       unsigned long long need = mul_ceil(tp, A + B + C + tie_w * keep.r);
       if (need == 0) need = 1;
       if (need > A + B + C) {  // into the ties of top_k
@@ -905,7 +931,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         counted = R.value(hi);
         break;
       }
-      // Off (a border within the guess's rounding): the bin from exact masses.
+      // Off (a border within the guess's rounding): most often by one bin, else the bin from exact masses.
+      const int next = need <= A ? bin - 1 : bin + 1;
+      if (!moved && next >= 0 && next < kBins) {
+        moved = true;
+        bin = next;
+        continue;
+      }
       const int h = R.buf;
       R.clear(h, 4);
       __syncthreads();
@@ -913,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!(x > least)) return;
         if (const unsigned long long w = wt(x)) R.add_mass(h, coarse(x), w);
       });
-      cl.sync();
+      R.sync();
       R.template find_bin<true>(h, need);
       R.buf ^= 1;
       bin = min((int)S.found_bin, kBins - 1);
@@ -950,31 +982,44 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (x > least && x <= counted) sum += kept_weight(x);
     });
   }
-  tell(cl, S, rank, nc, sum, 0, 0, ties, 0);
+  const Tail* tail = R.template tell<false>(sum, 0, 0, ties, 0);
   // Ties and mass before this CTA and in total; a CTA's ties count while fewer than keep.r came before.
   unsigned long long total = 0, mine0 = 0;
   unsigned int tied = 0, mytied0 = 0;
   for (int i = 0; i < nc; ++i) {
     if (i == rank) mine0 = total, mytied0 = tied;
-    total += S.tail[i].mass + tie_w * min(S.tail[i].ties, keep.r - min(keep.r, tied));
-    tied += S.tail[i].ties;
+    total += tail[i].mass + tie_w * min(tail[i].ties, keep.r - min(keep.r, tied));
+    tied += tail[i].ties;
   }
   const float uc = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
   const unsigned long long goal = mul_floor(uc, total);  // the token's running mass is the first above goal
-  // The segment (warp w of this CTA) whose running mass passes goal.
-  unsigned long long before = mine0;
-  unsigned int tb = mytied0;
-  int hit = -1;
-  for (int w = 0; w < kWarps; ++w) {
-    const unsigned long long here = S.wm[w] + tie_w * min(S.wc[w], keep.r - min(keep.r, tb));
-    if (before <= goal && goal < before + here) {
-      hit = w;
-      break;
+  // Lane w of every warp: the mass and the ties before S.wm[w], S.wc[w], and what the former and its ties weigh.
+  unsigned long long before, here;
+  unsigned int tb;
+  auto running = [&](unsigned long long mass0, unsigned int ties0) {
+    const unsigned int tc = lane < kWarps ? S.wc[lane] : 0;
+    unsigned int ti = tc;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const unsigned int up = __shfl_up_sync(0xffffffffu, ti, o);
+      if (lane >= o) ti += up;
     }
-    before += here;
-    tb += S.wc[w];
-  }
+    tb = ties0 + ti - tc;
+    here = lane < kWarps ? S.wm[lane] + tie_w * min(tc, keep.r - min(keep.r, tb)) : 0;
+    unsigned long long inc = here;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    before = mass0 + inc - here;
+  };
+  // The segment (warp `hit` of this CTA) whose running mass passes goal.
+  running(mine0, mytied0);
+  const int hit = __ffs(__ballot_sync(0xffffffffu, lane < kWarps && before <= goal && goal < before + here)) - 1;
   if (hit >= 0) {  // uniform in this CTA; no other CTA of the cluster has it
+    const unsigned long long before0 = __shfl_sync(0xffffffffu, before, hit);
+    const unsigned int tb0 = __shfl_sync(0xffffffffu, tb, hit);
     // The segment again, cut into one run of vectors per warp.
     __syncthreads();  // S.wm and S.wc are read
     const int g0 = min(nv, hit * seg), g1 = min(nv, g0 + seg);
@@ -991,12 +1036,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     tt = __reduce_add_sync(0xffffffffu, tt);
     if (lane == 0) S.wm[warp] = s, S.wc[warp] = tt;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-      before += S.wm[w] + tie_w * min(S.wc[w], keep.r - min(keep.r, tb));
-      tb += S.wc[w];
-    }
-    const unsigned long long end = before + S.wm[warp] + tie_w * min(S.wc[warp], keep.r - min(keep.r, tb));
-    if (before <= goal && goal < end) {
+    running(before0, tb0);
+    before = __shfl_sync(0xffffffffu, before, warp);
+    here = __shfl_sync(0xffffffffu, here, warp);
+    tb = __shfl_sync(0xffffffffu, tb, warp);
+    if (before <= goal && goal < before + here) {
       for (int i0 = a0 * E; i0 < a1 * E; i0 += 32) {  // in index order, 32 entries at a time
         const int i = i0 + lane;
         const float x = i < a1 * E ? xs[i / E].get(i % E) : -INFINITY;
