@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned int kept = 0;  // logits that stay, where by_value() counted them
   if constexpr (R_::kDrop == 16) {
     // The histogram of all CTAs is 16 KB a CTA to each of them: up to two CTAs it is the quicker (512 rows of
-    // 65536 logits, top_p 160 us against 208, behind top_k 117 against 126), with eight the slower by half.
+    // 65536 logits, top_p 165 us against 215, behind top_k 122 against 131, when added), with eight the slower by half.
     if (guess && nc <= 2) guess = !R.by_value(tp, zero, wt, keep, kept);
   }
   // This warp's segment of the slice: the sums below go by it.
