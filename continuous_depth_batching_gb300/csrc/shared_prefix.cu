@@ -180,166 +180,173 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;  // >= 1
   const int npg = (k_hi - k_lo) / 16;
 
-  if (warp == 8 || warp == 11) {
-    // ---------------- producers ----------------
-    constexpr int kPage = 16 * HD * (Q8 ? 1 : 2);  // bytes of a page of one head, K or V
-    const int kv = warp == 8 ? 0 : 1;
-    const int base = first_sequence(a);
-    const int* bt = c.block_table + (size_t)max(base, 0) * c.max_blocks + k_lo / 16;
-    uint64_t pol;  // the prefix is read again by the other tiles and by the next steps
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-    if (kv == 0 && elect_one()) {
-      mbar_arrive_tx(qbar, (uint32_t)(G::NX * A.group * A.tile_rows * 128));
-      for (int x = 0; x < G::NX; ++x) tma_3d(su32(qs + x * G::QSLICE), &tmq, qbar, x * 64, kh * A.group, row0);
-    }
-    __syncwarp();
-    // The ring this warp fills: K or V slots, or its half of the code slots.
-    const int slots = Q8 ? G::NR : kv ? G::VS : G::KS;
-    uint64_t* full = Q8 ? raw_full : kv ? v_full : k_full;
-    uint64_t* empty = Q8 ? raw_empty : kv ? o_done : s_full;
-    const uint32_t ring = su32(smem + (Q8 ? G::OFF_RAW + kv * G::RAWKV : kv ? G::OFF_V : G::OFF_K));
-    bool ok = true;
-    int issued = 0, blk_l = -1, s = 0;
-    uint32_t parity = 1;  // of the slot's last use, from the second round on
-    for (int j = 0; j < nb; ++j) {
-      if ((j & 7) == 0) {  // table entries of the next eight blocks, one per lane
-        const int pg = 4 * j + lane;
-        blk_l = base >= 0 && pg < npg ? bt[pg] : -1;
-        if (base >= 0 && pg < npg && (blk_l < 0 || blk_l >= c.kv_blocks)) report(a.status, CDB_OPS_BAD_BLOCK), blk_l = -1;
-      }
-      int blk[4], n = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        blk[i] = __shfl_sync(0xffffffffu, blk_l, (j & 7) * 4 + i);
-        n += blk[i] >= 0;
-      }
-      if (j >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], parity)))) break;
-      if (elect_one()) {
-        mbar_arrive_tx(&full[s], (uint32_t)n * (kPage + (Q8 ? 64 : 0)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (blk[i] < 0) continue;
-          // Key rows before this head's page (V follows n_kv_heads pages after K).
-          const long long at = ((((long long)blk[i] * c.n_kv_slots + a.slot_base) * 2 + kv) * c.n_kv_heads + kh) * 16;
-          if constexpr (Q8) {
-            tma_2d(ring + s * G::RAW + i * kPage, &tmk, &full[s], 0, (int)at, pol);
-            bulk_1d(ring + s * G::RAW + (2 - kv) * G::RAWKV + (kv * kKeys + i * 16) * 4, c.scales + at, 64, &full[s]);
-          } else
-            tma_4d(ring + s * G::KVB + i * G::PAGE, &tmk, &full[s], 0, 0, 0, (int)(at / 8), pol);
-        }
+  // e4m3: registers from the other warpgroups to the softmax groups (128 each at launch), whose reads of scales
+  // then overlap.
+  static_assert(!Q8 || (G::THREADS == 512 && 256 * 184 + 256 * 72 <= 512 * 128), "registers of the launch");
+  if (warp >= 8) {
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 || warp == 11) {
+      // ---------------- producers ----------------
+      constexpr int kPage = 16 * HD * (Q8 ? 1 : 2);  // bytes of a page of one head, K or V
+      const int kv = warp == 8 ? 0 : 1;
+      const int base = first_sequence(a);
+      const int* bt = c.block_table + (size_t)max(base, 0) * c.max_blocks + k_lo / 16;
+      uint64_t pol;  // the prefix is read again by the other tiles and by the next steps
+      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+      if (kv == 0 && elect_one()) {
+        mbar_arrive_tx(qbar, (uint32_t)(G::NX * A.group * A.tile_rows * 128));
+        for (int x = 0; x < G::NX; ++x) tma_3d(su32(qs + x * G::QSLICE), &tmq, qbar, x * 64, kh * A.group, row0);
       }
       __syncwarp();
-      issued = j + 1;
-      if (++s == slots) s = 0, parity ^= 1;
-    }
-    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-    // Copies in flight land before the CTA may leave (at once when everything was used).
-    if (kv == 0) mbar_wait(qbar, 0);
-    for (int j = max(0, issued - slots); j < issued; ++j) mbar_wait(&full[j % slots], (j / slots) & 1);
-  } else if (warp == 9) {
-    // ---------------- scores ----------------
-    constexpr uint32_t id = idesc_16(!Q8, kRows, kKeys, false);
-    const uint64_t kd = desc_k(su32(smem + G::OFF_K), G::OCT);  // addresses in 16-byte units
-    bool ok = __all_sync(0xffffffffu, mbar_wait(q_ready, 0));
-    for (int i = 0; ok && i < nb; ++i) {
-      const int s = i % G::KS;
-      // Lane 1 waits for the product with the weights that the buffer held, block i - 3's; the others for K.
-      uint64_t* bar = &k_full[s];
-      uint32_t parity = (i / G::KS) & 1;
-      if (lane == 1 && i >= 3) bar = &o_done[(i - 3) % G::VS], parity = ((i - 3) / G::VS) & 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)))) break;
-      fence_after();
-      const uint64_t kb = kd + (uint32_t)(s * (G::KVB / 16));
-      const uint32_t d = tmem + G::S_COL + (i % 3) * kKeys;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ts(d, tmem + G::Q_COL + kk * 8, kb + ((kk / 4) * 1024 + (kk % 4) * 32) / 16, id, kk > 0 ? 1u : 0u);
-        commit(&s_full[s]);
-      }
-      __syncwarp();
-    }
-    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-    if (elect_one()) commit(&done[0]);  // every MMA issued above completes before TMEM is released
-    __syncwarp();
-    mbar_wait(&done[0], 0);
-  } else if (warp == 10) {
-    // ---------------- weights times values ----------------
-    constexpr uint32_t id = idesc_16(!Q8, kRows, HD, true);
-    const uint64_t vd = desc_mn(su32(smem + G::OFF_V), 1024, G::OCT);
-    bool ok = true;
-    for (int i = 0; i < nb; ++i) {
-      const int s = i % G::VS, g = i & 1, n = i >> 1;
-      const bool other = lane == 1;  // lane 1 waits for V, the others for the weights
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &v_full[s] : &p_full[i % 3], (other ? i / G::VS : i / 3) & 1)))) break;
-      fence_after();
-      const uint64_t vb = vd + (uint32_t)(s * (G::KVB / 16));
-      const uint32_t d = tmem + G::O_COL + g * HD, p = tmem + G::S_COL + (i % 3) * kKeys;
-      const int steps = npg - 4 * i;  // pages behind the chunk were not copied
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * G::PAGE) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
-        commit(&o_done[s]);
-      }
-      __syncwarp();
-    }
-    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-    if (elect_one()) commit(&done[1]);
-    __syncwarp();
-    mbar_wait(&done[1], 0);
-  } else if (warp >= 12) {
-    // ---------------- code converters (e4m3) ----------------
-    if constexpr (Q8) {
-      // Two warps for K, two for V.  8 codes to 16 bytes at a time: the lanes of a half warp (hd 64: a quarter)
-      // take a key's row, so loads and stores of a warp meet every bank once, and the addresses of one thread
-      // are a constant apart.
-      const int kv = warp >= 14 ? 1 : 0, tid = (threadIdx.x - 384) & 63;
-      constexpr int C = HD / 8, KI = 64 / C;  // 8-code pieces of a row, rows of one step
-      const int key = tid / C, p = tid % C;
-      const int slots = kv ? G::VS : G::KS;
-      uint64_t* full = kv ? v_full : k_full;
-      uint64_t* empty = kv ? o_done : s_full;
-      const uint32_t to = su32(smem + (kv ? G::OFF_V : G::OFF_K)) + (p / 8) * 1024;
+      // The ring this warp fills: K or V slots, or its half of the code slots.
+      const int slots = Q8 ? G::NR : kv ? G::VS : G::KS;
+      uint64_t* full = Q8 ? raw_full : kv ? v_full : k_full;
+      uint64_t* empty = Q8 ? raw_empty : kv ? o_done : s_full;
+      const uint32_t ring = su32(smem + (Q8 ? G::OFF_RAW + kv * G::RAWKV : kv ? G::OFF_V : G::OFF_K));
       bool ok = true;
+      int issued = 0, blk_l = -1, s = 0;
+      uint32_t parity = 1;  // of the slot's last use, from the second round on
       for (int j = 0; j < nb; ++j) {
-        const int s = j % slots, r = j % G::NR;
-        const bool other = lane == 1 && j >= slots;  // lane 1 waits for the slot, the others for the codes
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &empty[s] : &raw_full[r],
-                                                     other ? ((j / slots) - 1) & 1 : (j / G::NR) & 1))))
-          break;
-        const uint8_t* raw = smem + G::OFF_RAW + (size_t)r * G::RAW;
-        const uint8_t* src = raw + kv * G::RAWKV + key * HD + p * 8;
-        uint2 w[kKeys / KI];
-#pragma unroll
-        for (int u = 0; u < kKeys / KI; ++u) w[u] = *reinterpret_cast<const uint2*>(src + u * KI * HD);
-        if (kv) {
-          // The scales move along: the code block is given back before the softmax group reads them.
-          float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + s * G::SCN;
-          const float* f = reinterpret_cast<const float*>(raw + 2 * G::RAWKV);
-          const float fv = f[kKeys + tid];
-          sc[tid] = f[tid];
-          sc[kKeys + tid] = fv;
-          // The largest of the value scales that were copied, by halves (as integers: none is negative).
-          const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fv) : 0u);
-          if (lane == 0) sc[2 * kKeys + tid / 32] = __uint_as_float(fm);
+        if ((j & 7) == 0) {  // table entries of the next eight blocks, one per lane
+          const int pg = 4 * j + lane;
+          blk_l = base >= 0 && pg < npg ? bt[pg] : -1;
+          if (base >= 0 && pg < npg && (blk_l < 0 || blk_l >= c.kv_blocks)) report(a.status, CDB_OPS_BAD_BLOCK), blk_l = -1;
         }
-#pragma unroll
-        for (int u = 0; u < kKeys / KI; ++u) {
-          const int k = key + u * KI;
-          st_shared_v4(to + s * G::KVB + (k / 8) * G::OCT + (k % 8) * 128 + (((p % 8) ^ (k % 8)) << 4), widen(w[u].x),
-                       widen_hi(w[u].x), widen(w[u].y), widen_hi(w[u].y));
+        int blk[4], n = 0;
+  #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          blk[i] = __shfl_sync(0xffffffffu, blk_l, (j & 7) * 4 + i);
+          n += blk[i] >= 0;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (j >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], parity)))) break;
+        if (elect_one()) {
+          mbar_arrive_tx(&full[s], (uint32_t)n * (kPage + (Q8 ? 64 : 0)));
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (blk[i] < 0) continue;
+            // Key rows before this head's page (V follows n_kv_heads pages after K).
+            const long long at = ((((long long)blk[i] * c.n_kv_slots + a.slot_base) * 2 + kv) * c.n_kv_heads + kh) * 16;
+            if constexpr (Q8) {
+              tma_2d(ring + s * G::RAW + i * kPage, &tmk, &full[s], 0, (int)at, pol);
+              bulk_1d(ring + s * G::RAW + (2 - kv) * G::RAWKV + (kv * kKeys + i * 16) * 4, c.scales + at, 64, &full[s]);
+            } else
+              tma_4d(ring + s * G::KVB + i * G::PAGE, &tmk, &full[s], 0, 0, 0, (int)(at / 8), pol);
+          }
+        }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[s]);
-          mbar_arrive(&raw_empty[r]);
-        }
+        issued = j + 1;
+        if (++s == slots) s = 0, parity ^= 1;
       }
       if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+      // Copies in flight land before the CTA may leave (at once when everything was used).
+      if (kv == 0) mbar_wait(qbar, 0);
+      for (int j = max(0, issued - slots); j < issued; ++j) mbar_wait(&full[j % slots], (j / slots) & 1);
+    } else if (warp == 9) {
+      // ---------------- scores ----------------
+      constexpr uint32_t id = idesc_16(!Q8, kRows, kKeys, false);
+      const uint64_t kd = desc_k(su32(smem + G::OFF_K), G::OCT);  // addresses in 16-byte units
+      bool ok = __all_sync(0xffffffffu, mbar_wait(q_ready, 0));
+      for (int i = 0; ok && i < nb; ++i) {
+        const int s = i % G::KS;
+        // Lane 1 waits for the product with the weights that the buffer held, block i - 3's; the others for K.
+        uint64_t* bar = &k_full[s];
+        uint32_t parity = (i / G::KS) & 1;
+        if (lane == 1 && i >= 3) bar = &o_done[(i - 3) % G::VS], parity = ((i - 3) / G::VS) & 1;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, parity)))) break;
+        fence_after();
+        const uint64_t kb = kd + (uint32_t)(s * (G::KVB / 16));
+        const uint32_t d = tmem + G::S_COL + (i % 3) * kKeys;
+        if (elect_one()) {
+  #pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_ts(d, tmem + G::Q_COL + kk * 8, kb + ((kk / 4) * 1024 + (kk % 4) * 32) / 16, id, kk > 0 ? 1u : 0u);
+          commit(&s_full[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+      if (elect_one()) commit(&done[0]);  // every MMA issued above completes before TMEM is released
+      __syncwarp();
+      mbar_wait(&done[0], 0);
+    } else if (warp == 10) {
+      // ---------------- weights times values ----------------
+      constexpr uint32_t id = idesc_16(!Q8, kRows, HD, true);
+      const uint64_t vd = desc_mn(su32(smem + G::OFF_V), 1024, G::OCT);
+      bool ok = true;
+      for (int i = 0; i < nb; ++i) {
+        const int s = i % G::VS, g = i & 1, n = i >> 1;
+        const bool other = lane == 1;  // lane 1 waits for V, the others for the weights
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &v_full[s] : &p_full[i % 3], (other ? i / G::VS : i / 3) & 1)))) break;
+        fence_after();
+        const uint64_t vb = vd + (uint32_t)(s * (G::KVB / 16));
+        const uint32_t d = tmem + G::O_COL + g * HD, p = tmem + G::S_COL + (i % 3) * kKeys;
+        const int steps = npg - 4 * i;  // pages behind the chunk were not copied
+        if (elect_one()) {
+  #pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * G::PAGE) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
+          commit(&o_done[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+      if (elect_one()) commit(&done[1]);
+      __syncwarp();
+      mbar_wait(&done[1], 0);
+    } else if (warp >= 12) {
+      // ---------------- code converters (e4m3) ----------------
+      if constexpr (Q8) {
+        // Two warps for K, two for V.  8 codes to 16 bytes at a time: the lanes of a half warp (hd 64: a quarter)
+        // take a key's row, so loads and stores of a warp meet every bank once, and the addresses of one thread
+        // are a constant apart.
+        const int kv = warp >= 14 ? 1 : 0, tid = (threadIdx.x - 384) & 63;
+        constexpr int C = HD / 8, KI = 64 / C;  // 8-code pieces of a row, rows of one step
+        const int key = tid / C, p = tid % C;
+        const int slots = kv ? G::VS : G::KS;
+        uint64_t* full = kv ? v_full : k_full;
+        uint64_t* empty = kv ? o_done : s_full;
+        const uint32_t to = su32(smem + (kv ? G::OFF_V : G::OFF_K)) + (p / 8) * 1024;
+        bool ok = true;
+        for (int j = 0; j < nb; ++j) {
+          const int s = j % slots, r = j % G::NR;
+          const bool other = lane == 1 && j >= slots;  // lane 1 waits for the slot, the others for the codes
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &empty[s] : &raw_full[r],
+                                                       other ? ((j / slots) - 1) & 1 : (j / G::NR) & 1))))
+            break;
+          const uint8_t* raw = smem + G::OFF_RAW + (size_t)r * G::RAW;
+          const uint8_t* src = raw + kv * G::RAWKV + key * HD + p * 8;
+          uint2 w[kKeys / KI];
+  #pragma unroll
+          for (int u = 0; u < kKeys / KI; ++u) w[u] = *reinterpret_cast<const uint2*>(src + u * KI * HD);
+          if (kv) {
+            // The scales move along: the code block is given back before the softmax group reads them.
+            float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + s * G::SCN;
+            const float* f = reinterpret_cast<const float*>(raw + 2 * G::RAWKV);
+            const float fv = f[kKeys + tid];
+            sc[tid] = f[tid];
+            sc[kKeys + tid] = fv;
+            // The largest of the value scales that were copied, by halves (as integers: none is negative).
+            const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fv) : 0u);
+            if (lane == 0) sc[2 * kKeys + tid / 32] = __uint_as_float(fm);
+          }
+  #pragma unroll
+          for (int u = 0; u < kKeys / KI; ++u) {
+            const int k = key + u * KI;
+            st_shared_v4(to + s * G::KVB + (k / 8) * G::OCT + (k % 8) * 128 + (((p % 8) ^ (k % 8)) << 4), widen(w[u].x),
+                         widen_hi(w[u].x), widen(w[u].y), widen_hi(w[u].y));
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[s]);
+            mbar_arrive(&raw_empty[r]);
+          }
+        }
+        if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+      }
     }
   } else {
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---------------- softmax groups ----------------
     const int q4 = warp & 3, g = warp >> 2;
     const int r = q4 * 32 + lane;
@@ -401,11 +408,15 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     int n = 0;  // blocks of this group so far
     for (int i = g; ok && i < nb; i += 2, ++n) {
-      // Lane 1 waits for the scales too (e4m3), which come with V.
-      const bool other = Q8 && lane == 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1) &&
-                                             (!other || mbar_wait(&v_full[i % G::VS], (i / G::VS) & 1)))))
-        break;
+      // e4m3: the scales of the block's keys, which come with V, before its scores; those of its values below.
+      float4 sf[Q8 ? 16 : 1];
+      const uint32_t scales = su32(smem + G::OFF_SC + (i % G::VS) * G::SCN * 4);
+      if constexpr (Q8) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % G::VS], (i / G::VS) & 1)))) break;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sf[k] = ld_shared_v4(scales + k * 16);
+      }
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1)))) break;
       fence_after();
       const uint32_t ts = trow + G::S_COL + (i % 3) * kKeys;
       float sv[64];
@@ -415,17 +426,18 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
       }
-      const float4* ks = nullptr;  // scales of the block's keys, then of its values
       float vmax = 0.f;
       if constexpr (Q8) {
-        ks = reinterpret_cast<const float4*>(smem + G::OFF_SC + (i % G::VS) * G::SCN * 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 4; ++k) {
-          const float4 f = ks[k];
+          const float4 f = sf[k];
           unpair(mul2(pair(sv[4 * k], sv[4 * k + 1]), pair(f.x, f.y)), sv[4 * k], sv[4 * k + 1]);
           unpair(mul2(pair(sv[4 * k + 2], sv[4 * k + 3]), pair(f.z, f.w)), sv[4 * k + 2], sv[4 * k + 3]);
         }
-        vmax = fmaxf(ks[kKeys / 2].x, ks[kKeys / 2].y);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sf[k] = ld_shared_v4(scales + 256 + k * 16);
+        const float4 f = ld_shared_v4(scales + 512);
+        vmax = fmaxf(f.x, f.y);
       }
       const int left = lim - i * kKeys;  // keys 0..left of the block are this row's
       if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
@@ -475,7 +487,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         l2[0] = add2(l2[0], pair(x0, x1));
         l2[1] = add2(l2[1], pair(x2, x3));
         if constexpr (Q8) {
-          const float4 f = ks[kKeys / 4 + e / 2];
+          const float4 f = sf[e / 2];
           // Keys behind the chunk may have any scale, NaN too, but their pages are not multiplied.
           unpair(mul2(pair(f.x, f.y), pair(x0, x1)), x0, x1);
           unpair(mul2(pair(f.z, f.w), pair(x2, x3)), x2, x3);
