@@ -35,9 +35,9 @@
 //                   would take four instructions).  A key's scale multiplies
 //                   its fp32 score, a value's scale its weight, relative to
 //                   the largest value scale so far (fp16's range); q becomes
-//                   fp16, each row divided by a power of two.  (Scaled by the
-//                   converters instead, rounded to fp16: 163 us where this takes
-//                   125 (bf16: 90), 256 rows x 32/8 heads behind 16384 tokens: the
+//                   fp16, each row divided by a power of two.  (Values scaled by
+//                   the converters instead, rounded to fp16: 168 us where this
+//                   took 125, 256 rows x 32/8 heads behind 16384 tokens: the
 //                   converters then hold the others up.)
 // Waits and issues of one block cost a warp some 500 cycles (a commit about
 // 140, a wait 100), as much as the products themselves: hence two issuing warps,
@@ -180,8 +180,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;  // >= 1
   const int npg = (k_hi - k_lo) / 16;
 
-  // e4m3: registers from the other warpgroups to the softmax groups (128 each at launch), whose reads of scales
-  // then overlap.
+  // e4m3: registers from the other warpgroups to the softmax groups (128 each at launch), which read the scales of
+  // a block's keys before its scores and those of its values before they are wanted: read where they are used, one
+  // read waits for another (256 rows x 32/8 heads behind 16384 tokens: 125 us, 108 so; bf16: 85).
   static_assert(!Q8 || (G::THREADS == 512 && 256 * 184 + 256 * 72 <= 512 * 128), "registers of the launch");
   if (warp >= 8) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
