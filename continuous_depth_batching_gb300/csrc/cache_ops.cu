@@ -400,8 +400,8 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
 }
 
 // Partials of a row of L keys.
-__device__ __forceinline__ int row_parts(int L, int first, int split, int wph) {
-  return L <= first ? 0 : (L - first + split - 1) / split * wph;
+__device__ __forceinline__ int row_parts(int L, int first, int split) {
+  return L <= first ? 0 : (L - first + split - 1) / split;
 }
 
 struct Args {
@@ -741,10 +741,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
   }
-  if (!ok) {
-    if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-    return;
-  }
+  if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);  // what follows is undefined, but in bounds
   // Sums over the keys; high and low weight parts of a narrow group added.
 #pragma unroll
   for (int e = 0; e < 2; ++e)
@@ -756,9 +753,42 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
   }
+  float fin = Q8 ? ref : 1.f;
+  if (A.wph > 1) {
+    // Below four KV heads: the warps of a head add up, in order, in the ring's memory (no copy is in flight once
+    // every warp is through its stages).
+    constexpr int N = G::NT * 4;
+    static_assert(kWarps * (N + 4) * 128 <= G::NS * G::STAGE, "exchange");
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    float* x = reinterpret_cast<float*>(smem) + lane;
+    if (sub > 0) {
+      float* w = x + warp * (N + 4) * 32;
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i * 32] = o[i / 4][i % 4] * fin;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) w[(N + e) * 32] = m[e], w[(N + 2 + e) * 32] = l[e];
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    if (sub > 0) return;
+    for (int s = 1; s < A.wph; ++s) {
+      const float* w = x + (s * A.hpc + hh) * (N + 4) * 32;
+      float f0[2], f1[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ms = w[(N + e) * 32], mj = fmaxf(m[e], ms);
+        f0[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - mj);
+        f1[e] = ms == -INFINITY ? 0.f : ex2(ms - mj);
+        m[e] = mj;
+        l[e] = l[e] * f0[e] + w[(N + 2 + e) * 32] * f1[e];
+        f0[e] *= fin;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i / 4][i % 4] = o[i / 4][i % 4] * f0[i % 2] + w[i * 32] * f1[i % 2];
+      fin = 1.f;
+    }
+  }
   if (!live) return;
-  const float fin = Q8 ? ref : 1.f;
-  const bool direct = A.chunks == 0 && row_parts(L, A.first, A.split, A.wph) <= 1;
+  const bool direct = A.chunks == 0 && row_parts(L, A.first, A.split) <= 1;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {  // query heads q0 + 2t, q0 + 2t + 1
     const int qi = 2 * t + e;
@@ -772,7 +802,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
             make_uint2(pack<false>(o[i / 2][e] * inv, o[i / 2][2 + e] * inv),
                        pack<false>(o[i / 2 + 1][e] * inv, o[i / 2 + 1][2 + e] * inv));
     } else {
-      const size_t pi = ((size_t)row * a.n_heads + q0 + qi) * A.parts + A.chunks + sp * A.wph + sub;
+      const size_t pi = ((size_t)row * a.n_heads + q0 + qi) * A.parts + A.chunks + sp;
       float* po = A.part_o + pi * HD;
 #pragma unroll
       for (int i = 0; i < HD / 8; i += 4)
@@ -822,7 +852,7 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   pdl_trigger();
   if (!live) return;
   const int L = pos + 1;
-  const int parts = A.chunks + row_parts(L, A.first, A.split, A.wph);
+  const int parts = A.chunks + row_parts(L, A.first, A.split);
   if (A.chunks == 0 && parts <= 1) return;  // written by the attention kernel
   const size_t pi = ((size_t)row * a.n_heads + h) * A.parts;
   const bool cols = 4 * lane < HD;
@@ -931,7 +961,11 @@ cudaError_t launch(cudaStream_t s, const Args& A, const SharedPlan& sh) {
 // Keys of a CTA: 128 per warp and head, 256 from four query heads per KV head
 // on, whose partials would else weigh more than 3% of the keys read (a partial
 // is head_dim + 2 floats per query head).  Below four KV heads the CTA's warps
-// share a head and take runs of its keys.  Nothing here looks at the batch, so
+// share a head, take runs of its keys and make one partial of them (123 rows of
+// 3 to 14 keys, 14/2 heads of 64: 5.5 us with a partial per warp and a join, 3.6
+// so; 128 rows of 100 to 8000, 8/1 heads, bf16: 54 and 50).  512 keys for one KV
+// head (1024: the latter 52 us, one row of 8000 keys 16 for 11), 512 for two (256:
+// 64 rows of 128 to 4096, 16/2 heads, bf16, 30 us for 27).  Nothing here looks at the batch, so
 // a row's bits do not depend on it.
 static AttnPlan attention_plan(int n_heads, int n_kv_heads, int max_ctx, int first) {
   AttnPlan p;
@@ -939,8 +973,8 @@ static AttnPlan attention_plan(int n_heads, int n_kv_heads, int max_ctx, int fir
   p.hpc = n_kv_heads >= 4 ? 4 : n_kv_heads >= 2 ? 2 : 1;
   p.warps_per_head = da::kWarps / p.hpc;
   p.qblocks = (group + 7) / 8;
-  p.split = (group >= 4 ? 256 : 128) * p.warps_per_head;
-  p.own_parts = (max_ctx - first + p.split - 1) / p.split * p.warps_per_head;
+  p.split = p.warps_per_head == 4 ? 512 : (group >= 4 ? 256 : 128) * p.warps_per_head;
+  p.own_parts = (max_ctx - first + p.split - 1) / p.split;
   return p;
 }
 

@@ -18,7 +18,7 @@ struct AttnPlan {
   int hpc;             // KV heads of one CTA
   int qblocks;         // groups of at most 8 query heads per KV head
   int split;           // keys of one CTA
-  int warps_per_head;  // partials of one CTA per head
+  int warps_per_head;  // of a CTA
   int own_parts;       // partials a row can have
 };
 // How a shared prefix is cut; chunks 0: it is not, every row reads it itself.
