@@ -457,10 +457,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int seq = a.seq[row];
+  const int seq = a.seq[row], pos = a.pos[row], depth = a.depth ? a.depth[row] : 0;  // one latency for all
   if (seq < 0) return;  // padding
-  const int pos = a.pos[row];
-  const int slot = a.slot_base + (a.depth ? a.depth[row] : 0);
+  const int slot = a.slot_base + depth;
   if (seq >= c.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= c.n_kv_slots) {
     if (threadIdx.x == 0 && sp == 0 && hg == 0)
       report(a.status, slot < 0 || slot >= c.n_kv_slots ? CDB_OPS_BAD_SLOT : CDB_OPS_BAD_ROW);
@@ -475,7 +474,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 
   if (warp == kWarps) {
     // ---------------- producer ----------------
-    const int* bt = c.block_table + (size_t)seq * c.max_blocks + (lo >> 4);
+    // The split's pages (at most 32), one per lane.
+    const int blk = lane < npg ? c.block_table[(size_t)seq * c.max_blocks + (lo >> 4) + lane] : -1;
+    const bool have = blk >= 0 && blk < c.kv_blocks;
+    if (lane < npg && !have) report(a.status, CDB_OPS_BAD_BLOCK);
+    const uint32_t pages = __ballot_sync(0xffffffffu, have);
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     const int heads = min(A.hpc, c.n_kv_heads - k0);
@@ -483,11 +486,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     int issued = 0;
     for (int st = 0; st < nst; ++st) {
       const int s = st % G::NS;
-      const int pg = st * pps + lane;
-      const int blk = lane < pps && pg < npg ? bt[pg] : -1;
-      const bool ok = blk >= 0 && blk < c.kv_blocks;
-      if (lane < pps && pg < npg && !ok) report(a.status, CDB_OPS_BAD_BLOCK);
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      const uint32_t mask = (pages >> (st * pps)) & ((1u << pps) - 1u);
       if (st >= G::NS && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((st / G::NS) - 1) & 1))) {
         fail = true;
         break;
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       }
       __syncwarp();
       for (int i = 0; i < pps; ++i) {
-        const int b = __shfl_sync(0xffffffffu, blk, i);
+        const int b = __shfl_sync(0xffffffffu, blk, st * pps + i);
         if (!((mask >> i) & 1u)) continue;
         if (elect_one()) {
           // Rows of head k0's page at this block and slot; V follows n_kv_heads pages later.
@@ -974,6 +973,7 @@ static AttnPlan attention_plan(int n_heads, int n_kv_heads, int max_ctx, int fir
   p.warps_per_head = da::kWarps / p.hpc;
   p.qblocks = (group + 7) / 8;
   p.split = p.warps_per_head == 4 ? 512 : (group >= 4 ? 256 : 128) * p.warps_per_head;
+  // At most 512: k_decode holds a split's 16-token pages in one warp.
   p.own_parts = (max_ctx - first + p.split - 1) / p.split;
   return p;
 }
