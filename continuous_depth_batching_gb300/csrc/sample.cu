@@ -22,9 +22,9 @@
 // the same decision; two histogram buffers leave one cluster barrier per step.
 // What bounds it: the instructions of the weights (about 50 for each logit that
 // has mass), shared atomics (some 20 cycles a warp) and, with few rows, the
-// barriers.  512 rows of 65536 bf16 logits (9.9 us of HBM traffic): argmax 21 us,
-// temperature alone 99, top_k 79, top_p 160, min_p 61; 64 rows of 49152 fp32: 5,
-// 17, 19, 32, 11; one row: 3.3, 9, 13, 20, 7.
+// barriers.  512 rows of 65536 bf16 logits (9.9 us of HBM traffic): argmax 22 us,
+// temperature alone 98, top_k 76, top_p 157, min_p 60; 64 rows of 49152 fp32: 5,
+// 16, 19, 30, 10; one row: 3.4, 8, 13, 18, 7.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -267,10 +267,12 @@ struct Row {
     return from_order((k << kDrop) | (kDrop && !(k & 0x8000u) ? 0xFFFFu : 0u));
   }
 
-  // Every logit of the slice, in no particular order.
+  // Every logit of the slice, in no particular order.  One vector a turn here and
+  // below: with two, fetching the longer code takes more than it saves (8 rows of
+  // 151936 bf16 logits, top_k and top_p: 33 us with two, 26 with one).
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
+#pragma unroll 1
     for (int i = threadIdx.x; i < nv; i += kThreads) {
       const Vec<T> v = xs[i];
 #pragma unroll
@@ -280,7 +282,7 @@ struct Row {
   // Vectors [v0, v1) by one warp.
   template <typename F>
   __device__ __forceinline__ void each_of(int v0, int v1, F f) const {
-#pragma unroll 2
+#pragma unroll 1
     for (int i = v0 + (threadIdx.x & 31); i < v1; i += 32) {
       const Vec<T> v = xs[i];
 #pragma unroll
