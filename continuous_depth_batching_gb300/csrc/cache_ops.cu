@@ -24,7 +24,7 @@ namespace cdb {
 // at most 24 KB of it, and its line of the rotation table into a three-stage
 // ring with bulk copies, so that lookups and loads run two rows ahead of the
 // arithmetic (one CTA per row, loading for itself, reached 3.8 TB/s where this
-// reaches 5.8, 8192 rows of 16 heads fp32 to e4m3).  Eight warps do the
+// reaches 5.4, 8192 rows of 16 heads fp32 to e4m3).  Eight warps do the
 // arithmetic: groups of GW lanes take one head at a time, 8 elements per lane,
 // four of the rotation's lower half and their four partners of the upper one
 // (or, behind rot_dim, 8 in a row), so a rotation stays in the lane and the
@@ -73,22 +73,37 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
 __device__ __forceinline__ uint2 pack4(const float* v) {
   return make_uint2(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]));
 }
-// Four e4m3 codes of v / s, inv the reciprocal of s: the quotients are corrected
-// by their remainders (to within an ulp of the division; a product with inv alone
-// would round twice and put more values on the other side of a code's border.
-// Carrying the roundings of norm and rotation along as well changed no more codes
-// and took 70 us where this takes 47, 8192 rows of 16 heads).
-__device__ __forceinline__ uint32_t code4(const float* v, float s, float inv) {
-  float q[4];
+// Eight e4m3 codes of v / (s + sl), inv the reciprocal of s, sl what rounding the
+// scale to s left.  The quotients are corrected by their remainders, to the nearest
+// fp32 number.  One that thereby lands halfway between two (normal) codes, the 20th
+// last bit set and none behind it, takes the side its remainder points to, so that
+// no value is rounded twice: of 34 million codes (8192 rows of 16 heads) some 28
+// differ from those of the formula in 64 bits, nearly all of them keys by norm and
+// rotation, where 40 would: 50 us, 47 without.  (Norm and rotation with their
+// roundings carried along took 70 and left as many.)
+__device__ __forceinline__ uint2 code8(const float* v, float s, float sl, float inv) {
+  float q[8];
+  uint32_t off = ~0u;  // 0 if one is halfway
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 8; ++e) {
     q[e] = v[e] * inv;
-    const float r = fmaf(-q[e], s, v[e]);
-    q[e] = fabsf(r) < INFINITY ? fmaf(r, inv, q[e]) : q[e];  // infinities and NaN as they came
+    const float r = fmaf(-q[e], sl, fmaf(-q[e], s, v[e]));
+    q[e] = fmaf(r, inv, q[e]);  // an infinite scale gives NaN codes: its products are NaN with any code
+    off = min(off, (__float_as_uint(q[e]) ^ 0x80000u) & 0xFFFFFu);
   }
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  if (off == 0u) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float left = fmaf(-q[e], sl, fmaf(-q[e], s, v[e]));
+      const uint32_t t = __float_as_uint(q[e]);
+      // Away from zero if the remainder has the quotient's sign.
+      if (left != 0.f && fabsf(left) < INFINITY && !(t & 0x7FFFFu)) q[e] = __uint_as_float((t - ((__float_as_uint(left) ^ t) >> 31)) | 1u);
+    }
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * e], q[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // unit_heads: heads of a part; parts: parts of a row.
@@ -237,11 +252,12 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
           for (int o = G::GW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o, G::GW));
           const float f = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f);
-          const float inv = __frcp_rn(f);
+          const float inv = __frcp_rn(f), fl = f > 0x1p-126f ? fmaf(-448.f, f, m) * (1.f / 448.f) : 0.f;
           uint8_t* dst = reinterpret_cast<uint8_t*>(c.pool) + at * HD;
           if (on) {
-            *reinterpret_cast<uint32_t*>(dst + e0) = code4(v, f, inv);
-            *reinterpret_cast<uint32_t*>(dst + e1) = code4(v + 4, f, inv);
+            const uint2 w = code8(v, f, fl, inv);
+            *reinterpret_cast<uint32_t*>(dst + e0) = w.x;
+            *reinterpret_cast<uint32_t*>(dst + e1) = w.y;
           }
           if (l == 0) c.scales[at] = f;
         } else if (on) {

@@ -98,7 +98,8 @@ typedef struct {
  *   rope[pos][j] (elements behind rot_dim are left);
  *   queries are rounded to bf16 into q; keys and values go to position pos of
  *   sequence seq, slot slot_base + depth: rounded to bf16, or as e4m3 with
- *   scale = max(max|x| / 448, 2^-126) and code = e4m3(x / scale).
+ *   scale = max(max|x| / 448, 2^-126) and code = e4m3(x / scale), the scale
+ *   rounded to float32 where it is stored but not in the quotient.
  * A row with seq < 0 is padding: nothing of it is read or written.  Two rows
  * of one call must not name the same position of the same sequence and slot. */
 typedef struct {
