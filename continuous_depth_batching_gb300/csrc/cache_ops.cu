@@ -96,8 +96,10 @@ __device__ __forceinline__ uint2 code8(const float* v, float s, float sl, float 
     for (int e = 0; e < 8; ++e) {
       const float left = fmaf(-q[e], sl, fmaf(-q[e], s, v[e]));
       const uint32_t t = __float_as_uint(q[e]);
-      // Away from zero if the remainder has the quotient's sign.
-      if (left != 0.f && fabsf(left) < INFINITY && !(t & 0x7FFFFu)) q[e] = __uint_as_float((t - ((__float_as_uint(left) ^ t) >> 31)) | 1u);
+      // Away from zero if the remainder has the quotient's sign.  A border (5 bits) times the largest magnitude
+      // differs from 448 v by 2^-34 of it or not at all; what is left of sl's rounding is below 2^-48.
+      if (fabsf(left) > 0x1p-40f * fabsf(v[e]) && fabsf(left) < INFINITY && !(t & 0x7FFFFu))
+        q[e] = __uint_as_float((t - ((__float_as_uint(left) ^ t) >> 31)) | 1u);
     }
   }
   uint32_t w[4];

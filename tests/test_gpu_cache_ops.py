@@ -660,3 +660,43 @@ def test_write_then_attend_in_a_graph():
     for i in range(rows):
         o, tol = expected(cs, i, hd ** -0.5)
         assert bool(((out[i].double().view(H, hd) - o).abs() <= tol).all())
+
+
+def test_value_codes_are_rounded_once():
+    """Codes of values (no norm, no rotation) equal the quotients' in 64 bits, also next to the borders between codes.
+
+    x 448 against a border times max|x| is exact in float64 (24 + 9 bits), and differs from it by 2^-34 of its value
+    at least, or not at all: far more than what the kernel's remainders are off by (2^-48).  Subnormal codes (|x| below
+    2^-6 of the scale) are off by at most one."""
+    import torch
+    from continuous_depth_batching_gb300 import ops
+    rows, hk, hd = 600, 2, 128
+    rng = np.random.default_rng(11)
+    table = torch.arange(rows // 16 + 1, dtype=torch.int32, device="cuda")[None].contiguous()
+    pool = torch.zeros(rows // 16 + 1, 1, 2, hk, 16, hd, dtype=torch.float8_e4m3fn, device="cuda")
+    c = ops.PagedCache(pool, table, torch.zeros(pool.shape[:-1], dtype=torch.float32, device="cuda"))
+    x = rng.standard_normal((rows, hk, hd)).astype(np.float32)
+    big = (np.abs(x).max(-1, keepdims=True) * rng.uniform(1, 2, (rows, hk, 1))).astype(np.float32)
+    border = (2 * rng.integers(8, 15, (rows, hk, hd)) + 1) * 2.0 ** rng.integers(-9, 4, (rows, hk, hd))  # 1.mmm1 in binary
+    near = (border * big.astype(np.float64) / 448).astype(np.float32)
+    near = np.nextafter(near, np.where(rng.random(near.shape) < 0.5, np.float32(0), np.float32(np.inf)), dtype=np.float32)
+    near = np.where(rng.random(near.shape) < 0.5, near, (border * big.astype(np.float64) / 448).astype(np.float32))
+    x = np.where(rng.random(x.shape) < 0.7, near * rng.choice([-1, 1], x.shape), x).astype(np.float32)
+    x[..., 5] = big[..., 0]  # the largest
+    x[::50, :, :] = np.round(x[::50] * 64) * 2.0 ** -6  # exact borders among them
+    x[::50, :, 5] = 7.0  # 448 / 64
+    x[::50] = np.clip(x[::50], -7, 7)
+    qkv = torch.zeros(rows, 3 * hk * hd, device="cuda")
+    qkv[:, 2 * hk * hd:] = torch.from_numpy(x.reshape(rows, -1)).cuda()
+    w = ops.CacheWriter(c, hk)
+    zero = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    w(qkv, zero, torch.arange(rows, dtype=torch.int32, device="cuda"))
+    w.check()
+    got = pool[:, 0, 1].permute(0, 2, 1, 3).reshape(-1, hk, hd)[:rows].double().cpu().numpy()
+    x = x.astype(np.float64)
+    z = x * 448 / np.abs(x).max(-1, keepdims=True)
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(z), 1e-30))), -6) - 3)
+    want = np.rint(z / step) * step
+    normal = np.abs(z) >= 2.0 ** -6
+    assert (got[normal] == want[normal]).all(), int((got != want)[normal].sum())
+    assert (np.abs(got - want)[~normal] <= 2.0 ** -9).all()
