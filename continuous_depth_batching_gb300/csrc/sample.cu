@@ -266,6 +266,9 @@ struct Row {
   static __device__ __forceinline__ float value(unsigned int k) {  // of a key
     return from_order((k << kDrop) | (kDrop && !(k & 0x8000u) ? 0xFFFFu : 0u));
   }
+  // The largest logit with a key <= k, for comparisons of logits against a border between keys.  No logit has the
+  // key of -0, but a border may: as a value it equals 0, whose key lies above it.
+  static __device__ __forceinline__ float at_most(unsigned int k) { return value(k == (0x7FFFFFFFu >> kDrop) ? k - 1 : k); }
 
   // Every logit of the slice, in no particular order.  One vector a turn here and
   // below: with two, fetching the longer code takes more than it saves (8 rows of
@@ -390,7 +393,7 @@ struct Row {
     List& all = *reinterpret_cast<List*>(S.hist[buf ^ 1]);
     if (tid == 0) S.list_n = 0;
     __syncthreads();
-    const float xlo = value(lo), xhi = value(hi);
+    const float xlo = value(lo), xhi = at_most(hi);
     each([&](float x) {
       if (x < xlo || x > xhi) return;
       const unsigned long long w = BY_MASS ? wt(x) : 1ull;
@@ -451,7 +454,7 @@ struct Row {
       const int b = buf;
       clear(b, BY_MASS ? 4 : 1);
       __syncthreads();
-      const float xlo = value(lo), xhi = value(hi);
+      const float xlo = value(lo), xhi = at_most(hi);
       each([&](float x) {
         if (x < xlo || x > xhi) return;
         const int bin = (int)((hi - key(x)) >> shift);
@@ -512,7 +515,7 @@ struct Row {
     const ValueBins vb{max((int)(__float_as_uint(far) >> 23) - 14, 1) << 7};
     const int last = keep.r ? vb.bin(__float_as_uint(value(keep.t)) >> 16) : -1;  // bin of top_k's ties
     if (last == ValueBins::kSmall) return false;
-    const float least = fmaxf(zero, value(keep.t));
+    const float least = fmaxf(zero, at_most(keep.t));
     clear(b, 4);
     if (tid < 4) S.small[tid] = 0;
     __syncthreads();
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // below decides.
     const float step = (float)kBins / 31.5f * wt.ch;
     auto coarse = [&](float x) { return min(kBins - 1, (int)((mx - x) * step)); };
-    const float least = fmaxf(zero, R.value(keep.t));  // above it is what top_k keeps whole and has mass
+    const float least = fmaxf(zero, R.at_most(keep.t));  // above it is what top_k keeps whole and has mass
     const float dither = ((float)(lane * 13 % 32) + 0.5f) / 32.f;
     const int b = R.buf;
     R.clear(b, 1);
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (need > A + B + C) {  // into the ties of top_k
         keep.r = min(keep.r, (unsigned int)((need - (A + B + C) + tie_w - 1) / tie_w));
         sum = above + in + below;
-        counted = R.value(keep.t);
+        counted = R.at_most(keep.t);
         break;
       }
       if (need > A && need <= A + B) {
@@ -930,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const unsigned int hi = S.hi;
         keep = R.template refine<true>(max(S.lo, keep.t + 1), hi, cnt, need - A, wt);
         sum = above;
-        counted = R.value(hi);
+        counted = R.at_most(hi);
         break;
       }
       // Off (a border within the guess's rounding): most often by one bin, else the bin from exact masses.
@@ -970,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // Kept mass of each warp's segment, in index order from warp to warp.
   // The threshold as a value; a tie of it counts only if some of them stay.
-  const float at = R.value(keep.t), least = fmaxf(cut, at), tie_x = keep.r ? at : NAN;
+  const float at = R.at_most(keep.t), least = fmaxf(cut, at), tie_x = keep.r ? at : NAN;
   unsigned int ties = 0;
   if ((dense || kept > (unsigned int)a.vocab / 32) && counted == INFINITY && !zero_u) {  // many stay
     if (keep.r) R.each_of(s0, s1, [&](float x) { ties += x == tie_x; });
