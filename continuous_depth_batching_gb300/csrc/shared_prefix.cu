@@ -515,7 +515,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     float2* xr = xch + 2 * kRows;  // e4m3: the groups' value scales
     xch[g * kRows + r] = make_float2(m, l);
     if (Q8 && r == 0) reinterpret_cast<float*>(xr)[g] = ref;
+    // Each group has waited for its own accumulator's last product; below it reads the other's too, which these
+    // fences order behind the other group's wait.
+    fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
+    fence_after();
     if (!ok) {
       if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     } else {
