@@ -335,8 +335,11 @@ cudaError_t launch_cache_write(cudaStream_t s, const cdb_cache_write_args& a) {
 // of the output columns is undone at the end); the pairs of keys that the MMA
 // wants side by side are made with byte permutes, for e4m3 before the codes are
 // widened to fp16 (exactly).  Codes are not scaled: a key's scale multiplies
-// its score, a value's scale its weight, relative to the largest value scale
-// seen so far so that weights stay within fp16's range.
+// its score, a value's scale its weight.  e4m3 weights are taken relative to the
+// largest weight times scale seen so far, not to the largest of either: a loud
+// value that has no weight and a sink whose value is near zero leave the others
+// their bits.  The sum of a key's two fp16 parts is within 2^-22 of its weight
+// times scale, or 2^-33 of the row's largest.
 // Partials (maximum, sum, unnormalised output) of the splits are joined in
 // split order by k_join; a row that fits one split is written directly.
 // ---------------------------------------------------------------------------
@@ -593,9 +596,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   float o[G::NT][4];
 #pragma unroll
   for (int j = 0; j < G::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  // Columns 2t, 2t + 1: reference maximum (log2, the same in the 8 lanes of a column), this lane's share of the sum.
+  // Columns 2t, 2t + 1: the reference that o and l are relative to (log2, the same in the 8 lanes of a column; bf16:
+  // the maximum score, within 8; e4m3: the maximum of score + log2(value scale), see below), this lane's share of the sum.
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float ref = 0x1p-126f, iref = 0x1p126f;  // value scale the weights are relative to (e4m3), its reciprocal
   constexpr int PW = G::KB / 16;           // pages of a warp per stage
   constexpr uint32_t kAll = PW == 1 ? 0xFFFFu : 0xffffffffu;
   bool ok = true;
@@ -662,51 +665,92 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
           for (int e = 0; e < 2; ++e)
             if (!((valid >> (16 * p + 8 * e + g)) & 1u)) sc[p][2 * e] = sc[p][2 * e + 1] = -INFINITY, vs[p][e] = 0.f;
       }
-      float mx[2] = {fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[0][1], sc[0][3])}, vmax = 0.f;
+      float mx[2] = {fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[0][1], sc[0][3])};
 #pragma unroll
       for (int p = 1; p < PW; ++p) {
         mx[0] = max3(mx[0], sc[p][0], sc[p][2]);
         mx[1] = max3(mx[1], sc[p][1], sc[p][3]);
       }
-      if constexpr (Q8) {
-#pragma unroll
-        for (int p = 0; p < PW; ++p) vmax = max3(vmax, vs[p][0], vs[p][1]);
-      }
-      // The reference maximum moves only when a score passes it by 2^8 (weights
-      // then reach 2^8), the reference value scale when one passes it by 2^6:
-      // fp16 weights stay below 2^14, and most stages rescale nothing.
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f || (Q8 && vmax > 64.f * ref))) {
+      float mm[2];
+      auto move = [&](const float* to) {  // to the references `to`
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-          const float mnew = mx[e] > m[e] + 8.f ? mx[e] : m[e];
-          f[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - mnew);
+          f[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - to[e]);
           l[e] *= f[e];
-          m[e] = mnew;
-        }
-        if constexpr (Q8) {
-          vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-          const float rnew = vmax > 64.f * ref ? vmax : ref;
-          f[0] *= ref / rnew, f[1] *= ref / rnew;
-          ref = rnew, iref = 1.f / rnew;
+          m[e] = to[e];
         }
 #pragma unroll
         for (int j = 0; j < G::NT; ++j) {
           o[j][0] *= f[0], o[j][1] *= f[1];
           o[j][2] *= f[0], o[j][3] *= f[1];
         }
+      };
+      auto offsets = [&] { mm[0] = m[0] == -INFINITY ? 0.f : m[0], mm[1] = m[1] == -INFINITY ? 0.f : m[1]; };
+      float w[PW][4], sum[2];  // e4m3: weights times value scales; the sums of the weights
+      if constexpr (Q8) {
+        // Weights times scales stay below 2^15.  Where one passes that, or at a column's first keys, the reference
+        // goes to the largest one / 2^8, so that the smallest step of fp16, 2^-24, is 2^-32 of it.  The weights'
+        // sum may be as far above as the scale of a zero value lets it, up to 2^107: no reference is further below a
+        // score.
+        float top[2];
+        auto weigh = [&] {
+          offsets();
+          top[0] = top[1] = sum[0] = sum[1] = 0.f;
+#pragma unroll
+          for (int p = 0; p < PW; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = ex2(sc[p][e] - mm[e & 1]);
+              sum[e & 1] += x;
+              w[p][e] = x * vs[p][e >> 1];
+              top[e & 1] = fmaxf(top[e & 1], fabsf(w[p][e]));
+            }
+        };
+        weigh();
+        if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > 0x1p15f || fmaxf(sum[0], sum[1]) > 0x1p100f ||
+                                        fminf(m[0], m[1]) == -INFINITY)) {
+          float to[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = mx[e] - 100.f;
+#pragma unroll
+            for (int p = 0; p < PW; ++p)
+              t = max3(t, sc[p][e] + (__log2f(fabsf(vs[p][0])) - 8.f), sc[p][2 + e] + (__log2f(fabsf(vs[p][1])) - 8.f));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+            to[e] = t > m[e] + 7.f ? t : m[e];
+          }
+          move(to);
+          weigh();
+        }
+        l[0] += sum[0], l[1] += sum[1];
+      } else {
+        // The reference maximum moves only when a score passes it by 2^8: most stages rescale nothing.
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+          float to[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+            to[e] = mx[e] > m[e] + 8.f ? mx[e] : m[e];
+          }
+          move(to);
+        }
+        offsets();
       }
-      const float mm[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
       uint32_t bh[PW][2], bl[PW][2];  // weights of keys 0..7, 8..15 of the page as B fragments
 #pragma unroll
       for (int p = 0; p < PW; ++p)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float p0 = ex2(sc[p][2 * e] - mm[0]), p1 = ex2(sc[p][2 * e + 1] - mm[1]);
-          l[0] += p0, l[1] += p1;
-          if constexpr (Q8) p0 *= vs[p][e] * iref, p1 *= vs[p][e] * iref;
+          float p0, p1;
+          if constexpr (Q8) {
+            p0 = w[p][2 * e], p1 = w[p][2 * e + 1];
+          } else {
+            p0 = ex2(sc[p][2 * e] - mm[0]), p1 = ex2(sc[p][2 * e + 1] - mm[1]);
+            l[0] += p0, l[1] += p1;
+          }
           const uint32_t high = pack<Q8>(p0, p1);
           const float2 back = unpack<Q8>(high);
           const uint32_t low = pack<Q8>(p0 - back.x, p1 - back.y);
@@ -770,7 +814,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
   }
-  float fin = Q8 ? ref : 1.f;
+  // e4m3: sums may lie far from 1.  With the power of two in them taken into the reference, partials are joined by
+  // what their rows weigh; fin is the factor for o.
+  float fin[2] = {1.f, 1.f};
+  if constexpr (Q8) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) fin[e] = unit_sum(m[e], l[e]);
+  }
   if (A.wph > 1) {
     // Below four KV heads: the warps of a head add up, in order, in the ring's memory (no copy is in flight once
     // every warp is through its stages).
@@ -781,7 +831,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     if (sub > 0) {
       float* w = x + warp * (N + 4) * 32;
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i * 32] = o[i / 4][i % 4] * fin;
+      for (int i = 0; i < N; ++i) w[i * 32] = o[i / 4][i % 4] * fin[i % 2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) w[(N + e) * 32] = m[e], w[(N + 2 + e) * 32] = l[e];
     }
@@ -797,11 +847,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         f1[e] = ms == -INFINITY ? 0.f : ex2(ms - mj);
         m[e] = mj;
         l[e] = l[e] * f0[e] + w[(N + 2 + e) * 32] * f1[e];
-        f0[e] *= fin;
+        f0[e] *= fin[e];
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i / 4][i % 4] = o[i / 4][i % 4] * f0[i % 2] + w[i * 32] * f1[i % 2];
-      fin = 1.f;
+      fin[0] = fin[1] = 1.f;
     }
   }
   if (!live) return;
@@ -811,7 +861,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     const int qi = 2 * t + e;
     if (qi >= nq || (!WIDE && t >= 2)) continue;
     if (direct) {
-      const float inv = l[e] > 0.f ? fin / l[e] : l[e] == 0.f ? 0.f : l[e];  // no keys: zeros; NaN stays
+      const float inv = l[e] > 0.f ? fin[e] / l[e] : l[e] == 0.f ? 0.f : l[e];  // no keys: zeros; NaN stays
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.ldo + (size_t)(q0 + qi) * HD;
 #pragma unroll
       for (int i = 0; i < HD / 8; i += 4)
@@ -824,7 +874,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 #pragma unroll
       for (int i = 0; i < HD / 8; i += 4)
         *reinterpret_cast<float4*>(po + G::v_elem(g, i)) =
-            make_float4(o[i / 2][e] * fin, o[i / 2][2 + e] * fin, o[i / 2 + 1][e] * fin, o[i / 2 + 1][2 + e] * fin);
+            make_float4(o[i / 2][e] * fin[e], o[i / 2][2 + e] * fin[e], o[i / 2 + 1][e] * fin[e], o[i / 2 + 1][2 + e] * fin[e]);
       if (g == 0) A.part_ml[pi] = make_float2(m[e], l[e]);
     }
   }

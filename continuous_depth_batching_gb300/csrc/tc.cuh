@@ -82,6 +82,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// A partial softmax: sum l against the reference m (log2).  Moves the power of two in l into m, so that l is in
+// [1, 2) (0, infinite and NaN sums stay), and returns what the partial's output has to be multiplied by.
+__device__ __forceinline__ float unit_sum(float& m, float& l) {
+  const uint32_t eb = __float_as_uint(l) >> 23;  // l >= 0: the biased exponent
+  if (eb < 1u || eb > 253u) return 1.f;
+  const float f = __uint_as_float((254u - eb) << 23);  // 2^(127 - eb)
+  m += (float)((int)eb - 127);
+  l *= f;
+  return f;
+}
 // Two fp32 numbers in one 64-bit register, added or multiplied by one instruction.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
