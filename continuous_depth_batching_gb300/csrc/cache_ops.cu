@@ -690,9 +690,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       float w[PW][4], sum[2];  // e4m3: weights times value scales; the sums of the weights
       if constexpr (Q8) {
         // Weights times scales stay below 2^15.  Where one passes that, or at a column's first keys, the reference
-        // goes to the largest one / 2^8, so that the smallest step of fp16, 2^-24, is 2^-32 of it.  The weights'
-        // sum may be as far above as the scale of a zero value lets it, up to 2^107: no reference is further below a
-        // score.
+        // goes to the largest one / 2^8, so that the smallest step of fp16, 2^-24, is 2^-32 of it.  A weight itself,
+        // that of a zero value say, may be as far above the reference as 2^97.
         float top[2];
         auto weigh = [&] {
           offsets();
@@ -713,7 +712,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
           float to[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = mx[e] - 100.f;
+            float t = mx[e] - 90.f;
 #pragma unroll
             for (int p = 0; p < PW; ++p)
               t = max3(t, sc[p][e] + (__log2f(fabsf(vs[p][0])) - 8.f), sc[p][2 + e] + (__log2f(fabsf(vs[p][1])) - 8.f));

@@ -33,8 +33,10 @@
 //   warps 12-15     e4m3 only: widen code blocks to fp16 in the MMA's swizzled
 //                   layout (exactly; one conversion per two codes, where bf16
 //                   would take four instructions).  A key's scale multiplies
-//                   its fp32 score, a value's scale its weight, relative to
-//                   the largest value scale so far (fp16's range); q becomes
+//                   its fp32 score, a value's scale its weight; weights are
+//                   relative to the largest weight times scale of their row,
+//                   as in k_decode, and one fp16 number (within 2^-11, or
+//                   2^-33 of that largest one); q becomes
 //                   fp16, each row divided by a power of two.  (Values scaled by
 //                   the converters instead, rounded to fp16: 168 us where this
 //                   took 125, 256 rows x 32/8 heads behind 16384 tokens: the
@@ -83,12 +85,12 @@ struct Geo {
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_V = OFF_K + KS * KVB;
   static constexpr int OFF_RAW = OFF_V + VS * KVB;
+  static constexpr int SCN = 2 * kKeys + 4;
   static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: [VS] scales of K, of V, and two maxima of V's
-  static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * (2 * kKeys + 4) * 4 : 0);  // float2 [2][kRows], float [2]
-  static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8 + 16;
+  static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * SCN * 4 : 0);  // float2 [2][kRows]
+  static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8;
   static constexpr int NBAR = 4 + 2 * KS + 2 * VS + 3 + 2 * 4;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
-  static constexpr int SCN = 2 * kKeys + 4;
   static constexpr int THREADS = 384 + (Q8 ? 128 : 0);
   static constexpr int O_COL = 0;                     // [2][HD]
   static constexpr int Q_COL = 2 * HD;                // head_dim / 2, two 16-bit elements per column
@@ -326,9 +328,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
             const float fv = f[kKeys + tid];
             sc[tid] = f[tid];
             sc[kKeys + tid] = fv;
-            // The largest of the value scales that were copied, by halves (as integers: none is negative).
-            const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fv) : 0u);
-            if (lane == 0) sc[2 * kKeys + tid / 32] = __uint_as_float(fm);
+            // The largest magnitude of the value scales that were copied, by halves: its logarithm, at least -82.
+            const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fabsf(fv)) : 0u);
+            if (lane == 0) sc[2 * kKeys + tid / 32] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
           }
   #pragma unroll
           for (int u = 0; u < kKeys / KI; ++u) {
@@ -363,9 +365,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     constexpr float kTau = 8.f;  // rescale O only when the row maximum grows by more than 2^8
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const uint32_t to = trow + G::O_COL + g * HD;
+    // What O and l are relative to (log2; bf16: the row's maximum score, within 8; e4m3: its maximum of score +
+    // log2(value scale), see k_decode), and the sum of the weights.
     float m = -INFINITY, l = 0.f;
-    float ref = 0x1p-60f, lref = -60.f;      // e4m3: value scale the weights are relative to, its logarithm
-    float up = 1.f;                          // e4m3: what q was divided by
+    float up = 1.f;  // e4m3: what q was divided by
     bool ok = true;
     {
       // q to TMEM, row by row (two 16-bit elements per column): the groups take a 64-element slice each.
@@ -409,100 +412,137 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     int n = 0;  // blocks of this group so far
     for (int i = g; ok && i < nb; i += 2, ++n) {
-      // e4m3: the scales of the block's keys, which come with V, before its scores; those of its values below.
-      float4 sf[Q8 ? 16 : 1];
-      const uint32_t scales = su32(smem + G::OFF_SC + (i % G::VS) * G::SCN * 4);
+      const uint32_t ts = trow + G::S_COL + (i % 3) * kKeys;
+      const int left = lim - i * kKeys;  // keys 0..left of the block are this row's
+      float sv[64];
+      uint32_t p[32];
+      auto mask = [&] {
+        if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) sv[k] = k <= left ? sv[k] : -INFINITY;
+        }
+      };
+      auto greatest = [&] {
+        float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 64; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x4[e] = max3(x4[e], sv[k + 2 * e], sv[k + 2 * e + 1]);
+        return fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale;
+      };
+      // Moves the row to the reference `to`; O holds the group's earlier blocks against the old one.
+      auto move = [&](float to_m) {
+        const float f = m == -INFINITY ? 0.f : ex2(m - to_m);
+        l *= f;
+        m = to_m;
+        if (n == 0) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(i - 2) % G::VS], ((i - 2) / G::VS) & 1))) return false;
+        fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 32) {
+          float v[32];
+          tmem_ld32(to + c0, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= f;
+          tmem_st32(to + c0, reinterpret_cast<const uint32_t*>(v));
+        }
+        return true;
+      };
       if constexpr (Q8) {
+        // The scales of the block's keys, which come with V, before its scores; those of its values below.
+        float4 sf[16];
+        const uint32_t scales = su32(smem + G::OFF_SC + (i % G::VS) * G::SCN * 4);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % G::VS], (i / G::VS) & 1)))) break;
 #pragma unroll
         for (int k = 0; k < 16; ++k) sf[k] = ld_shared_v4(scales + k * 16);
-      }
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1)))) break;
-      fence_after();
-      const uint32_t ts = trow + G::S_COL + (i % 3) * kKeys;
-      float sv[64];
-      tmem_ld32(ts, sv);
-      tmem_ld32(ts + 32, sv + 32);
-      if (turn_round) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1)))) break;
+        fence_after();
+        tmem_ld32(ts, sv);
+        tmem_ld32(ts + 32, sv + 32);
+        if (turn_round) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
-      }
-      float vmax = 0.f;
-      if constexpr (Q8) {
+          for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
+        }
 #pragma unroll
-        for (int k = 0; k < kKeys / 4; ++k) {
+        for (int k = 0; k < 16; ++k) {
           const float4 f = sf[k];
           unpair(mul2(pair(sv[4 * k], sv[4 * k + 1]), pair(f.x, f.y)), sv[4 * k], sv[4 * k + 1]);
           unpair(mul2(pair(sv[4 * k + 2], sv[4 * k + 3]), pair(f.z, f.w)), sv[4 * k + 2], sv[4 * k + 3]);
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) sf[k] = ld_shared_v4(scales + 256 + k * 16);
-        const float4 f = ld_shared_v4(scales + 512);
-        vmax = fmaxf(f.x, f.y);
-      }
-      const int left = lim - i * kKeys;  // keys 0..left of the block are this row's
-      if (!__all_sync(0xffffffffu, left >= kKeys - 1)) {
+        const float4 vm = ld_shared_v4(scales + 512);
+        mask();
+        // No weight times scale may pass 2^15 (fp16 ends at 2^16), no weight 2^97.  The largest score with the largest
+        // scale (2^-82 if that is less) bounds them; only where that passes, and so at a row's first keys, is the
+        // largest product looked for (for every block: 141 us where this takes 130, 256 rows x 32/8 heads behind
+        // 16384 tokens).
+        const float mx = greatest();
+        if (__any_sync(0xffffffffu, mx + fmaxf(vm.x, vm.y) > m + 15.f)) {
+          float t = mx - 90.f;
 #pragma unroll
-        for (int k = 0; k < 64; ++k) sv[k] = k <= left ? sv[k] : -INFINITY;
-      }
-      float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < 64; k += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x4[e] = max3(x4[e], sv[k + 2 * e], sv[k + 2 * e + 1]);
-      const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale;
-      const float mnew = mx > m + kTau ? mx : m;
-      const float rnew = Q8 && vmax > 64.f * ref ? vmax : ref;  // the same in every thread
-      if (__any_sync(0xffffffffu, mnew != m) || rnew != ref) {
-        const float f = m == -INFINITY ? 0.f : ex2(m - mnew);
-        l *= f;
-        m = mnew;
-        if (n > 0) {
-          // O holds the group's earlier blocks against the old maximum.
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[(i - 2) % G::VS], ((i - 2) / G::VS) & 1)))) break;
-          fence_after();
-          const float fo = Q8 ? f * (ref / rnew) : f;
-#pragma unroll 1
-          for (int c0 = 0; c0 < HD; c0 += 32) {
-            float v[32];
-            tmem_ld32(to + c0, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= fo;
-            tmem_st32(to + c0, reinterpret_cast<const uint32_t*>(v));
+          for (int k = 0; k < 16; ++k) {
+            const float4 f = sf[k];
+            t = max3(t, fmaf(sv[4 * k], scale, __log2f(fabsf(f.x)) - 8.f), fmaf(sv[4 * k + 1], scale, __log2f(fabsf(f.y)) - 8.f));
+            t = max3(t, fmaf(sv[4 * k + 2], scale, __log2f(fabsf(f.z)) - 8.f), fmaf(sv[4 * k + 3], scale, __log2f(fabsf(f.w)) - 8.f));
           }
+          t = t > m + 7.f ? t : m;
+          if (__any_sync(0xffffffffu, t != m) && !(ok = move(t))) break;
         }
-        if (Q8 && rnew != ref) ref = rnew, lref = log2f(rnew);
-      }
-      // e4m3: the weights come out of the exponential divided by ref (their sum is multiplied back; ref is at
-      // least 2^-60, so none overflows, and a weight that this flushes is no weight beside the maximum's).
-      const float mm = (m == -INFINITY ? 0.f : m) + (Q8 ? lref : 0.f);
-      uint32_t p[32];
-      const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
-      uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+        uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x0, x1, x2, x3;
-        unpair(fma2(pair(sv[2 * e], sv[2 * e + 1]), s2, m2), x0, x1);
-        unpair(fma2(pair(sv[2 * e + 2], sv[2 * e + 3]), s2, m2), x2, x3);
-        x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
-        l2[0] = add2(l2[0], pair(x0, x1));
-        l2[1] = add2(l2[1], pair(x2, x3));
-        if constexpr (Q8) {
-          const float4 f = sf[e / 2];
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1, x2, x3;
+          unpair(fma2(pair(sv[2 * e], sv[2 * e + 1]), s2, m2), x0, x1);
+          unpair(fma2(pair(sv[2 * e + 2], sv[2 * e + 3]), s2, m2), x2, x3);
+          x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+          l2[0] = add2(l2[0], pair(x0, x1));
+          l2[1] = add2(l2[1], pair(x2, x3));
           // Keys behind the chunk may have any scale, NaN too, but their pages are not multiplied.
+          const float4 f = sf[e / 2];
           unpair(mul2(pair(f.x, f.y), pair(x0, x1)), x0, x1);
           unpair(mul2(pair(f.z, f.w), pair(x2, x3)), x2, x3);
           p[e] = pack_f16(x0, x1);
           p[e + 1] = pack_f16(x2, x3);
-        } else {
+        }
+        float la, lb, lc, ld;
+        unpair(l2[0], la, lb);
+        unpair(l2[1], lc, ld);
+        l += (la + lb) + (lc + ld);
+      } else {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i % G::KS], (i / G::KS) & 1)))) break;
+        fence_after();
+        tmem_ld32(ts, sv);
+        tmem_ld32(ts + 32, sv + 32);
+        if (turn_round) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) sv[k] = -sv[k];
+        }
+        mask();
+        const float mx = greatest();
+        const float mnew = mx > m + kTau ? mx : m;
+        if (__any_sync(0xffffffffu, mnew != m) && !(ok = move(mnew))) break;
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+        uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1, x2, x3;
+          unpair(fma2(pair(sv[2 * e], sv[2 * e + 1]), s2, m2), x0, x1);
+          unpair(fma2(pair(sv[2 * e + 2], sv[2 * e + 3]), s2, m2), x2, x3);
+          x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+          l2[0] = add2(l2[0], pair(x0, x1));
+          l2[1] = add2(l2[1], pair(x2, x3));
           p[e] = pack_bf16(x0, x1);
           p[e + 1] = pack_bf16(x2, x3);
         }
+        float la, lb, lc, ld;
+        unpair(l2[0], la, lb);
+        unpair(l2[1], lc, ld);
+        l += (la + lb) + (lc + ld);
       }
-      float la, lb, lc, ld;
-      unpair(l2[0], la, lb);
-      unpair(l2[1], lc, ld);
-      l += ((la + lb) + (lc + ld)) * (Q8 ? ref : 1.f);
       tmem_st32(ts, p);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
@@ -512,9 +552,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     const int last = g + 2 * (n - 1);
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[last % G::VS], (last / G::VS) & 1));
     fence_after();
-    float2* xr = xch + 2 * kRows;  // e4m3: the groups' value scales
     xch[g * kRows + r] = make_float2(m, l);
-    if (Q8 && r == 0) reinterpret_cast<float*>(xr)[g] = ref;
     // Each group has waited for its own accumulator's last product; below it reads the other's too, which these
     // fences order behind the other group's wait.
     fence_before();
@@ -524,10 +562,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       if (lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     } else {
       // Join the groups; warps of group g write columns g HD/2 .. of the partial.
-      const float2 e0 = xch[r], e1 = xch[kRows + r];
+      float2 e0 = xch[r], e1 = xch[kRows + r];
+      const float r0 = Q8 ? unit_sum(e0.x, e0.y) : 1.f, r1 = Q8 ? unit_sum(e1.x, e1.y) : 1.f;
       const float mj = fmaxf(e0.x, e1.x);
       const float f0 = e0.x == -INFINITY ? 0.f : ex2(e0.x - mj), f1 = e1.x == -INFINITY ? 0.f : ex2(e1.x - mj);
-      const float r0 = Q8 ? reinterpret_cast<const float*>(xr)[0] : 1.f, r1 = Q8 ? reinterpret_cast<const float*>(xr)[1] : 1.f;
       const int h = kh * A.group + r % A.group;
       const size_t pi = ((size_t)br * a.n_heads + h) * A.parts + chunk;
       float* po = A.part_o + pi * HD + g * (HD / 2);

@@ -30,11 +30,11 @@ def bound(cs, row, scale):
     p = torch.softmax(torch.einsum("hd,lhd->hl", q, k) * scale, -1)
     w = p * vs.T
     o = torch.einsum("hl,lhd->hd", w, code)
-    mass = torch.einsum("hl,lhd->hd", w, code.abs())
+    mass = torch.einsum("hl,lhd->hd", w.abs(), code.abs())
     S = torch.einsum("hd,lhd->hl", q.abs(), k.abs()).amax(1, keepdim=True) * abs(scale)
     part = 2.0 ** -11 if cs["shared"] else 2.0 ** -22
     rel = 2 * (hd * 2.0 ** -23 * S + 2.0 ** -17 + 2.0 ** -22) + part + (16 + L / 16 + L / 64) * 2.0 ** -23
-    floor = 2.0 ** -33 * w.amax(1, keepdim=True) * code.abs().sum(0)
+    floor = 2.0 ** -33 * w.abs().amax(1, keepdim=True) * code.abs().sum(0)
     return o, 2.0 ** -8 * o.abs() + rel * mass + floor
 
 
@@ -127,3 +127,18 @@ KINDS = [loud, sink, far_sink, spread, climb, fall]
 @pytest.mark.parametrize("heads", [(4, 4, 64), (12, 2, 128), (6, 1, 96), (8, 4, 32), (20, 2, 64)])
 def test_own_keys(keys, heads):
     check(case(*heads, [1, 40, 130, 300, 700], 0, keys, seed=heads[0]))
+
+
+@pytest.mark.parametrize("keys", KINDS)
+@pytest.mark.parametrize("heads", [(4, 4, 64), (12, 2, 128), (20, 2, 64), (8, 8, 128)])
+def test_shared_prefix(keys, heads):
+    for shared, lengths in ((48, [1, 40, 3]), (720, [20, 1, 90, 2, 33])):
+        check(case(*heads, lengths, shared, keys, seed=heads[0] + shared))
+
+
+def test_negative_scales():
+    """A value's scale may be negative; its magnitude is what counts."""
+    for shared, heads in ((0, (12, 2, 128)), (320, (8, 4, 64))):
+        cs = case(*heads, [70, 20, 5], shared, climb, seed=3)
+        cs["cache"].scales[:, :, 1, :, ::3] *= -1
+        check(cs)
