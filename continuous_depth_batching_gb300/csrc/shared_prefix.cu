@@ -16,11 +16,13 @@
 // the other group is in its exponentials.  The two are joined at the end.
 //   warps 0-3, 4-7  softmax groups: thread t owns query row t (its TMEM lane);
 //                   it reads its 64 scores, and writes the weights back over
-//                   them in 16 bits (each rounded by at most 2^-8 of it in
-//                   bf16, less than the output's own rounding does to a sum;
-//                   the sum that normalises is of the fp32 weights): the
-//                   weights are the A operand of the second product straight
-//                   from TMEM;
+//                   them in 16 bits: the weights are the A operand of the
+//                   second product straight from TMEM.  bf16 weights are two
+//                   numbers, what the first one leaves in the second, which
+//                   take the space of the 64 scores and a product each: within
+//                   2^-17, as in the kernel for a row's own keys (256 rows x
+//                   32/8 heads behind 16384 tokens: 116 us, 112 with one; an
+//                   output's error then is its own rounding's alone);
 //   warps 8, 11     TMA producers: q tile and K blocks, V blocks.  A copy takes
 //                   its warp some 70 cycles to issue, so a page is one copy: a
 //                   4-dimensional box lays its 128-byte slices out as
@@ -29,7 +31,7 @@
 //                   from TMEM too (the softmax groups put it there): shared
 //                   memory has to feed K and V only, 64 KB a block with the
 //                   copies, where q would add 32;
-//   warp 10         issues O += P V;
+//   warp 10         issues O += P V, with a bf16 cache for both parts of P;
 //   warps 12-15     e4m3 only: widen code blocks to fp16 in the MMA's swizzled
 //                   layout (exactly; one conversion per two codes, where bf16
 //                   would take four instructions).  A key's scale multiplies
@@ -288,6 +290,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * G::PAGE) / 16, id, (n > 0 || kk > 0) ? 1u : 0u);
+          if constexpr (!Q8) {
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps) mma_ts(d, p + 32 + kk * 8, vb + (kk * G::PAGE) / 16, id, 1u);
+          }
           commit(&o_done[s]);
         }
         __syncwarp();
@@ -527,6 +534,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         const float mm = m == -INFINITY ? 0.f : m;
         const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
         uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        uint32_t low[32];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float x0, x1, x2, x3;
@@ -537,7 +545,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           l2[1] = add2(l2[1], pair(x2, x3));
           p[e] = pack_bf16(x0, x1);
           p[e + 1] = pack_bf16(x2, x3);
+          low[e] = bf16_rest(x0, x1, p[e]);
+          low[e + 1] = bf16_rest(x2, x3, p[e + 1]);
         }
+        tmem_st32(ts + 32, low);
         float la, lb, lc, ld;
         unpair(l2[0], la, lb);
         unpair(l2[1], lc, ld);

@@ -132,6 +132,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// What rounding lo and hi to the bf16 numbers of `packed` left of them, as bf16.
+__device__ __forceinline__ uint32_t bf16_rest(float lo, float hi, uint32_t packed) {
+  float a, b;
+  unpair(add2(pair(lo, hi), pair(-__uint_as_float(packed << 16), -__uint_as_float(packed & 0xFFFF0000u))), a, b);
+  return pack_bf16(a, b);
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
