@@ -957,10 +957,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     tie_w = keep.r ? wt(R.value(keep.t)) : 0ull;
   }
-  if (mp > 0.f) {
-    sum = 0, counted = INFINITY;  // some of it may fall below the floor
-    if (tie_w < floor_w) keep.r = 0;
-  }
   // With u = 0 the first kept token wins however small its mass: weights that
   // the fixed-point unit rounds to none count as one unit there.
   const bool zero_u = !(u > 0.f) && floor_w == 1;
@@ -970,6 +966,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (w >= floor_w) return w;
     return zero_u && (x - mx) * wt.ch > -700.f ? 1ull : 0ull;
   };
+  if (zero_u && keep.r) tie_w = kept_weight(R.value(keep.t));
+  if (mp > 0.f) {
+    sum = 0, counted = INFINITY;  // some of it may fall below the floor
+    if (tie_w < floor_w) keep.r = 0;
+  }
 
   // Kept mass of each warp's segment, in index order from warp to warp.
   // The threshold as a value; a tie of it counts only if some of them stay.

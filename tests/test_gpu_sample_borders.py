@@ -60,3 +60,21 @@ def test_thresholds_among_subnormal_logits(bf16):
     check(x, u, t, k=k + more, bf16=bf16)
     check(x, u, t, k=k + more, p=rng.uniform(0.5, 0.999, rows), bf16=bf16)
     check(x, u, t, p=rng.uniform(0.05, 0.7, rows), bf16=bf16)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("vocab", [700, 20000])
+def test_u_zero_takes_a_far_tie_of_top_k(vocab, bf16):
+    # The ties weigh e^-50 of the largest logit, far below the unit of the masses, and one of them is the first token kept.
+    rows = 8
+    x = np.full((rows, vocab), -200.0)
+    x[:, 5::7] = -50.0
+    x[:, [40, 300]] = 0.0
+    k = np.array([1, 2, 3, 4, 5, 40, 99, 102])  # the two largest, then ties
+    token = check(x, np.zeros(rows), np.ones(rows), k=k, bf16=bf16)
+    # Of 700 tokens 99 are ties (index 40, the 100th, holds one of the largest): the 102nd token kept is then one of -200, index 0.
+    assert list(token) == [40, 40] + [5] * 5 + [0 if vocab == 700 else 5]
+    check(x, np.full(rows, -1.0), np.ones(rows), k=k, p=np.full(rows, 1.0), bf16=bf16)
+    token = check(x, np.zeros(rows), np.full(rows, 0.05), k=k, bf16=bf16)  # e^-1000: no weight left
+    assert list(token) == [40] * 8
+    assert list(check(x, np.zeros(rows), np.ones(rows), k=k, mp=np.full(rows, 1e-9), bf16=bf16)) == [40] * 8
