@@ -961,10 +961,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the fixed-point unit rounds to none count as one unit there.
   const bool zero_u = !(u > 0.f) && floor_w == 1;
   if (zero_u) sum = 0, counted = INFINITY, cut = -INFINITY;
+  // min_p may lie below the unit too: its logarithm.
+  const float lowest = mp > 0.f ? logf(mp) : -INFINITY;
   auto kept_weight = [&](float x) {
     const unsigned long long w = wt(x);
     if (w >= floor_w) return w;
-    return zero_u && (x - mx) * wt.ch > -700.f ? 1ull : 0ull;
+    const float z = (x - mx) * wt.ch;
+    return zero_u && z > -700.f && z >= lowest ? 1ull : 0ull;
   };
   if (zero_u && keep.r) tie_w = kept_weight(R.value(keep.t));
   if (mp > 0.f) {

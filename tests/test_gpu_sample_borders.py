@@ -78,3 +78,19 @@ def test_u_zero_takes_a_far_tie_of_top_k(vocab, bf16):
     token = check(x, np.zeros(rows), np.full(rows, 0.05), k=k, bf16=bf16)  # e^-1000: no weight left
     assert list(token) == [40] * 8
     assert list(check(x, np.zeros(rows), np.ones(rows), k=k, mp=np.full(rows, 1e-9), bf16=bf16)) == [40] * 8
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_u_zero_keeps_to_a_tiny_min_p(bf16):
+    # min_p below the unit of the masses still rules out what weighs less: e^-60 < 1e-20 < e^-40.
+    rows = 5
+    x = np.full((rows, 3000), -60.0)
+    x[:, 100:200] = -40.0
+    x[:, 2000] = 0.0
+    mp = np.array([1e-20, 1e-30, 1e-10, 1e-44, 0.0])
+    token = check(x, np.zeros(rows), np.ones(rows), mp=mp, bf16=bf16)
+    assert list(token) == [100, 0, 2000, 0, 0]
+    # With top_k too, whose threshold is a tie.
+    token = check(x, np.zeros(rows), np.ones(rows), k=np.full(rows, 150), mp=mp, bf16=bf16)
+    assert list(token) == [100, 0, 2000, 0, 0]
+    check(x, np.full(rows, 0.5), np.ones(rows), mp=mp, bf16=bf16)
