@@ -5,8 +5,13 @@ For programs that drive the model themselves instead of through
 structure and the output buffers of its operator, and enqueues one call on the
 current CUDA stream; nothing synchronizes, and every call can be captured into
 a CUDA graph.  An object's default outputs and its workspace are overwritten by
-its next call, so one object serves one stream at a time.  An object works on
-the device that was current when it was made; no gradients are recorded.
+its next call, so one object serves one stream at a time.  It may be called on
+other streams than the one it was made on, and dropped while a call is in
+flight: its own memory (default outputs, status, workspace) waits for every
+stream that called it.  A graph that captured its calls needs the object for as
+long as it is replayed.  Tensors that the caller gives are the caller's to
+order and to keep.  An object works on the device that was current when it was
+made; no gradients are recorded.
 """
 
 from __future__ import annotations
@@ -85,12 +90,17 @@ def _tensor_calls():
 class _Op:
     """Shared argument checks; the device is the current one when the object is made."""
 
+    _at = 0  # handle of the last call's stream
+
     def __init__(self):
         import torch
         self._t = torch
         self.L = _lib()
         self.dev = torch.cuda.current_device()
         self._device, self._raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._streams = [torch.cuda.current_stream(self.dev)]  # the one it was made on, then others that called it
+        self._memory = []  # the object's own tensors
+        self._at = self._raw_stream(self.dev)
 
     def _bind(self, what, call):
         """The C entry point and the argument structure that self._call fills in."""
@@ -100,7 +110,23 @@ class _Op:
     def _stream(self):
         if self._device() != self.dev:
             raise ValueError(f"made on cuda:{self.dev}, the current device is cuda:{self._device()}")
-        return self._raw_stream(self.dev)
+        at = self._raw_stream(self.dev)
+        if at != self._at:
+            self._moved()
+            self._at = at
+        return at
+
+    def _moved(self):
+        """The first call on a stream: the object's memory is allocated and cleared on the stream it was made on."""
+        t = self._t
+        stream = t.cuda.current_stream(self.dev)
+        if stream in self._streams:
+            return
+        if not t.cuda.is_current_stream_capturing():  # a capture starts behind all work of the device
+            stream.wait_stream(self._streams[0])
+        for m in self._memory:
+            m.record_stream(stream)
+        self._streams.append(stream)
 
     def _fail(self, rc):
         if rc is None:
@@ -145,6 +171,7 @@ class Sampler(_Op):
         self.max_rows, self.vocab = int(max_rows), int(vocab)
         self.token = t.empty(self.max_rows, dtype=t.int32, device=f"cuda:{self.dev}")
         self.logprob = t.empty(self.max_rows, dtype=t.float32, device=f"cuda:{self.dev}")
+        self._memory += [self.token, self.logprob]
         self.args = SampleArgs(vocab=self.vocab, token=self.token.data_ptr(), logprob=self.logprob.data_ptr())
         self._bind("cdb_sample", "sample")
         self._out = self.token, self.logprob  # of the last number of rows
@@ -216,16 +243,22 @@ class _CacheOp(_Op):
         self.cache, self.n_heads = cache, int(n_heads)
         self.width = self.n_heads * cache.head_dim
         self.status = self._t.zeros(1, dtype=self._t.int32, device=cache.pool.device)
+        self._memory.append(self.status)
 
     def _rows(self, rows, seq, pos, depth):
         for name, v, needed in (("seq", seq, True), ("pos", pos, True), ("depth", depth, False)):
             self._vec(name, v, self._t.int32, rows, needed)
 
     def check(self):
-        """Wait for the device and raise if a call found an index out of range."""
+        """Wait for the object's calls, on whichever streams, and raise if one found an index out of range."""
+        now = self._t.cuda.current_stream(self.dev)
+        for s in self._streams:
+            if s != now:
+                now.wait_stream(s)
         st = int(self.status.item())
         if st:
             self.status.zero_()
+            now.synchronize()  # before the next call, on whichever stream
             raise CdbError(-5, "; ".join(v for k, v in STATUS.items() if st & k) or f"status {st}")
 
 
@@ -289,6 +322,7 @@ class DecodeAttention(_CacheOp):
                              f"{cache.n_kv_heads} KV heads of {hd}")
         t = self._t
         self.workspace = t.empty(n + 256, dtype=t.uint8, device=cache.pool.device)
+        self._memory.append(self.workspace)
         base = (self.workspace.data_ptr() + 255) // 256 * 256
         self.args = AttentionArgs(cache=cache.desc, n_heads=self.n_heads, scale=hd ** -0.5 if scale is None else scale,
                                   max_ctx=self.max_ctx, status=self.status.data_ptr(), workspace=base,
