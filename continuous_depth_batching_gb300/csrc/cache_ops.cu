@@ -15,6 +15,12 @@
 
 namespace cdb {
 
+// The slot of a row, -1 for one that the cache does not have.
+__device__ __forceinline__ int row_slot(const cdb_paged_cache& c, int base, int depth) {
+  const long long s = (long long)base + depth;
+  return s >= 0 && s < c.n_kv_slots ? (int)s : -1;
+}
+
 // ---------------------------------------------------------------------------
 // Cache write.
 //
@@ -145,14 +151,14 @@ __global__ void __launch_bounds__(kThreads, 3)
           const int seq = a.seq[row_l];
           if (seq >= 0) {
             pos_l = a.pos[row_l];
-            const int slot = a.slot_base + (a.depth ? a.depth[row_l] : 0);
+            const int slot = row_slot(c, a.slot_base, a.depth ? a.depth[row_l] : 0);
             if (seq >= c.n_seqs || pos_l < 0 || pos_l >= c.max_blocks * 16 || (a.rope && pos_l >= a.rope_positions)) {
               report(a.status, CDB_OPS_BAD_ROW);
             } else {
               const int blk = c.block_table[(size_t)seq * c.max_blocks + (pos_l >> 4)];
               if (blk < 0 || blk >= c.kv_blocks) {
                 report(a.status, CDB_OPS_BAD_BLOCK);
-              } else if (slot < 0 || slot >= c.n_kv_slots) {
+              } else if (slot < 0) {
                 report(a.status, CDB_OPS_BAD_SLOT);
               } else {
                 cell_l = ((long long)blk * c.n_kv_slots + slot) * 2 * Hk;
@@ -480,10 +486,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   pdl_trigger();
   const int seq = a.seq[row], pos = a.pos[row], depth = a.depth ? a.depth[row] : 0;  // one latency for all
   if (seq < 0) return;  // padding
-  const int slot = a.slot_base + depth;
-  if (seq >= c.n_seqs || pos >= a.max_ctx || slot < 0 || slot >= c.n_kv_slots) {
-    if (threadIdx.x == 0 && sp == 0 && hg == 0)
-      report(a.status, slot < 0 || slot >= c.n_kv_slots ? CDB_OPS_BAD_SLOT : CDB_OPS_BAD_ROW);
+  const int slot = row_slot(c, a.slot_base, depth);
+  if (seq >= c.n_seqs || pos >= a.max_ctx || slot < 0) {
+    if (threadIdx.x == 0 && sp == 0 && hg == 0) report(a.status, slot < 0 ? CDB_OPS_BAD_SLOT : CDB_OPS_BAD_ROW);
     return;
   }
   const int L = pos + 1;
@@ -897,8 +902,8 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Args A) {
   const int row = item / a.n_heads, h = item % a.n_heads;
   const bool in = row < a.rows;
   const int seq = in ? a.seq[row] : -1, pos = in ? a.pos[row] : -1;
-  const int slot = a.slot_base + (in && a.depth ? a.depth[row] : 0);
-  const bool live = seq >= 0 && seq < a.cache.n_seqs && pos < a.max_ctx && slot >= 0 && slot < a.cache.n_kv_slots;
+  const int slot = row_slot(a.cache, a.slot_base, in && a.depth ? a.depth[row] : 0);
+  const bool live = seq >= 0 && seq < a.cache.n_seqs && pos < a.max_ctx && slot >= 0;
   if (A.chunks > 0 && h == 0 && live && (!TEAM || warp == 0)) {  // does the row name the prefix's blocks?
     int base = -1;
     for (int r0 = 0; base < 0; r0 += 32) {  // ends: this row has a sequence
