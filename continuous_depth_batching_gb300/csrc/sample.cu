@@ -479,31 +479,6 @@ struct Row {
     return Keep{lo, (unsigned int)((need + each_w - 1) / each_w)};
   }
 
-  // Of v[0..7] of every thread: the sum before this thread's, and of all.
-  __device__ __forceinline__ unsigned long long scan8(const unsigned long long* v, unsigned long long* total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    unsigned long long inc = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) inc += v[e];
-    const unsigned long long mine = inc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    __syncthreads();  // S.wm and S.found_* are free
-    if (lane == 31) S.wm[w] = inc;
-    if (threadIdx.x == 0) S.found_bin = ValueBins::kAll;
-    __syncthreads();
-    unsigned long long before = inc - mine, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i == w) before += all;
-      all += S.wm[i];
-    }
-    *total = all;
-    return before;
-  }
   // bf16: the threshold of top_p among the logits that `keep` leaves, from one
   // histogram with a bin per value, whose masses are counts times weights.  `zero`:
   // logits at or below it have no mass.  False, and nothing done, where a threshold
