@@ -75,7 +75,8 @@ struct Head {
   }
   PyObject* call() const {
     int rc;
-    Py_BEGIN_ALLOW_THREADS rc = fn(a, stream);
+    const A args = *a;  // another thread may fill in the structure as soon as this one lets go
+    Py_BEGIN_ALLOW_THREADS rc = fn(&args, stream);
     Py_END_ALLOW_THREADS return PyLong_FromLong(rc);
   }
 };

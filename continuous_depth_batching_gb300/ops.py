@@ -183,10 +183,10 @@ class Sampler(_Op):
             if rc is None:
                 self._explain(logits, u, temperature, top_k, top_p, min_p)
             self._fail(rc)
-        rows = self.args.rows
-        if self._out[0].shape[0] != rows:
-            self._out = self.token[:rows], self.logprob[:rows]
-        return self._out
+        rows, out = logits.shape[0], self._out
+        if out[0].shape[0] != rows:
+            out = self._out = self.token[:rows], self.logprob[:rows]
+        return out
 
     def _explain(self, logits, u, temperature, top_k, top_p, min_p):
         t, rows = self._t, logits.shape[0]
