@@ -21,8 +21,9 @@
 //                   numbers, what the first one leaves in the second, which
 //                   take the space of the 64 scores and a product each: within
 //                   2^-17, as in the kernel for a row's own keys (256 rows x
-//                   32/8 heads behind 16384 tokens: 116 us, 112 with one; an
-//                   output's error then is its own rounding's alone);
+//                   32/8 heads behind 16384 tokens: 117 us, 112 with one; 8
+//                   rows behind 512: 10.1 and 9.4; an output's error then is
+//                   its own rounding's alone);
 //   warps 8, 11     TMA producers: q tile and K blocks, V blocks.  A copy takes
 //                   its warp some 70 cycles to issue, so a page is one copy: a
 //                   4-dimensional box lays its 128-byte slices out as
@@ -87,8 +88,8 @@ struct Geo {
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_V = OFF_K + KS * KVB;
   static constexpr int OFF_RAW = OFF_V + VS * KVB;
-  static constexpr int SCN = 2 * kKeys + 4;
-  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: [VS] scales of K, of V, and two maxima of V's
+  static constexpr int SCN = 3 * kKeys + 4;
+  static constexpr int OFF_SC = OFF_RAW + NR * RAW;   // e4m3: [VS] scales of K, of V, the latter's logarithms, two maxima of those
   static constexpr int OFF_XCH = OFF_SC + (Q8 ? VS * SCN * 4 : 0);  // float2 [2][kRows]
   static constexpr int OFF_BAR = OFF_XCH + 2 * kRows * 8;
   static constexpr int NBAR = 4 + 2 * KS + 2 * VS + 3 + 2 * 4;
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
 
   // e4m3: registers from the other warpgroups to the softmax groups (128 each at launch), which read the scales of
   // a block's keys before its scores and those of its values before they are wanted: read where they are used, one
-  // read waits for another (256 rows x 32/8 heads behind 16384 tokens: 125 us, 108 so; bf16: 85).
+  // read waits for another (256 rows x 32/8 heads behind 16384 tokens, few keys of their own: 125 us, 108 so; it is
+  // 112 now, bf16 97).
   static_assert(!Q8 || (G::THREADS == 512 && 256 * 184 + 256 * 72 <= 512 * 128), "registers of the launch");
   if (warp >= 8) {
     if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -335,9 +337,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
             const float fv = f[kKeys + tid];
             sc[tid] = f[tid];
             sc[kKeys + tid] = fv;
+            sc[2 * kKeys + tid] = __log2f(fabsf(fv));
             // The largest magnitude of the value scales that were copied, by halves: its logarithm, at least -82.
             const uint32_t fm = __reduce_max_sync(0xffffffffu, tid / 16 < npg - 4 * j ? __float_as_uint(fabsf(fv)) : 0u);
-            if (lane == 0) sc[2 * kKeys + tid / 32] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
+            if (lane == 0) sc[3 * kKeys + tid / 32] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
           }
   #pragma unroll
           for (int u = 0; u < kKeys / KI; ++u) {
@@ -478,21 +481,22 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) sf[k] = ld_shared_v4(scales + 256 + k * 16);
-        const float4 vm = ld_shared_v4(scales + 512);
+        const float4 vm = ld_shared_v4(scales + 768);
         mask();
         // No weight times scale may pass 2^15 (fp16 ends at 2^16), no weight 2^97.  The largest score with the largest
         // scale (2^-82 if that is less) bounds them; only where that passes, and so at a row's first keys, is the
-        // largest product looked for (for every block: 141 us where this takes 130, 256 rows x 32/8 heads behind
-        // 16384 tokens).
+        // largest product looked for (for every block: 141 us where this takes 126, 256 rows x 32/8 heads behind
+        // 16384 tokens; logarithms of the scales taken here and not by the converters: 129).
         const float mx = greatest();
         if (__any_sync(0xffffffffu, mx + fmaxf(vm.x, vm.y) > m + 15.f)) {
-          float t = mx - 90.f;
+          float t4[4] = {mx - 82.f, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float4 f = sf[k];
-            t = max3(t, fmaf(sv[4 * k], scale, __log2f(fabsf(f.x)) - 8.f), fmaf(sv[4 * k + 1], scale, __log2f(fabsf(f.y)) - 8.f));
-            t = max3(t, fmaf(sv[4 * k + 2], scale, __log2f(fabsf(f.z)) - 8.f), fmaf(sv[4 * k + 3], scale, __log2f(fabsf(f.w)) - 8.f));
+            const float4 f = ld_shared_v4(scales + 512 + k * 16);
+            t4[k % 4] = max3(t4[k % 4], fmaf(sv[4 * k], scale, f.x), fmaf(sv[4 * k + 1], scale, f.y));
+            t4[k % 4] = max3(t4[k % 4], fmaf(sv[4 * k + 2], scale, f.z), fmaf(sv[4 * k + 3], scale, f.w));
           }
+          float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) - 8.f;
           t = t > m + 7.f ? t : m;
           if (__any_sync(0xffffffffu, t != m) && !(ok = move(t))) break;
         }
