@@ -81,7 +81,9 @@ __device__ __forceinline__ uint2 pack4(const float* v) {
 }
 // Eight e4m3 codes of v / (s + sl), inv the reciprocal of s, sl what rounding the
 // scale to s left.  The quotients are corrected by their remainders, to the nearest
-// fp32 number.  One that thereby lands halfway between two (normal) codes, the 20th
+// fp32 number (P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, IBM J. Res. Dev. 34, 1990; the scale's rest is added to its
+// remainder).  One that thereby lands halfway between two (normal) codes, the 20th
 // last bit set and none behind it, takes the side its remainder points to, so that
 // no value is rounded twice: of 34 million codes (8192 rows of 16 heads) some 28
 // differ from those of the formula in 64 bits, nearly all of them keys by norm and
@@ -324,8 +326,8 @@ cudaError_t launch_cache_write(cudaStream_t s, const cdb_cache_write_args& a) {
 // Decode attention, grouped heads, bf16 or e4m3 cache.
 //
 // One query token per row: every cached key of a row is read once per KV head,
-// so HBM bounds it (128 rows of 17 to 8192 keys, 32/8 heads, bf16: 330 us, 6.4
-// TB/s; 64 rows of 128 to 1280 keys, 16 heads, e4m3: 35 us, 5.4 TB/s).  A CTA takes `split` keys of one row and up to four KV
+// so HBM bounds it (128 rows of 17 to 8192 keys, 32/8 heads, bf16: 310 to 330 us, 6.4
+// TB/s and more; 64 rows of 128 to 1280 keys, 16 heads, e4m3: 35 us, 5.4 TB/s).  A CTA takes `split` keys of one row and up to four KV
 // heads: a producer warp moves 16-key pages of those heads (16 * heads rows of
 // one rectangular tile for K, one for V, and the scales) with TMA into a ring,
 // four consumer warps each take one (KV head, run of keys).  A warp computes
@@ -348,6 +350,9 @@ cudaError_t launch_cache_write(cudaStream_t s, const cdb_cache_write_args& a) {
 // times scale, or 2^-33 of the row's largest.
 // Partials (maximum, sum, unnormalised output) of the splits are joined in
 // split order by k_join; a row that fits one split is written directly.
+// The grid has every split of max_ctx for every row: a CTA without keys leaves
+// after reading its row's place, but takes its turn on an SM (128 rows of 1000
+// keys, 32/8 heads, bf16: 82 us with max_ctx 1024, 126 with 32768, 252 with 131072).
 // ---------------------------------------------------------------------------
 namespace da {
 
