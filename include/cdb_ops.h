@@ -129,6 +129,8 @@ int cdb_cache_write(const cdb_cache_write_args *a, void *stream);
  * Weights enter the products as 16-bit numbers: bf16 cache, two of them, within
  * 2^-17 of the weight; e4m3 cache, weight times value scale within 2^-22 of its
  * value or 2^-33 of the row's largest (behind a shared prefix 2^-11 or 2^-33).
+ * With an e4m3 cache a query's elements are exact down to 2^-17 of the head's
+ * largest one, smaller ones within 2^-25 of that.
  * A row with seq < 0 is padding: its output is left as it was.  A row with
  * pos < 0 has no keys: zeros.  Without a shared prefix, keys are taken a fixed
  * number at a time and joined in order, so a row's bits do not depend on the
