@@ -1,6 +1,6 @@
 """Operators called on other streams than the one they were made on.
 
-torch.cuda._sleep holds a stream up for some tens of milliseconds, so that what is not ordered shows."""
+torch.cuda._sleep holds a stream up for about half a second, so that what is not ordered shows."""
 
 import gc
 
@@ -8,7 +8,7 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
-CYCLES = 100_000_000
+CYCLES = 1_000_000_000
 
 
 def attention(rows=4):
