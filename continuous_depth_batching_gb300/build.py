@@ -42,6 +42,8 @@ SOURCES = [
     "sample.cu",
     "cache_ops.cu",
     "shared_prefix.cu",
+    "prompt_attention.cu",
+    "row_ops.cu",
     "ops.cu",
 ]
 

@@ -1,0 +1,919 @@
+// Attention of packed prompts and of drafted tokens over the paged cache
+// (cdb_prompt_attention, cdb_draft_attention of include/cdb_ops.h) on the
+// 5th-generation tensor cores: bf16 or e4m3 cache, head_dim 32, 64, 96 or 128.
+//
+// The query rows of a tile are tokens times the query heads of one KV head, 128
+// rows of a matrix product with the keys (so grouped heads read K and V once and
+// a tile's rows lie close together: with four heads per KV head, 32 tokens of a
+// causal prompt, hence little work above the diagonal).  An item is a stretch
+// of a request's rows, up to two tiles of them, for one KV head, and a range of its
+// keys, walked in blocks of 128; one CTA takes one item.  Two softmax groups
+// of 128 threads, a thread per query row, work in turn:
+//   two tiles   each group has a tile of its own and takes every block, so that a
+//               block of keys is read once for 256 rows;
+//   one tile    the groups take even and odd blocks of the same rows, and are joined
+//               at the end.
+// Either way the tensor cores work for one group while the other is in its
+// exponentials.  Jobs (block, group) go in order t = 0, 1, ..; t + 2 is the same group's next.
+//   warps 0-7    softmax: a thread reads the 128 scores of its row from TMEM, masks
+//                them, and writes the weights over them in 16 bits, the A operand of
+//                the second product.  bf16 weights are two numbers, what the first
+//                leaves in the second (within 2^-17, a product each); e4m3: one
+//                fp16 number of weight times value scale, relative to the row's largest;
+//   warp 9       issues S = Q K^T (128 x 128) and O += P V.  The next scores of a group
+//                follow its product with V in the tensor core's queue, which keeps order,
+//                so they may overwrite the weights, and their commit covers both;
+//   warps 8, 11  bf16: copy K and V pages by TMA; then warp 11 looks the blocks that some
+//                rows do not see through (below).  e4m3: copy codes and scales in units of
+//                64 keys of K or of V;
+//   warps 12-15  e4m3: widen codes to fp16 in the MMA's swizzled layout.
+// A weight of 0 times an infinite or NaN value is NaN, so in blocks that not all
+// rows see, V rows with such an element are set to zero in shared memory before the
+// product, and rows that see them take a NaN weight; V rows behind the sequence's
+// end, which may hold anything, are set to zero too.
+// What bounds it: two products (three with two-part weights) of 512 cycles and 128 x 128
+// exponentials of 512 or more a job, for a long prompt; HBM for drafts over long caches.
+// Every mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT,
+// lets its copies and MMAs finish (bounded), frees TMEM and returns.
+#include <algorithm>
+#include <climits>
+
+#include "../../include/cdb.h"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "row_ops.h"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace cdb {
+namespace pa {
+
+using namespace tc;
+
+constexpr int kRows = 128;   // query rows of a tile
+constexpr int kKeys = 128;   // keys of a block: eight pages
+constexpr int kSms = 152;
+constexpr int kItems = 3 * kSms;  // items (times KV heads) that cutting keys aims at
+constexpr int kMinBlocks = 2;     // blocks of a cut item, at least
+constexpr int kCutBelow = 4 * kSms;  // items without cutting, above which no call cuts
+
+template <int HD, bool Q8>
+struct Geo {
+  static_assert(HD % 32 == 0 && HD <= 128, "head dim");
+  static constexpr int NX = (HD + 63) / 64;       // 128-byte slices of a 16-bit row
+  static constexpr int SLICE = 128 * 128;         // one slice of 128 rows
+  static constexpr int TILE = NX * SLICE;         // Q tile, K or V block
+  static constexpr int KS = NX == 2 ? 2 : 4;      // K blocks in flight
+  static constexpr int VS = NX == 2 ? (Q8 ? 2 : 3) : 4;
+  // e4m3: units of 64 keys of K or V, as they come: codes, then their scales.
+  static constexpr int UNIT = 64 * HD + 64 * 4;
+  static constexpr int NU = NX == 2 ? 3 : 6;
+  static constexpr int SCN = 3 * kKeys + 4;       // scales of K, of V, the latter's logarithms, the largest of those by quarters
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KS * TILE;
+  static constexpr int OFF_U = OFF_V + VS * TILE;
+  static constexpr int OFF_SC = OFF_U + (Q8 ? NU * UNIT : 0);
+  static constexpr int OFF_BAD = OFF_SC + (Q8 ? VS * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
+  static constexpr int OFF_BAR = OFF_BAD + VS * (Q8 ? kKeys : 16);
+  static constexpr int NBAR = 2 + 2 * KS + 3 * VS + 2 + 2 + 2 + 1 + 2 * 6;
+  static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
+  static constexpr int THREADS = Q8 ? 512 : 384;
+  static constexpr int S_COL = 256;               // [2][128] scores, then weights
+  static constexpr int O_COL = 0;                 // [2][128], HD of them used
+  static_assert(SMEM + 512 <= 232448, "shared memory, static too");
+};
+
+struct Args {
+  cdb_prompt_attention_args a;
+  int group;    // query heads per KV head
+  int tokens;   // of a tile: tokens * group <= 128
+  int cut;      // items (per KV head) that cutting keys may add; 0: no request is cut
+  int tiles;    // upper bound of double tiles
+  float* part_o;   // [item][KV head][256][HD]
+  float2* part_ml; // [item][KV head][256]
+  int4* info;      // [tiles]: request, first token, first item, chunks
+};
+
+struct Item {
+  int request, seq, row0, count, len;  // of the request
+  int t0;                              // first token
+  int chunk, chunks, cb;               // chunk of `chunks`, blocks of a chunk
+  int tile;                            // of all double tiles, -1: this item is not there
+};
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// The request's double tiles, its blocks of keys; false: it is not there.
+__device__ __forceinline__ bool look(const Args& A, int i, Item& it, bool tell) {
+  const cdb_prompt_attention_args& a = A.a;
+  const int r0 = a.row_start[i], r1 = a.row_start[i + 1], len = a.lens[i], seq = a.seq ? a.seq[i] : i;
+  it.request = i, it.seq = seq, it.row0 = r0, it.count = r1 - r0, it.len = len;
+  if (seq < 0 || r1 == r0) return false;
+  const bool ok = seq < a.cache.n_seqs && r0 >= 0 && r1 > r0 && r1 <= a.rows && len >= 0 && len <= a.max_ctx &&
+                  (!a.visible || r1 - r0 <= 64 * a.mask_words);
+  if (!ok && tell) report(a.status, CDB_OPS_BAD_ROW);
+  return ok;
+}
+
+// Which item this CTA takes, found by all its threads: requests in order, of each
+// request its cut ranges of keys, of those its double tiles, the last (most keys) first.
+// A request's keys are cut into ranges of `cb` blocks, the same for the whole call, such
+// that all of it makes about kItems items.
+template <int THREADS>
+__device__ __forceinline__ Item find_item(const Args& A, int y) {
+  __shared__ int sh[THREADS / 32][2];
+  __shared__ long long work_s[THREADS / 32];
+  __shared__ Item found;
+  const cdb_prompt_attention_args& a = A.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, step = 2 * A.tokens;
+  const bool tell = blockIdx.x == 0 && y == 0;
+  Item it;
+  int cb = INT_MAX / kKeys;
+  if (A.cut) {
+    long long work = 0;  // blocks of keys, once for each double tile
+    for (int i = tid; i < a.requests; i += THREADS)
+      if (look(A, i, it, false)) work += (long long)div_up(it.count, step) * max(1, div_up(it.len, kKeys));
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) work += __shfl_xor_sync(0xffffffffu, work, o);
+    if (lane == 0) work_s[warp] = work;
+    __syncthreads();
+    work = 0;
+    for (int w = 0; w < THREADS / 32; ++w) work += work_s[w];
+    cb = (int)max((long long)kMinBlocks, (work + A.cut - 1) / A.cut);
+  }
+  if (tid == 0) found.tile = -1;
+  int items = 0, tiles = 0;  // of the requests before this round
+  for (int i0 = 0; i0 < a.requests; i0 += THREADS) {
+    const int i = i0 + tid;
+    const bool on = i < a.requests && look(A, i, it, tell);
+    const int nt = on ? div_up(it.count, step) : 0, nc = on ? max(1, div_up(div_up(it.len, kKeys), cb)) : 0;
+    int xi = nt * nc, xt = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
+      if (lane >= o) xi += p, xt += q;
+    }
+    if (lane == 31) sh[warp][0] = xi, sh[warp][1] = xt;
+    __syncthreads();
+    int all_i = 0, all_t = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w == warp) xi += items + all_i - nt * nc, xt += tiles + all_t - nt;
+      all_i += sh[w][0], all_t += sh[w][1];
+    }
+    items += all_i, tiles += all_t;
+    if (on && y >= xi && y < xi + nt * nc) {
+      const int k = y - xi, tile = nt - 1 - k % nt;
+      it.t0 = tile * step;
+      it.chunk = k / nt, it.chunks = nc, it.cb = cb;
+      it.tile = xt + tile;
+      found = it;
+    }
+    if (A.cut && tell && on)  // for the join
+      for (int k = 0; k < nt; ++k) A.info[xt + k] = make_int4(i, k * step, xi + nt - 1 - k, nc | (nt << 16));
+    __syncthreads();
+  }
+  if (A.cut && tell)
+    for (int t = tiles + tid; t < A.tiles; t += THREADS) A.info[t] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  return found;
+}
+
+// 32 keys from position s on that a row sees, as bits.  Prompt: positions up to
+// lim.  Draft: those before `lim`, and behind them the row's mask.
+__device__ __forceinline__ uint32_t seen(int s, int lim, const uint32_t* mask, int nodes) {
+  if (!mask) return lim < s ? 0u : lim - s >= 31 ? ~0u : (2u << (lim - s)) - 1;
+  const int u = s - lim;  // node of the first bit
+  uint32_t w = u <= -32 ? ~0u : u < 0 ? (1u << -u) - 1 : 0u;
+  if (u > -32 && u < nodes) {
+    const int at = max(u, 0) / 32, off = max(u, 0) % 32, words = div_up(nodes, 32);
+    uint32_t b = __funnelshift_r(mask[at], at + 1 < words ? mask[at + 1] : 0u, off);
+    const int left = nodes - max(u, 0);
+    if (left < 32) b &= (1u << left) - 1;
+    w |= u < 0 ? b << -u : b;
+  }
+  return w;
+}
+
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
+    k_prompt(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ Args A) {
+  using G = Geo<HD, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float2* xch = reinterpret_cast<float2*>(smem + G::TILE);  // [2][kRows], with one tile: the second's place
+  uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem + G::OFF_BAD);
+  uint8_t* bad_bytes = smem + G::OFF_BAD;
+  uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);  // [2]
+  uint64_t* k_full = q_ready + 2;
+  uint64_t* k_empty = k_full + G::KS;
+  uint64_t* v_full = k_empty + G::KS;
+  uint64_t* v_empty = v_full + G::VS;
+  uint64_t* v_clean = v_empty + G::VS;   // blocks that were looked through
+  uint64_t* s_full = v_clean + G::VS;    // [2] by group
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_final = p_full + 2;
+  uint64_t* done = o_final + 2;
+  uint64_t* u_full = done + 1;           // [NU <= 6]
+  uint64_t* u_empty = u_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + 6);
+
+  const cdb_prompt_attention_args& a = A.a;
+  const cdb_paged_cache& c = a.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kh = blockIdx.x;
+  if (threadIdx.x == 0) {
+    if constexpr (!Q8) asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&q_ready[g], 4);
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&o_final[g], 1);
+    }
+    for (int s = 0; s < G::KS; ++s) {
+      mbar_init(&k_full[s], Q8 ? 4 : 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < G::VS; ++s) {
+      mbar_init(&v_full[s], Q8 ? 4 : 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_clean[s], 1);
+    }
+    mbar_init(done, 1);
+    for (int s = 0; s < 6; ++s) {
+      mbar_init(&u_full[s], 1);
+      mbar_init(&u_empty[s], 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  const Item it = find_item<G::THREADS>(A, blockIdx.y);
+  if (it.tile < 0) return;
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tt = A.tokens;
+  const int n_tok = min(2 * tt, it.count - it.t0);      // tokens of this item
+  const bool two = n_tok > tt;
+  const int before = it.len - it.count;                 // position of the request's first token; < 0: that many see nothing
+  // Keys that a tile's rows may see, all of them together: the end of the last.
+  auto end_of = [&](int last_token) { return a.visible ? it.len : min(it.len, max(0, before + last_token + 1)); };
+  const int b_lo = it.chunk * it.cb;                    // first block of the range (cb is bounded: no overflow with chunk 0)
+  auto blocks_to = [&](int keys) { return max(0, min(div_up(keys, kKeys) - b_lo, it.cb)); };
+  const int end = end_of(it.t0 + n_tok - 1);
+  const int nb = blocks_to(end);                        // blocks of the item
+  const int nb0 = two ? blocks_to(end_of(it.t0 + tt - 1)) : nb;  // of the first tile
+  // Blocks from this one on are not seen whole by every row: they are looked through.
+  const int whole = max(0, a.visible ? before : before + it.t0 + 1) / kKeys - b_lo;
+  const int first_part = max(0, min(nb, whole));
+  const int jobs = two ? 2 * nb : nb;
+  auto block_of = [&](int t) { return two ? t >> 1 : t; };
+  auto valid = [&](int t) { return t < jobs && (!two || (t & 1) || (t >> 1) < nb0); };
+
+  static_assert(!Q8 || 256 * 176 + 256 * 80 <= 512 * 128, "registers of the launch");
+  static_assert(Q8 || 256 * 208 + 128 * 72 <= 384 * 168, "registers of the launch");
+  if (warp >= 8) {
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 9) {
+      // ---------------- products ----------------
+      constexpr uint32_t idS = idesc_16(!Q8, kRows, kKeys, false), idO = idesc_16(!Q8, kRows, HD, true);
+      const uint64_t qd = desc_k(su32(smem), 1024), kd = desc_k(su32(smem + G::OFF_K), 1024);
+      const uint64_t vd = desc_mn(su32(smem + G::OFF_V), G::SLICE, 1024);
+      bool ok = true;
+      auto scores = [&](int t) {
+        const int b = block_of(t), g = t & 1, s = b % G::KS;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&k_full[s], (b / G::KS) & 1)))) return;
+        fence_after();
+        const uint64_t qb = qd + (uint32_t)((two ? g : 0) * (G::TILE / 16)), kb = kd + (uint32_t)(s * (G::TILE / 16));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t at = ((kk / 4) * G::SLICE + (kk % 4) * 32) / 16;
+            mma_ss(tmem + G::S_COL + g * kKeys, qb + at, kb + at, idS, kk > 0 ? 1u : 0u);
+          }
+          commit(&s_full[g]);
+          if (!two || g == 1) commit(&k_empty[s]);
+        }
+        __syncwarp();
+      };
+      for (int g = 0; ok && g < 2; ++g) {
+        if (!valid(g)) continue;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_ready[two ? g : 0], 0)))) break;
+        scores(g);
+      }
+      for (int t = 0; ok && t < jobs; ++t) {
+        if (!valid(t)) continue;
+        const int b = block_of(t), g = t & 1, n = t >> 1, s = b % G::VS;
+        uint64_t* bar = lane == 1 ? &p_full[g] : b >= first_part && !Q8 ? &v_clean[s] : &v_full[s];
+        // v_clean completes a phase for each block looked through that came to this slot.
+        const int use = b >= first_part && !Q8 ? (b - first_part) / G::VS : b / G::VS;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, (lane == 1 ? n : use) & 1)))) break;
+        fence_after();
+        const uint64_t vb = vd + (uint32_t)(s * (G::TILE / 16));
+        const uint32_t d = tmem + G::O_COL + g * kRows, p = tmem + G::S_COL + g * kKeys;
+        const int steps = min(8, div_up(end - (b_lo + b) * kKeys, 16));  // pages with keys
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * 2048) / 16, idO, (n > 0 || kk > 0) ? 1u : 0u);
+          if constexpr (!Q8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < steps) mma_ts(d, p + 64 + kk * 8, vb + (kk * 2048) / 16, idO, 1u);
+          }
+          if (!two || g == 1) commit(&v_empty[s]);
+          if (!valid(t + 2)) commit(&o_final[g]);
+        }
+        __syncwarp();
+        if (valid(t + 2)) scores(t + 2);
+      }
+      if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+      if (elect_one()) commit(done);  // every MMA issued above completes before TMEM is released
+      __syncwarp();
+      mbar_wait(done, 0);
+    } else if (warp == 8 || warp == 11) {
+      const int kv = warp == 8 ? 0 : 1;
+      const int* bt = c.block_table + (size_t)it.seq * c.max_blocks;
+      const int npg = div_up(end, 16);  // pages with keys
+      bool ok = true;
+      int issued = 0;
+      auto block_at = [&](int pg) {
+        int blk = pg < npg ? bt[pg] : -1;
+        if (pg < npg && (blk < 0 || blk >= c.kv_blocks)) report(a.status, CDB_OPS_BAD_BLOCK), blk = -1;
+        return blk;
+      };
+      // Key rows before this head's page of a block (V follows n_kv_heads pages after K).
+      auto row_of = [&](int blk, int v) { return ((((long long)blk * c.n_kv_slots + a.slot) * 2 + v) * c.n_kv_heads + kh) * 16; };
+      if constexpr (Q8) {
+        // Units: K of a block in two halves, then V; even ones are warp 8's, odd ones warp 11's.
+        for (int u = kv; u < 4 * nb; u += 2) {
+          const int s = u % G::NU, b = u >> 2, v = (u >> 1) & 1, pg = (b_lo + b) * 8 + (u & 1) * 4;
+          const int blk = lane < 4 ? block_at(pg + lane) : -1;
+          const int n = __popc(__ballot_sync(0xffffffffu, blk >= 0));
+          if (u >= G::NU && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[s], (u / G::NU - 1) & 1)))) break;
+          const uint32_t at = su32(smem + G::OFF_U + s * G::UNIT);
+          if (elect_one()) mbar_arrive_tx(&u_full[s], (uint32_t)n * (16 * HD + 64));
+          __syncwarp();
+          if (blk >= 0) {
+            const long long r = row_of(blk, v);
+            bulk_1d(at + lane * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD, &u_full[s]);
+            bulk_1d(at + 64 * HD + lane * 64, c.scales + r, 64, &u_full[s]);
+          }
+          __syncwarp();
+          issued = u + 1;
+        }
+        if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+        // Copies in flight land before the CTA may leave.  A slot that the other warp filled again was used, and its
+        // phase has moved on: where all went well only this warp's last unit is left to wait for, and that was used too.
+        for (int u = ok ? issued - 1 : max(kv, issued - 1 - 2 * ((G::NU - 1) / 2)); u >= 0 && u < issued; u += 2)
+          mbar_wait(&u_full[u % G::NU], (u / G::NU) & 1);
+      } else {
+        constexpr int slots_k = G::KS, slots_v = G::VS;
+        const int slots = kv ? slots_v : slots_k;
+        uint64_t* full = kv ? v_full : k_full;
+        uint64_t* empty = kv ? v_empty : k_empty;
+        const uint32_t ring = su32(smem + (kv ? G::OFF_V : G::OFF_K));
+        uint64_t pol;  // a sequence's keys are read again by its other tiles
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+        // The blocks that some rows do not see: rows behind the end and rows with a value that is not finite
+        // become zeros; the latter are noted.
+        auto clean = [&](int b) {
+          const int s = b % slots, left = min(kKeys, end - (b_lo + b) * kKeys);
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[s], (b / slots) & 1))) return false;
+          uint8_t* v = smem + G::OFF_V + s * G::TILE;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 32 + lane;
+            uint32_t top = 0;
+            if (r < left) {
+#pragma unroll
+              for (int x = 0; x < HD / 8; ++x) {
+                const uint4 w = *reinterpret_cast<const uint4*>(v + (x / 8) * G::SLICE + r * 128 + (((x % 8) ^ (r & 7)) << 4));
+                // an exponent of all ones carries into the sign's place
+                top |= (((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                        ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u));
+              }
+            }
+            const bool bad = (top & 0x80008000u) != 0;
+            if (bad || r >= left) {
+#pragma unroll
+              for (int x = 0; x < G::NX * 8; ++x)
+                *reinterpret_cast<uint4*>(v + (x / 8) * G::SLICE + r * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t bits = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) bad_keys[s * 4 + i] = bits;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_clean[s]);
+          return true;
+        };
+        int cleaned = kv ? first_part : nb;
+        for (int j = 0; j < nb; ++j) {
+          const int s = j % slots;
+          const int blk = lane < 8 ? block_at((b_lo + j) * 8 + lane) : -1;
+          const uint32_t there = __ballot_sync(0xffffffffu, blk >= 0);
+          // A slot to be filled again may hold a block that waits to be looked through.
+          while (cleaned < nb && cleaned <= j - slots && ok) ok = clean(cleaned++);
+          if (!ok) break;
+          if (j >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((j / slots) - 1) & 1)))) break;
+          if (elect_one()) mbar_arrive_tx(&full[s], (uint32_t)__popc(there) * (G::NX * 16 * 128));
+          __syncwarp();
+          for (int i = 0; i < 8; ++i) {
+            const int bi = __shfl_sync(0xffffffffu, blk, i);
+            if (bi >= 0 && elect_one()) {
+              const int y = (int)row_of(bi, kv);
+#pragma unroll
+              for (int x = 0; x < G::NX; ++x)
+                tma_2d(ring + s * G::TILE + x * G::SLICE + i * 2048, &tmk, &full[s], x * 128, y, pol);
+            }
+            __syncwarp();
+          }
+          issued = j + 1;
+        }
+        while (cleaned < nb && ok) ok = clean(cleaned++);
+        if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+        for (int j = max(0, issued - slots); j < issued; ++j) mbar_wait(&full[j % slots], (j / slots) & 1);
+      }
+    } else if (Q8 && warp >= 12) {
+      // ---------------- code converters ----------------
+      // 16 codes to 32 bytes at a time; lanes of the upper half of a row store their second piece first, so that
+      // the stores of eight lanes meet every bank once.
+      const int tid = threadIdx.x - 384;
+      constexpr int C = HD / 16, CL = HD == 96 ? 8 : C, PIECES = 64 * CL;  // of a row: pieces, lanes
+      bool ok = true;
+      for (int u = 0; u < 4 * nb; ++u) {
+        const int s = u % G::NU, b = u >> 2, v = (u >> 1) & 1, half = u & 1;
+        const int slots = v ? G::VS : G::KS, slot = b % slots;
+        uint64_t* empty = v ? v_empty : k_empty;
+        const bool other = lane == 1 && b >= slots;  // lane 1 waits for the slot, the others for the codes
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &empty[slot] : &u_full[s],
+                                                     other ? (b / slots - 1) & 1 : (u / G::NU) & 1))))
+          break;
+        const uint8_t* raw = smem + G::OFF_U + (size_t)s * G::UNIT;
+        uint8_t* to = smem + (v ? G::OFF_V : G::OFF_K) + slot * G::TILE;
+        const int left = end - (b_lo + b) * kKeys - half * 64;  // keys of this unit that are there
+        const bool part = v && b >= first_part;
+        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::VS) * G::SCN;
+        // K's scales go where V's slot is free: the product with the block before in that slot is done (v_empty).
+        if (!v && b >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[b % G::VS], (b / G::VS - 1) & 1)))) break;
+        const float* raw_scale = reinterpret_cast<const float*>(raw + 64 * HD);
+#pragma unroll
+        for (int i = 0; i < PIECES / 128; ++i) {
+          const int key = (i * 128 + tid) / CL, x = tid % CL, r = half * 64 + key;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (x < C && !(v && key >= left)) w = *reinterpret_cast<const uint4*>(raw + key * HD + x * 16);
+          if (part) {
+            // A code of NaN has all seven lower bits.  Every element of a key that holds one, or whose scale is not
+            // finite, becomes 0.
+            const uint32_t f = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                               ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            const uint32_t found = __ballot_sync(0xffffffffu, (f & 0x80808080u) != 0);
+            const bool bad = key < left && (((found >> (lane / CL * CL)) & ((1u << CL) - 1)) || !(fabsf(raw_scale[key]) < INFINITY));
+            if (bad) w = make_uint4(0, 0, 0, 0);
+            if (x == 0) bad_bytes[slot * kKeys + r] = bad;
+          }
+          if (x < C) {
+            uint8_t* d = to + (x / 4) * G::SLICE + r * 128;
+            const uint4 lo = make_uint4(widen(w.x), widen_hi(w.x), widen(w.y), widen_hi(w.y));
+            const uint4 hi = make_uint4(widen(w.z), widen_hi(w.z), widen(w.w), widen_hi(w.w));
+            const int c0 = (x % 4) * 2, sw = r & 7;
+            const bool swap = x >= 4;
+            *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ sw) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(d + (((c0 + !swap) ^ sw) << 4)) = swap ? lo : hi;
+          }
+        }
+        if (tid < 64) {
+          const float f = raw_scale[tid];
+          if (!v) {
+            sc[half * 64 + tid] = f;
+          } else {
+            // Keys behind the end, and in blocks looked through those whose scale is not finite, take no part.
+            const float fv = tid >= left || (part && !(fabsf(f) < INFINITY)) ? 0.f : f;
+            sc[kKeys + half * 64 + tid] = fv;
+            sc[2 * kKeys + half * 64 + tid] = __log2f(fabsf(fv));
+            const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
+            if (lane == 0) sc[3 * kKeys + half * 2 + tid / 32] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&u_empty[s]);
+          if (half) mbar_arrive(v ? &v_full[slot] : &k_full[slot]);
+        }
+      }
+      if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    }
+  } else {
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------- softmax groups ----------------
+    const int q4 = warp & 3, g = warp >> 2;
+    const int r = q4 * 32 + lane;
+    const int tile = two ? g : 0;
+    const int tk = it.t0 + tile * tt + r / A.group;  // token of this row
+    const int head = kh * A.group + r % A.group;
+    const bool live = r < tt * A.group && tk < it.count;
+    const long long row = it.row0 + (live ? tk : 0);
+    // Prompt: the last key of this row.  Draft: the first key of the request's rows, which the mask is for.
+    const int lim = a.visible ? before : live ? before + tk : -1;
+    const int nodes = live ? it.count : 0;
+    const uint32_t* mask = a.visible ? reinterpret_cast<const uint32_t*>(a.visible + row * a.mask_words) : nullptr;
+    const bool turn_round = a.scale < 0.f;  // a negative factor turns the scores around first
+    float scale = fabsf(a.scale) * 1.4426950408889634f;
+    constexpr float kTau = 8.f;  // rescale O only when the row maximum grows by more than 2^8
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t to = trow + G::O_COL + g * kRows, ts = trow + G::S_COL + g * kKeys;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    {
+      // This row of q into the tile, swizzled; with one tile the first group does it.
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + (size_t)head * HD);
+      uint8_t* dst = smem + tile * G::TILE + r * 128;
+      float down = 1.f, up = 1.f;
+      if constexpr (Q8) {
+        // e4m3: each row divided by a power of two, in fp16.
+        float mx = 0.f;
+#pragma unroll
+        for (int x = 0; x < HD / 8; ++x) {
+          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+        }
+        const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
+        const bool norm = eb > 0x00800000u && eb < 0x7E000000u;  // else zero, tiny, infinite or NaN
+        down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f;
+        up = norm ? __uint_as_float(eb) : 1.f;
+      }
+      if (two || g == 0) {
+#pragma unroll
+        for (int x = 0; x < HD / 8; ++x) {
+          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
+          uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          if constexpr (Q8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xFFFF0000u) * down);
+          }
+          st_shared_v4(su32(dst + (x / 8) * G::SLICE + (((x % 8) ^ (r & 7)) << 4)), v[0], v[1], v[2], v[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready[tile]);
+      }
+      scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
+    }
+    int n = 0;  // jobs of this group so far
+    for (int t = g; ok && valid(t); t += 2, ++n) {
+      const int b = block_of(t);
+      const int k0 = (b_lo + b) * kKeys;
+      float sv[128];
+      auto load = [&] {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], n & 1)))) return;
+        fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32_ahead(ts + i * 32, sv + i * 32);
+        tmem_arrived();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pin32(sv + i * 32);
+        if (turn_round) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) sv[k] = -sv[k];
+        }
+      };
+      // Scores that the row does not see become -inf; those of keys whose value is not finite NaN.
+      auto mask_out = [&] {
+        if (b < first_part) return true;
+        if (!Q8 && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_clean[b % G::VS], ((b - first_part) / G::VS) & 1)))) return false;
+        // Four keys of a lane are looked at at once; hardly ever is one bad.
+        const bool some = Q8 && __any_sync(0xffffffffu, bad_keys[(b % G::VS) * (kKeys / 4) + lane] != 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = seen(k0 + i * 32, lim, mask, nodes);
+          const uint32_t bits = !Q8 ? bad_keys[(b % G::VS) * 4 + i]
+                                : some ? __ballot_sync(0xffffffffu, bad_bytes[(b % G::VS) * kKeys + i * 32 + lane] != 0) : 0u;
+          const uint32_t bad = bits & w;
+          if (!__all_sync(0xffffffffu, w == ~0u)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sv[i * 32 + k] = (w >> k) & 1 ? sv[i * 32 + k] : -INFINITY;
+          }
+          if (__any_sync(0xffffffffu, bad != 0)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sv[i * 32 + k] = (bad >> k) & 1 ? NAN : sv[i * 32 + k];
+          }
+        }
+        return true;
+      };
+      auto greatest = [&] {
+        float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x4[e] = max3(x4[e], sv[k + 2 * e], sv[k + 2 * e + 1]);
+        return fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale;
+      };
+      // Moves the row to the reference `to_m`; O holds the group's earlier blocks, whose products the commit of these
+      // scores covers, against the old one.
+      auto move = [&](float to_m) {
+        const float f = m == -INFINITY ? 0.f : ex2(m - to_m);
+        l *= f;
+        m = to_m;
+        if (n == 0) return;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 16) {
+          float v[16];
+          tmem_ld16(to + c0, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] *= f;
+          tmem_st16(to + c0, reinterpret_cast<const uint32_t*>(v));
+        }
+      };
+      if constexpr (Q8) {
+        const uint32_t scales = su32(smem + G::OFF_SC + (b % G::VS) * G::SCN * 4);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[b % G::VS], (b / G::VS) & 1)))) break;
+        load();
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float4 f = ld_shared_v4(scales + k * 16);
+          unpair(mul2(pair(sv[4 * k], sv[4 * k + 1]), pair(f.x, f.y)), sv[4 * k], sv[4 * k + 1]);
+          unpair(mul2(pair(sv[4 * k + 2], sv[4 * k + 3]), pair(f.z, f.w)), sv[4 * k + 2], sv[4 * k + 3]);
+        }
+        if (!mask_out()) break;
+        // No weight times scale may pass 2^15 (fp16 ends at 2^16), no weight 2^97.  The largest score with the largest
+        // scale (2^-82 if that is less) bounds them; only where that passes is the largest product looked for.
+        const float4 vm = ld_shared_v4(scales + 3 * kKeys * 4);
+        const float mx = greatest();
+        if (__any_sync(0xffffffffu, mx + fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)) > m + 15.f)) {
+          float t4[4] = {mx - 82.f, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float4 f = ld_shared_v4(scales + 2 * kKeys * 4 + k * 16);
+            t4[k % 4] = max3(t4[k % 4], fmaf(sv[4 * k], scale, f.x), fmaf(sv[4 * k + 1], scale, f.y));
+            t4[k % 4] = max3(t4[k % 4], fmaf(sv[4 * k + 2], scale, f.z), fmaf(sv[4 * k + 3], scale, f.w));
+          }
+          float tm = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) - 8.f;
+          tm = tm > m + 7.f ? tm : m;
+          if (__any_sync(0xffffffffu, tm != m)) move(tm);
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+        uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int k = i * 32 + 2 * e;
+            float x0, x1, x2, x3;
+            unpair(fma2(pair(sv[k], sv[k + 1]), s2, m2), x0, x1);
+            unpair(fma2(pair(sv[k + 2], sv[k + 3]), s2, m2), x2, x3);
+            x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+            l2[0] = add2(l2[0], pair(x0, x1));
+            l2[1] = add2(l2[1], pair(x2, x3));
+            const float4 f = ld_shared_v4(scales + (kKeys + k) * 4);
+            unpair(mul2(pair(f.x, f.y), pair(x0, x1)), x0, x1);
+            unpair(mul2(pair(f.z, f.w), pair(x2, x3)), x2, x3);
+            p[e] = pack_f16(x0, x1);
+            p[e + 1] = pack_f16(x2, x3);
+          }
+          tmem_st16(ts + i * 16, p);
+        }
+        float la, lb, lc, ld;
+        unpair(l2[0], la, lb);
+        unpair(l2[1], lc, ld);
+        l += (la + lb) + (lc + ld);
+      } else {
+        load();
+        if (!ok || !mask_out()) break;
+        const float mx = greatest();
+        const float mnew = mx > m + kTau ? mx : m;
+        if (__any_sync(0xffffffffu, mnew != m)) move(mnew);
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t s2 = pair(scale, scale), m2 = pair(-mm, -mm);
+        uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16], low[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int k = i * 32 + 2 * e;
+            float x0, x1, x2, x3;
+            unpair(fma2(pair(sv[k], sv[k + 1]), s2, m2), x0, x1);
+            unpair(fma2(pair(sv[k + 2], sv[k + 3]), s2, m2), x2, x3);
+            x0 = ex2(x0), x1 = ex2(x1), x2 = ex2(x2), x3 = ex2(x3);
+            l2[0] = add2(l2[0], pair(x0, x1));
+            l2[1] = add2(l2[1], pair(x2, x3));
+            p[e] = pack_bf16(x0, x1);
+            p[e + 1] = pack_bf16(x2, x3);
+            low[e] = bf16_rest(x0, x1, p[e]);
+            low[e + 1] = bf16_rest(x2, x3, p[e + 1]);
+          }
+          tmem_st16(ts + i * 16, p);
+          tmem_st16(ts + 64 + i * 16, low);
+        }
+        float la, lb, lc, ld;
+        unpair(l2[0], la, lb);
+        unpair(l2[1], lc, ld);
+        l += (la + lb) + (lc + ld);
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[g]);
+    }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[g], 0));
+    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    fence_after();
+    const size_t pi = (((size_t)blockIdx.y * c.n_kv_heads + kh) * 256) + tile * kRows + r;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + (size_t)head * HD;
+    auto store = [&](int c0, float* v, float f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= f;
+      if (it.chunks > 1) {
+        float* po = A.part_o + pi * HD + c0;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(po + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          *reinterpret_cast<uint4*>(out + c0 + e) = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
+                                                               pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
+      }
+    };
+    if (two) {
+      if (ok) {
+        const float r1 = Q8 ? unit_sum(m, l) : 1.f;
+        const float f = it.chunks > 1 ? r1 : l == 0.f ? 0.f : r1 / l;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 16) {
+          float v[16];
+          if (n > 0) {
+            tmem_ld16(to + c0, v);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          }
+          store(c0, v, f);
+        }
+        if (it.chunks > 1) A.part_ml[pi] = make_float2(m, l);
+      }
+    } else {
+      // The groups' halves: each has waited for its own accumulator's last product, and reads the other's too, which
+      // these fences order behind the other group's wait.
+      xch[g * kRows + r] = make_float2(m, l);
+      fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      fence_after();
+      if (ok) {
+        float2 e0 = xch[r], e1 = xch[kRows + r];
+        const float r0 = Q8 ? unit_sum(e0.x, e0.y) : 1.f, r1 = Q8 ? unit_sum(e1.x, e1.y) : 1.f;
+        const float mj = fmaxf(e0.x, e1.x);
+        const float f0 = e0.x == -INFINITY ? 0.f : ex2(e0.x - mj), f1 = e1.x == -INFINITY ? 0.f : ex2(e1.x - mj);
+        const float lj = e0.y * f0 + e1.y * f1;
+        const float f = it.chunks > 1 ? 1.f : lj == 0.f ? 0.f : 1.f / lj;
+        const uint32_t t0 = trow + G::O_COL;
+#pragma unroll 1
+        for (int c0 = g * 16; c0 < HD; c0 += 32) {
+          float v[16], w[16];
+          if (nb > 0) tmem_ld16(t0 + c0, v);
+          if (nb > 1) tmem_ld16(t0 + kRows + c0, w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = (nb > 0 ? v[e] * (f0 * r0) : 0.f) + (nb > 1 ? w[e] * (f1 * r1) : 0.f);
+          store(c0, v, f);
+        }
+        if (it.chunks > 1 && g == 0) A.part_ml[pi] = make_float2(mj, lj);
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// Adds up the ranges of keys of the requests that were cut.  A warp takes a token's row of one head; x: double tile
+// and its rows, 8 warps each.  Latency bounds it.
+template <int HD>
+__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ Args A) {
+  pdl_wait();
+  pdl_trigger();
+  const int4 info = A.info[blockIdx.x];
+  const int chunks = info.w & 0xFFFF, nt = info.w >> 16;
+  if (chunks < 2) return;
+  const cdb_prompt_attention_args& a = A.a;
+  const int lane = threadIdx.x & 31, w = blockIdx.z * 8 + (threadIdx.x >> 5), kh = blockIdx.y;
+  const int tile = w / kRows, r = w % kRows, tk = info.y + tile * A.tokens + r / A.group;
+  const int row0 = a.row_start[info.x], count = a.row_start[info.x + 1] - row0;
+  if (r >= A.tokens * A.group || tk >= count) return;
+  constexpr int E = HD / 32;
+  const size_t p0 = ((size_t)info.z * a.cache.n_kv_heads + kh) * 256 + w, step = (size_t)nt * a.cache.n_kv_heads * 256;
+  float mj = -INFINITY;
+  for (int k = lane; k < chunks; k += 32) mj = fmaxf(mj, A.part_ml[p0 + k * step].x);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, o));
+  float l = 0.f, v[E] = {};
+#pragma unroll 4
+  for (int k = 0; k < chunks; ++k) {
+    const float2 ml = A.part_ml[p0 + k * step];
+    const float f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - mj);
+    const float* po = A.part_o + (p0 + k * step) * HD + lane * E;
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = fmaf(po[e], f, v[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)(row0 + tk) * a.ldo + (size_t)(kh * A.group + r % A.group) * HD + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(v[e] * inv);
+}
+
+struct Plan {
+  int group, tokens, tiles, cut;
+  size_t o_bytes, ml_bytes, info_bytes;
+};
+
+Plan plan(int rows, int requests, int n_heads, int n_kv_heads, int head_dim, int max_ctx) {
+  Plan p = {};
+  p.group = n_heads / n_kv_heads;
+  p.tokens = kRows / p.group;
+  // sum of ceil(count / (2 tokens)) over requests that have rows
+  p.tiles = (int)std::min<long long>(rows, rows / (2 * p.tokens) + requests);
+  // Cut only where a call may leave SMs without work for long: few items, and enough keys to cut.
+  const long long items = (long long)p.tiles * n_kv_heads;
+  const bool may = max_ctx > kMinBlocks * kKeys && items < kCutBelow;
+  p.cut = may ? (kItems + n_kv_heads - 1) / n_kv_heads : 0;
+  const size_t cells = may ? (size_t)(p.tiles + p.cut) * n_kv_heads * 256 : 0;
+  p.o_bytes = cells * head_dim * 4;
+  p.ml_bytes = cells * 8;
+  p.info_bytes = may ? ((size_t)p.tiles * 16 + 255) / 256 * 256 : 0;
+  return p;
+}
+
+template <int HD, bool Q8>
+cudaError_t launch(cudaStream_t s, const Args& A) {
+  using G = Geo<HD, Q8>;
+  const cdb_paged_cache& c = A.a.cache;
+  CUtensorMap tk = {};
+  const uint64_t rows = (uint64_t)c.kv_blocks * c.n_kv_slots * 2 * c.n_kv_heads * 16;
+  // A page is a box of 16 rows of 128 bytes; what a row has less is filled with zeros.
+  if (!Q8 && !tmap_u8_2d(&tk, c.pool, HD * 2, rows, HD * 2, 128, 16, 128)) return cudaErrorInvalidValue;
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (!set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(k_prompt<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  count_launch();
+  cudaError_t e = launch_pdl(k_prompt<HD, Q8>, dim3(c.n_kv_heads, A.tiles + A.cut), dim3(G::THREADS), G::SMEM, s, tk, A);
+  if (e != cudaSuccess || !A.cut) return e;
+  count_launch();
+  return launch_pdl(k_prompt_join<HD>, dim3(A.tiles, c.n_kv_heads, 32), dim3(256), 0, s, A);
+}
+
+}  // namespace pa
+
+size_t prompt_attention_workspace(int rows, int requests, int n_heads, int n_kv_heads, int head_dim, int max_ctx) {
+  // Smaller calls may cut where this one does not: the most tiles that a call that cuts has.
+  const pa::Plan p = pa::plan(rows, requests, n_heads, n_kv_heads, head_dim, max_ctx);
+  if (max_ctx <= pa::kMinBlocks * pa::kKeys) return 256;
+  const size_t tiles = std::min(p.tiles, (pa::kCutBelow - 1) / n_kv_heads);
+  const size_t cells = (tiles * n_kv_heads + pa::kItems + n_kv_heads) * 256;
+  return cells * (head_dim * 4 + 8) + tiles * 16 + 512;
+}
+
+cudaError_t launch_prompt_attention(cudaStream_t s, const cdb_prompt_attention_args& a) {
+  const pa::Plan p = pa::plan(a.rows, a.requests, a.n_heads, a.cache.n_kv_heads, a.cache.head_dim, a.max_ctx);
+  pa::Args A;
+  A.a = a;
+  A.group = p.group;
+  A.tokens = p.tokens;
+  A.cut = p.cut;
+  A.tiles = p.tiles;
+  A.info = static_cast<int4*>(a.workspace);
+  A.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.info_bytes);
+  A.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(A.part_o) + p.o_bytes);
+  const bool q8 = a.cache.dtype == CDB_E4M3;
+  switch (a.cache.head_dim) {
+    case 32: return q8 ? pa::launch<32, true>(s, A) : pa::launch<32, false>(s, A);
+    case 64: return q8 ? pa::launch<64, true>(s, A) : pa::launch<64, false>(s, A);
+    case 96: return q8 ? pa::launch<96, true>(s, A) : pa::launch<96, false>(s, A);
+    case 128: return q8 ? pa::launch<128, true>(s, A) : pa::launch<128, false>(s, A);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace cdb

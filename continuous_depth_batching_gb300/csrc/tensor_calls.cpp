@@ -160,10 +160,112 @@ PyObject* attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return h.call();
 }
 
+// A contiguous vector of int64.
+bool vec64(PyObject* o, int dev, int64_t n, const void** p, bool needed) { return vec(o, dev, at::kLong, n, p, needed); }
+
+// (fn, args, stream, dev, x, pos, out)
+PyObject* rotate(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  Head<cdb_rotate_args> h;
+  if (n != 7 || !h.get(v)) return wrong_call();
+  try {
+    cdb_rotate_args& a = *h.a;
+    const int64_t width = ((int64_t)a.n_heads + a.n_kv_heads) * a.head_dim;
+    int to, most;
+    if (!input(v[4], h.dev, &a.dtype, &a.rows, INT_MAX, width, &a.x, &a.ldx) ||
+        !vec(v[5], h.dev, at::kInt, a.rows, (const void**)&a.pos, true) ||
+        !input(v[6], h.dev, &to, &most, INT_MAX, width, (const void**)&a.out, &a.ldo) || to != a.dtype || most < a.rows)
+      Py_RETURN_NONE;
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+  return h.call();
+}
+
+// (fn, args, stream, dev, state, lens, new_tokens, seq, state_out, lens_out); requests: what lens has
+PyObject* plan_pages(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  Head<cdb_plan_pages_args> h;
+  if (n != 10 || !h.get(v)) return wrong_call();
+  try {
+    cdb_plan_pages_args& a = *h.a;
+    const at::Tensor* lens = tensor(v[5], h.dev);
+    if (!lens || lens->dim() != 1 || lens->numel() > INT_MAX) Py_RETURN_NONE;
+    a.requests = (int)lens->numel();
+    if (!vec64(v[4], h.dev, 2, (const void**)&a.state, true) || !vec(v[5], h.dev, at::kInt, a.requests, (const void**)&a.lens, true) ||
+        !vec(v[6], h.dev, at::kInt, a.requests, (const void**)&a.new_tokens, true) ||
+        !vec(v[7], h.dev, at::kInt, a.requests, (const void**)&a.seq, false) ||
+        !vec64(v[8], h.dev, 2, (const void**)&a.state_out, true) ||
+        !vec(v[9], h.dev, at::kInt, a.requests, (const void**)&a.lens_out, true))
+      Py_RETURN_NONE;
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+  return h.call();
+}
+
+// (fn, args, stream, dev, max_rows, max_requests, q, row_start, lens, visible, seq, slot, out); requests: what lens has
+PyObject* prompt_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  Head<cdb_prompt_attention_args> h;
+  int most, most_requests;
+  if (n != 13 || !h.get(v) || !get_int(v[4], &most) || !get_int(v[5], &most_requests) || !get_int(v[11], &h.a->slot))
+    return wrong_call();
+  try {
+    cdb_prompt_attention_args& a = *h.a;
+    const int64_t width = (int64_t)a.n_heads * a.cache.head_dim;
+    int dtype;
+    const at::Tensor* lens = tensor(v[8], h.dev);
+    if (!lens || lens->dim() != 1 || lens->numel() > most_requests) Py_RETURN_NONE;
+    a.requests = (int)lens->numel();
+    if (!input(v[6], h.dev, &dtype, &a.rows, most, width, &a.q, &a.ldq) || dtype != CDB_BF16 ||
+        !vec(v[7], h.dev, at::kInt, (int64_t)a.requests + 1, (const void**)&a.row_start, true) ||
+        !vec(v[8], h.dev, at::kInt, a.requests, (const void**)&a.lens, true) ||
+        !vec(v[10], h.dev, at::kInt, a.requests, (const void**)&a.seq, false) ||
+        !bf16_mat(v[12], h.dev, a.rows, width, (const void**)&a.out, &a.ldo))
+      Py_RETURN_NONE;
+    a.visible = nullptr;
+    if (a.mask_words) {
+      const at::Tensor* m = tensor(v[9], h.dev);
+      if (!m || m->scalar_type() != at::kLong || m->dim() != 2 || m->size(0) < a.rows || m->size(1) != a.mask_words ||
+          !m->is_contiguous())
+        Py_RETURN_NONE;
+      a.visible = static_cast<const uint64_t*>(m->data_ptr());
+    }
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+  return h.call();
+}
+
+// (fn, args, stream, dev, base, path, keep, seq); requests: what base has
+PyObject* keep_path(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  Head<cdb_keep_path_args> h;
+  if (n != 8 || !h.get(v)) return wrong_call();
+  try {
+    cdb_keep_path_args& a = *h.a;
+    const at::Tensor *base = tensor(v[4], h.dev), *path = tensor(v[5], h.dev);
+    if (!base || base->dim() != 1 || base->numel() > INT_MAX || !path || path->dim() != 2 || path->scalar_type() != at::kInt ||
+        path->size(1) > INT_MAX)
+      Py_RETURN_NONE;
+    a.requests = (int)base->numel();
+    a.max_path = (int)path->size(1);
+    if (!vec(v[4], h.dev, at::kInt, a.requests, (const void**)&a.base, true) ||
+        !mat(*path, a.requests, a.max_path, (const void**)&a.path, &a.ld_path) ||
+        !vec(v[6], h.dev, at::kInt, a.requests, (const void**)&a.keep, true) ||
+        !vec(v[7], h.dev, at::kInt, a.requests, (const void**)&a.seq, false))
+      Py_RETURN_NONE;
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+  return h.call();
+}
+
 PyMethodDef kMethods[] = {
     {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {"cache_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_write)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
+    {"rotate", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotate)), METH_FASTCALL, nullptr},
+    {"plan_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan_pages)), METH_FASTCALL, nullptr},
+    {"prompt_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prompt_attention)), METH_FASTCALL, nullptr},
+    {"keep_path", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(keep_path)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "cdb_tensor_calls", nullptr, -1, kMethods};
 

@@ -1,7 +1,9 @@
 /*
- * cdb_ops.h — operators of one decode step for programs that drive the model
- * themselves: write a token's keys and values to the paged cache, attend to
- * the cache, pick the next token from the logits.  The engine of cdb.h runs
+ * cdb_ops.h — operators of a step for programs that drive the model
+ * themselves: plan pages and rows, rotate queries and keys, write a token's keys
+ * and values to the paged cache, attend to the cache (one token per row, whole
+ * prompts, drafted tokens), pick the next token from the logits, keep the
+ * accepted part of a draft.  The engine of cdb.h runs
  * the same steps inside cdb_step_core and cdb_step_boundary; requests admitted
  * with cdb_admit_sampled use the sampler below.
  *
@@ -89,6 +91,8 @@ typedef struct {
 #define CDB_OPS_BAD_ROW 8     /* sequence or position out of range */
 #define CDB_OPS_TIMEOUT 32    /* a bounded wait inside a kernel expired */
 #define CDB_OPS_NOT_SHARED 128 /* rows name different blocks inside shared_len */
+#define CDB_OPS_NO_BLOCKS 256 /* pages: fewer free blocks than the requests need */
+#define CDB_OPS_NO_ROWS 512   /* pages: more new tokens than max_rows */
 
 /* ------------------------------------------------------------- cache write
  * Row i of qkv holds n_heads query heads, n_kv_heads key heads and n_kv_heads
@@ -171,6 +175,149 @@ int cdb_attention(const cdb_attention_args *a, void *stream);
 /* Workspace for a call of this many rows; shared_len < 0: for any shared_len
  * and any number of rows up to this.  0 for arguments cdb_attention refuses. */
 size_t cdb_attention_workspace(int rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx, int shared_len);
+
+/* --------------------------------------------------------- pages and rows
+ * Block tables and packed rows from the lengths of a step's requests, and the
+ * blocks of dropped tokens back to the free list.  Request i is sequence seq[i]
+ * with lens[i] cached tokens.  new_tokens[i] >= 0 adds that many: blocks for its
+ * pages ceil(lens / 16) .. ceil((lens + new) / 16) - 1 are taken, and it gets
+ * rows row_start[i] .. row_start[i + 1] - 1, row r with row_seq[r] = seq[i], the
+ * next positions in row_pos[r], and row_slot[r] = 16 * block + position % 16.
+ * new_tokens[i] < 0 drops that many of its last tokens (all, if it has fewer):
+ * blocks of its pages from ceil(what is left / 16) on are given back.
+ * Free blocks are the entries state[0] .. state[1] - 1, modulo free_slots, of the
+ * ring `free_blocks`: blocks are taken at state[0] and given at state[1], requests
+ * and pages in ascending order, and blocks that a call gives are not taken by it.
+ * lens_out[i] is the new length and state_out the new counters; they may be lens
+ * and state themselves.  Rows from row_start[requests] to max_rows - 1 are padding:
+ * row_seq, row_pos and row_slot -1.  Table entries behind a sequence's last page
+ * are left as they were.  A sequence is named by one request at most.
+ * A call that cannot be served in full changes nothing: it sets a status bit
+ * (CDB_OPS_NO_BLOCKS; CDB_OPS_NO_ROWS; CDB_OPS_BAD_ROW: a sequence, length or
+ * counter out of range, or pages past max_blocks), lens_out and state_out are as
+ * before, row_start is 0 and every row padding. */
+#define CDB_PLAN_MAX_REQUESTS 8192
+typedef struct {
+  int requests;                 /* <= CDB_PLAN_MAX_REQUESTS */
+  const int32_t *lens, *new_tokens; /* [requests] */
+  const int32_t *seq;           /* [requests], or NULL: request i is sequence i */
+  int32_t *block_table;         /* [n_seqs][max_blocks] */
+  int n_seqs, max_blocks;
+  int32_t *free_blocks;         /* [free_slots] */
+  int free_slots;
+  const int64_t *state;         /* [2]: blocks taken and given so far */
+  int64_t *state_out;           /* [2] */
+  int32_t *lens_out;            /* [requests] */
+  int32_t *row_start;           /* [requests + 1] */
+  int32_t *row_seq, *row_pos;   /* [max_rows] */
+  int64_t *row_slot;            /* [max_rows], or NULL */
+  int max_rows;
+  int32_t *status;
+} cdb_plan_pages_args;
+int cdb_plan_pages(const cdb_plan_pages_args *a, void *stream);
+
+/* --------------------------------------------------------------- rotation
+ * Query / key norm and rotary positions of rows whose positions are not their
+ * places in the cache, or that cdb_cache_write's table does not cover: pairs of
+ * neighbours, scaled angles, far positions, drafted tokens (which share a depth).
+ * A row of x holds n_heads query heads, then n_kv_heads key heads.  In fp32: with
+ * gains, each head becomes x / sqrt(mean x^2 + eps) * gain; then pair j < rot_dim /
+ * 2 is turned by the angle of 2 pi * (pos * steps[j] mod 2^64) / 2^64 and
+ * multiplied by `factor`; elements behind rot_dim are left as they are.  A pair
+ * is (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved.  Angles are exact sums of
+ * a 64-bit fraction of a turn, whatever the position.
+ * out may be x itself; otherwise they do not overlap.  A row with pos < 0 is
+ * padding: nothing of it is read or written. */
+typedef struct {
+  int rows, n_heads, n_kv_heads, head_dim; /* head_dim 32, 64, 96 or 128 */
+  const void *x;          /* [rows][ldx], ldx >= (n_heads + n_kv_heads) head_dim; 16-byte aligned rows */
+  int dtype;              /* CDB_FP32 or CDB_BF16, of out too */
+  int64_t ldx;
+  const int32_t *pos;     /* [rows] */
+  const uint64_t *steps;  /* [rot_dim / 2]: turns per position, times 2^64 */
+  int rot_dim;            /* a multiple of 16, <= head_dim */
+  int interleaved;
+  float factor;           /* of cos and sin; finite */
+  const float *q_gain, *k_gain; /* [head_dim] each, or both NULL: no norm */
+  float eps;
+  void *out;              /* [rows][ldo]; 16-byte aligned rows */
+  int64_t ldo;
+} cdb_rotate_args;
+int cdb_rotate(const cdb_rotate_args *a, void *stream);
+
+/* ------------------------------------------- attention of prompts and drafts
+ * Request i has query rows row_start[i] .. row_start[i + 1] - 1, its last
+ * tokens: lens[i] counts its cached tokens, these among them, so row t of n is at
+ * position lens - n + t.  Their keys and values are in the cache (slot `slot`) before the
+ * call.  o = sum_j softmax_j(scale * q . k_j) v_j per head, query head h reading
+ * KV head h / (n_heads / n_kv_heads), over the positions j that the row sees:
+ *   cdb_prompt_attention  all up to its own;
+ *   cdb_draft_attention   all before the request's rows, and of those the ones
+ *                         whose bits are set in the row's mask: bit u % 64 of
+ *                         visible[row][u / 64] for row u of the request (a tree's
+ *                         nodes: its ancestors and itself).  Bits of rows that the
+ *                         request does not have are ignored.
+ * A row that sees nothing gives zeros.  Rows behind row_start[requests] are left as
+ * they were.  Softmax statistics and sums are fp32; weights enter the products
+ * as 16-bit numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache,
+ * one, weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
+ * With an e4m3 cache a query's elements are exact down to 2^-17 of the head's largest
+ * one, smaller ones within 2^-25 of that.
+ * Keys and values that no row sees may hold anything.  Inside the stretch that
+ * some rows of a request see and others do not, a value with an infinite or NaN
+ * element makes the rows that see it NaN in all elements of the head, and does not
+ * touch the others.
+ * Where a call has less work than the GPU has room for, keys are cut among CTAs
+ * and joined, by the lengths of all its requests: this changes roundings, never
+ * from one run to the next.
+ * workspace: cdb_prompt_attention_workspace() bytes, 256-byte aligned, any
+ * contents; used by one call at a time. */
+#define CDB_DRAFT_MAX 256
+typedef struct {
+  cdb_paged_cache cache;
+  int rows, n_heads;        /* rows of q and out; at most 128 query heads per KV head */
+  const void *q;            /* bf16 [rows][ldq]; 16-byte aligned rows */
+  int64_t ldq;
+  int requests;
+  const int32_t *row_start; /* [requests + 1], ascending, row_start[0] >= 0 */
+  const int32_t *lens;      /* [requests] */
+  const int32_t *seq;       /* [requests], or NULL: request i is sequence i; < 0: skipped */
+  int slot;
+  float scale;              /* finite */
+  int max_ctx;              /* every length <= max_ctx (checked on the device), <= max_blocks * 16 */
+  const uint64_t *visible;  /* draft: [rows][mask_words]; prompt: NULL */
+  int mask_words;           /* draft: 1 .. CDB_DRAFT_MAX / 64; a request has at most 64 mask_words rows */
+  void *out;                /* bf16 [rows][ldo]; 16-byte aligned rows */
+  int64_t ldo;
+  int32_t *status;
+  void *workspace;
+  size_t workspace_bytes;
+} cdb_prompt_attention_args;
+int cdb_prompt_attention(const cdb_prompt_attention_args *a, void *stream);
+int cdb_draft_attention(const cdb_prompt_attention_args *a, void *stream);
+/* Workspace for any call of up to this many rows and requests.  0 for arguments that are refused. */
+size_t cdb_prompt_attention_workspace(int rows, int requests, int n_heads, int n_kv_heads, int head_dim, int max_ctx);
+
+/* ---------------------------------------------------------- accepted drafts
+ * Moves the cached keys, values and scales of a draft's accepted nodes to the
+ * positions they have in the text, in every slot: entry k < keep[i] of request i
+ * from position base[i] + path[i][k] to base[i] + k.  path ascends strictly from
+ * path[i][0] >= 0.  keep[i] = 0 moves nothing.  The positions behind are left
+ * as they were (drop them with cdb_plan_pages).  A request with seq < 0 is
+ * skipped; one with a sequence, node or position out of range sets
+ * CDB_OPS_BAD_ROW and moves nothing.  A sequence is named by one request at most. */
+typedef struct {
+  cdb_paged_cache cache;
+  int requests;
+  const int32_t *base;     /* [requests] */
+  const int32_t *path;     /* [requests][ld_path] */
+  int64_t ld_path;         /* >= max_path */
+  int max_path;            /* 1 .. CDB_DRAFT_MAX */
+  const int32_t *keep;     /* [requests], <= max_path */
+  const int32_t *seq;      /* [requests], or NULL: request i is sequence i */
+  int32_t *status;
+} cdb_keep_path_args;
+int cdb_keep_path(const cdb_keep_path_args *a, void *stream);
 
 #ifdef __cplusplus
 }
