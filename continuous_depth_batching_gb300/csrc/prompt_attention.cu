@@ -14,7 +14,7 @@
 //   one tile    the groups take even and odd blocks of the same rows, and are joined
 //               at the end.
 // Either way the tensor cores work for one group while the other is in its
-// exponentials.  Jobs (block, group) go in order t = 0, 1, ..; t + 2 is the same group's next.
+// exponentials.
 //   warps 0-7    softmax: a thread reads the 128 scores of its row from TMEM, masks
 //                them, and writes the weights over them in 16 bits, the A operand of
 //                the second product.  bf16 weights are two numbers, what the first
@@ -68,14 +68,16 @@ struct Geo {
   // e4m3: units of 64 keys of K or V, as they come: codes, then their scales.
   static constexpr int UNIT = 64 * HD + 64 * 4;
   static constexpr int NU = NX == 2 ? 3 : 6;
+  static constexpr int NT = 8;                    // blocks whose end is told apart: more than a ring's slots and three
+  static constexpr int NSC = 4;                   // blocks whose scales are kept
   static constexpr int SCN = 3 * kKeys + 4;       // scales of K, of V, the latter's logarithms, the largest of those by quarters
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + KS * TILE;
   static constexpr int OFF_U = OFF_V + VS * TILE;
   static constexpr int OFF_SC = OFF_U + (Q8 ? NU * UNIT : 0);
-  static constexpr int OFF_BAD = OFF_SC + (Q8 ? VS * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
+  static constexpr int OFF_BAD = OFF_SC + (Q8 ? NSC * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
   static constexpr int OFF_BAR = OFF_BAD + VS * (Q8 ? kKeys : 16);
-  static constexpr int NBAR = 2 + 2 * KS + 3 * VS + 2 + 2 + 2 + 1 + 2 * 6;
+  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 6;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int THREADS = Q8 ? 512 : 384;
   static constexpr int S_COL = 256;               // [2][128] scores, then weights
@@ -119,8 +121,49 @@ __device__ __forceinline__ bool look(const Args& A, int i, Item& it, bool tell) 
 // request its cut ranges of keys, of those its double tiles, the last (most keys) first.
 // A request's keys are cut into ranges of `cb` blocks, the same for the whole call, such
 // that all of it makes about kItems items.
+// Up to 32 requests: every warp by itself, without a barrier.
+__device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
+  const cdb_prompt_attention_args& a = A.a;
+  const int lane = threadIdx.x & 31, step = 2 * A.tokens;
+  const bool tell = blockIdx.x == 0 && y == 0 && threadIdx.x < 32;
+  Item it = {};
+  const bool on = lane < a.requests && look(A, lane, it, tell);
+  const int nt = on ? div_up(it.count, step) : 0, blocks = max(1, div_up(it.len, kKeys));
+  int cb = INT_MAX / kKeys;
+  if (A.cut) {
+    const int work = __reduce_add_sync(0xffffffffu, on ? nt * blocks : 0);  // cutting calls have few tiles
+    cb = max(kMinBlocks, div_up(work, A.cut));
+  }
+  const int nc = on ? div_up(blocks, cb) : 0;
+  int xi = nt * nc, xt = nt;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
+    if (lane >= o) xi += p, xt += q;
+  }
+  const int tiles = __shfl_sync(0xffffffffu, xt, 31);
+  xi -= nt * nc, xt -= nt;
+  const uint32_t mine = __ballot_sync(0xffffffffu, on && y >= xi && y < xi + nt * nc);
+  if (A.cut && tell) {  // for the join
+    if (on)
+      for (int k = 0; k < nt; ++k) A.info[xt + k] = make_int4(lane, k * step, xi + nt - 1 - k, nc | (nt << 16));
+    for (int t = tiles + lane; t < A.tiles; t += 32) A.info[t] = make_int4(0, 0, 0, 0);
+  }
+  const int from = mine ? __ffs(mine) - 1 : 0;
+  const int k = y - xi, tile = nt ? nt - 1 - k % nt : 0;
+  it.t0 = tile * step;
+  it.chunk = nt ? k / nt : 0, it.chunks = nc, it.cb = cb;
+  it.tile = xt + tile;
+  int* f = reinterpret_cast<int*>(&it);
+#pragma unroll
+  for (int e = 0; e < (int)(sizeof(Item) / 4); ++e) f[e] = __shfl_sync(0xffffffffu, f[e], from);
+  if (!mine) it.tile = -1;
+  return it;
+}
+
 template <int THREADS>
 __device__ __forceinline__ Item find_item(const Args& A, int y) {
+  if (A.a.requests <= 32) return find_item_warp(A, y);
   __shared__ int sh[THREADS / 32][2];
   __shared__ long long work_s[THREADS / 32];
   __shared__ Item found;
@@ -194,6 +237,51 @@ __device__ __forceinline__ uint32_t seen(int s, int lim, const uint32_t* mask, i
   return w;
 }
 
+// The products of one job, each issued as one piece: one lane is elected inside, and descriptors
+// are made from 32-bit words by additions of constants.  (A call for every 128 x 128 x 16 product
+// took its warp 65 cycles to issue, as long as it takes to compute.)
+#define CDB_SS(off, acc)                                                                         \
+  " add.u32 x, %1, " off ";\n mov.b64 da, {x, %3};\n add.u32 x, %2, " off ";\n mov.b64 db, {x, %3};\n" \
+  " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " acc ";\n"
+#define CDB_SS_BEGIN                                                                  \
+  "{\n .reg .pred q, f, t;\n .reg .b32 x;\n .reg .b64 da, db;\n setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n" \
+  " elect.sync _|q, 0xffffffff;\n"
+// S[tmem] = Q K^T; q, k: lower words of the descriptors, whose upper words are the same.
+template <int STEPS>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t upper, uint32_t id) {
+  static_assert(STEPS == 2 || STEPS == 4 || STEPS == 6 || STEPS == 8, "head dim");
+  if constexpr (STEPS == 2)
+    asm volatile(CDB_SS_BEGIN CDB_SS("0", "f") CDB_SS("2", "t") "}\n" ::"r"(d), "r"(q), "r"(k), "r"(upper), "r"(id) : "memory");
+  if constexpr (STEPS == 4)
+    asm volatile(CDB_SS_BEGIN CDB_SS("0", "f") CDB_SS("2", "t") CDB_SS("4", "t") CDB_SS("6", "t") "}\n" ::"r"(d), "r"(q), "r"(k),
+                 "r"(upper), "r"(id)
+                 : "memory");
+  if constexpr (STEPS == 6)
+    asm volatile(CDB_SS_BEGIN CDB_SS("0", "f") CDB_SS("2", "t") CDB_SS("4", "t") CDB_SS("6", "t") CDB_SS("1024", "t")
+                     CDB_SS("1026", "t") "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+  if constexpr (STEPS == 8)
+    asm volatile(CDB_SS_BEGIN CDB_SS("0", "f") CDB_SS("2", "t") CDB_SS("4", "t") CDB_SS("6", "t") CDB_SS("1024", "t")
+                     CDB_SS("1026", "t") CDB_SS("1028", "t") CDB_SS("1030", "t") "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+}
+// O[tmem] (+)= P[tmem] V over `steps` pages of 16 keys (all eight where FULL).
+#define CDB_TS(n, a, off, acc)                                                              \
+  " setp.gt.s32 s, %5, " n ";\n and.pred s, s, q;\n add.u32 x, %1, " a ";\n add.u32 y, %2, " off ";\n mov.b64 db, {y, %3};\n" \
+  " @s tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, " acc ";\n"
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t p, uint32_t v, uint32_t upper, uint32_t id, int steps,
+                                             bool add) {
+  asm volatile(
+      "{\n .reg .pred q, f, t, s;\n .reg .b32 x, y;\n .reg .b64 db;\n setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, %6, 0;\n"
+      " elect.sync _|q, 0xffffffff;\n" CDB_TS("0", "0", "0", "f") CDB_TS("1", "8", "128", "t") CDB_TS("2", "16", "256", "t")
+          CDB_TS("3", "24", "384", "t") CDB_TS("4", "32", "512", "t") CDB_TS("5", "40", "640", "t")
+              CDB_TS("6", "48", "768", "t") CDB_TS("7", "56", "896", "t") "}\n" ::"r"(d),
+      "r"(p), "r"(v), "r"(upper), "r"(id), "r"(steps), "r"((int)add)
+      : "memory");
+}
+
 template <int HD, bool Q8>
 __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     k_prompt(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ Args A) {
@@ -205,15 +293,15 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint8_t* bad_bytes = smem + G::OFF_BAD;
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);  // [2]
   uint64_t* k_full = q_ready + 2;
-  uint64_t* k_empty = k_full + G::KS;
-  uint64_t* v_full = k_empty + G::KS;
-  uint64_t* v_empty = v_full + G::VS;
-  uint64_t* v_clean = v_empty + G::VS;   // blocks that were looked through
-  uint64_t* s_full = v_clean + G::VS;    // [2] by group
+  uint64_t* v_full = k_full + G::KS;
+  uint64_t* v_clean = v_full + G::VS;    // blocks that were looked through
+  uint64_t* taken = v_clean + G::VS;     // V of this block, and K of the next, are free
+  uint64_t* s_full = taken + G::NT;      // [2] by group
   uint64_t* p_full = s_full + 2;
   uint64_t* o_final = p_full + 2;
   uint64_t* done = o_final + 2;
-  uint64_t* u_full = done + 1;           // [NU <= 6]
+  uint64_t* k_first = done + 1;          // K of the groups' first blocks is free
+  uint64_t* u_full = k_first + 1;        // [NU <= 6]
   uint64_t* u_empty = u_full + 6;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + 6);
 
@@ -231,14 +319,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     }
     for (int s = 0; s < G::KS; ++s) {
       mbar_init(&k_full[s], Q8 ? 4 : 1);
-      mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < G::VS; ++s) {
       mbar_init(&v_full[s], Q8 ? 4 : 1);
-      mbar_init(&v_empty[s], 1);
       mbar_init(&v_clean[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(k_first, 1);
+    for (int s = 0; s < G::NT; ++s) mbar_init(&taken[s], 1);
     for (int s = 0; s < 6; ++s) {
       mbar_init(&u_full[s], 1);
       mbar_init(&u_empty[s], 4);
@@ -250,6 +338,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   pdl_trigger();
   const Item it = find_item<G::THREADS>(A, blockIdx.y);
   if (it.tile < 0) return;
+  const int tt = A.tokens;
+  const int n_tok = min(2 * tt, it.count - it.t0);      // tokens of this item
+  const bool two = n_tok > tt;
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -259,9 +350,6 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int tt = A.tokens;
-  const int n_tok = min(2 * tt, it.count - it.t0);      // tokens of this item
-  const bool two = n_tok > tt;
   const int before = it.len - it.count;                 // position of the request's first token; < 0: that many see nothing
   // Keys that a tile's rows may see, all of them together: the end of the last.
   auto end_of = [&](int last_token) { return a.visible ? it.len : min(it.len, max(0, before + last_token + 1)); };
@@ -273,9 +361,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   // Blocks from this one on are not seen whole by every row: they are looked through.
   const int whole = max(0, a.visible ? before : before + it.t0 + 1) / kKeys - b_lo;
   const int first_part = max(0, min(nb, whole));
-  const int jobs = two ? 2 * nb : nb;
-  auto block_of = [&](int t) { return two ? t >> 1 : t; };
-  auto valid = [&](int t) { return t < jobs && (!two || (t & 1) || (t >> 1) < nb0); };
+
+  auto wait_taken = [&](int b) { return mbar_wait(&taken[b % G::NT], (b / G::NT) & 1); };
+  // K of block j may be written: the scores of the block that its slot held were issued with the job of the same group
+  // before, a block earlier with two tiles, two with one.
+  auto wait_k = [&](int j) {
+    const int gone = j - G::KS - (two ? 1 : 2);
+    return gone < 0 ? mbar_wait(k_first, 0) : wait_taken(gone);
+  };
 
   static_assert(!Q8 || 256 * 176 + 256 * 80 <= 512 * 128, "registers of the launch");
   static_assert(Q8 || 256 * 208 + 128 * 72 <= 384 * 168, "registers of the launch");
@@ -284,56 +377,54 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 9) {
       // ---------------- products ----------------
+      // Jobs (block, group) in order t = 0, 1, ..; t + 2 is the same group's next.  The waits and commits of a job take
+      // its warp nearly as long as the tensor cores take to compute it.  So both products of a job are issued in one go, after
+      // one wait for all they need (lane 1 for the weights, lane 2 for the next keys, the others for the values), and
+      // there is one commit for the scores and one for a block's K and V.
       constexpr uint32_t idS = idesc_16(!Q8, kRows, kKeys, false), idO = idesc_16(!Q8, kRows, HD, true);
-      const uint64_t qd = desc_k(su32(smem), 1024), kd = desc_k(su32(smem + G::OFF_K), 1024);
-      const uint64_t vd = desc_mn(su32(smem + G::OFF_V), G::SLICE, 1024);
-      bool ok = true;
-      auto scores = [&](int t) {
-        const int b = block_of(t), g = t & 1, s = b % G::KS;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&k_full[s], (b / G::KS) & 1)))) return;
-        fence_after();
-        const uint64_t qb = qd + (uint32_t)((two ? g : 0) * (G::TILE / 16)), kb = kd + (uint32_t)(s * (G::TILE / 16));
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t at = ((kk / 4) * G::SLICE + (kk % 4) * 32) / 16;
-            mma_ss(tmem + G::S_COL + g * kKeys, qb + at, kb + at, idS, kk > 0 ? 1u : 0u);
-          }
-          commit(&s_full[g]);
-          if (!two || g == 1) commit(&k_empty[s]);
-        }
-        __syncwarp();
+      const uint32_t q = (uint32_t)desc_k(su32(smem), 1024), k = (uint32_t)desc_k(su32(smem + G::OFF_K), 1024);
+      const uint32_t v = (uint32_t)desc_mn(su32(smem + G::OFF_V), G::SLICE, 1024);
+      const uint32_t up_k = (uint32_t)(desc_k(0, 1024) >> 32), up_v = (uint32_t)(desc_mn(0, G::SLICE, 1024) >> 32);
+      const int jobs = two ? 2 * nb : nb;
+      auto scores = [&](int b, int g) {
+        issue_scores<HD / 16>(tmem + G::S_COL + g * kKeys, q + (two ? g : 0) * (G::TILE / 16), k + (b % G::KS) * (G::TILE / 16),
+                              up_k, idS);
       };
+      bool ok = true;
       for (int g = 0; ok && g < 2; ++g) {
-        if (!valid(g)) continue;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_ready[two ? g : 0], 0)))) break;
-        scores(g);
-      }
-      for (int t = 0; ok && t < jobs; ++t) {
-        if (!valid(t)) continue;
-        const int b = block_of(t), g = t & 1, n = t >> 1, s = b % G::VS;
-        uint64_t* bar = lane == 1 ? &p_full[g] : b >= first_part && !Q8 ? &v_clean[s] : &v_full[s];
-        // v_clean completes a phase for each block looked through that came to this slot.
-        const int use = b >= first_part && !Q8 ? (b - first_part) / G::VS : b / G::VS;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, (lane == 1 ? n : use) & 1)))) break;
+        const int b = two ? 0 : g;
+        if (b >= (two && g == 0 ? nb0 : nb)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(lane == 1 ? &q_ready[two ? g : 0] : &k_full[b % G::KS], 0));
+        if (!ok) break;
         fence_after();
-        const uint64_t vb = vd + (uint32_t)(s * (G::TILE / 16));
+        scores(b, g);
+        if (elect_one()) commit(&s_full[g]);
+        __syncwarp();
+      }
+      if (ok && elect_one()) commit(k_first);
+      __syncwarp();
+      for (int t = 0; ok && t < jobs; ++t) {
+        const int b = two ? t >> 1 : t, g = t & 1, n = t >> 1, next = two ? b + 1 : b + 2;
+        const int last = two && g == 0 ? nb0 : nb;  // blocks of this group end here
+        if (b >= last) continue;
+        const bool more = next < last, look = !Q8 && b >= first_part;
+        const int s = b % G::VS;
+        // v_clean completes a phase for each block looked through that came to this slot.
+        uint64_t* bar = lane == 1 ? &p_full[g] : lane == 2 && more ? &k_full[next % G::KS] : look ? &v_clean[s] : &v_full[s];
+        const int phase = lane == 1 ? n : lane == 2 && more ? next / G::KS : look ? (b - first_part) / G::VS : b / G::VS;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)))) break;
+        fence_after();
+        const uint32_t vb = v + s * (G::TILE / 16);
         const uint32_t d = tmem + G::O_COL + g * kRows, p = tmem + G::S_COL + g * kKeys;
         const int steps = min(8, div_up(end - (b_lo + b) * kKeys, 16));  // pages with keys
+        issue_values(d, p, vb, up_v, idO, steps, n > 0);
+        if constexpr (!Q8) issue_values(d, p + 64, vb, up_v, idO, steps, true);
+        if (more) scores(next, g);
         if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < steps) mma_ts(d, p + kk * 8, vb + (kk * 2048) / 16, idO, (n > 0 || kk > 0) ? 1u : 0u);
-          if constexpr (!Q8) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (kk < steps) mma_ts(d, p + 64 + kk * 8, vb + (kk * 2048) / 16, idO, 1u);
-          }
-          if (!two || g == 1) commit(&v_empty[s]);
-          if (!valid(t + 2)) commit(&o_final[g]);
+          commit(more ? &s_full[g] : &o_final[g]);
+          if (!two || g == 1) commit(&taken[b % G::NT]);
         }
         __syncwarp();
-        if (valid(t + 2)) scores(t + 2);
       }
       if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
       if (elect_one()) commit(done);  // every MMA issued above completes before TMEM is released
@@ -379,7 +470,6 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         constexpr int slots_k = G::KS, slots_v = G::VS;
         const int slots = kv ? slots_v : slots_k;
         uint64_t* full = kv ? v_full : k_full;
-        uint64_t* empty = kv ? v_empty : k_empty;
         const uint32_t ring = su32(smem + (kv ? G::OFF_V : G::OFF_K));
         uint64_t pol;  // a sequence's keys are read again by its other tiles
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
@@ -424,7 +514,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           // A slot to be filled again may hold a block that waits to be looked through.
           while (cleaned < nb && cleaned <= j - slots && ok) ok = clean(cleaned++);
           if (!ok) break;
-          if (j >= slots && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((j / slots) - 1) & 1)))) break;
+          if (j >= slots && !(ok = __all_sync(0xffffffffu, kv ? wait_taken(j - slots) : wait_k(j)))) break;
           if (elect_one()) mbar_arrive_tx(&full[s], (uint32_t)__popc(there) * (G::NX * 16 * 128));
           __syncwarp();
           for (int i = 0; i < 8; ++i) {
@@ -453,18 +543,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       for (int u = 0; u < 4 * nb; ++u) {
         const int s = u % G::NU, b = u >> 2, v = (u >> 1) & 1, half = u & 1;
         const int slots = v ? G::VS : G::KS, slot = b % slots;
-        uint64_t* empty = v ? v_empty : k_empty;
-        const bool other = lane == 1 && b >= slots;  // lane 1 waits for the slot, the others for the codes
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(other ? &empty[slot] : &u_full[s],
-                                                     other ? (b / slots - 1) & 1 : (u / G::NU) & 1))))
+        // Lane 1 waits for the slot, the others for the codes.
+        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= slots ? v ? wait_taken(b - slots) : wait_k(b)
+                                                                    : mbar_wait(&u_full[s], (u / G::NU) & 1))))
           break;
         const uint8_t* raw = smem + G::OFF_U + (size_t)s * G::UNIT;
         uint8_t* to = smem + (v ? G::OFF_V : G::OFF_K) + slot * G::TILE;
         const int left = end - (b_lo + b) * kKeys - half * 64;  // keys of this unit that are there
         const bool part = v && b >= first_part;
-        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::VS) * G::SCN;
-        // K's scales go where V's slot is free: the product with the block before in that slot is done (v_empty).
-        if (!v && b >= G::VS && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[b % G::VS], (b / G::VS - 1) & 1)))) break;
+        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::NSC) * G::SCN;
+        if (!v && b >= G::NSC && !(ok = __all_sync(0xffffffffu, wait_taken(b - G::NSC)))) break;
         const float* raw_scale = reinterpret_cast<const float*>(raw + 64 * HD);
 #pragma unroll
         for (int i = 0; i < PIECES / 128; ++i) {
@@ -574,8 +662,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     }
     int n = 0;  // jobs of this group so far
-    for (int t = g; ok && valid(t); t += 2, ++n) {
-      const int b = block_of(t);
+    const int n_jobs = two ? (g ? nb : nb0) : (nb + 1 - g) / 2;
+    for (; ok && n < n_jobs; ++n) {
+      const int b = two ? n : 2 * n + g;
       const int k0 = (b_lo + b) * kKeys;
       float sv[128];
       auto load = [&] {
@@ -639,7 +728,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         }
       };
       if constexpr (Q8) {
-        const uint32_t scales = su32(smem + G::OFF_SC + (b % G::VS) * G::SCN * 4);
+        const uint32_t scales = su32(smem + G::OFF_SC + (b % G::NSC) * G::SCN * 4);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[b % G::VS], (b / G::VS) & 1)))) break;
         load();
         if (!ok) break;

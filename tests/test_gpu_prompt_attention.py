@@ -229,6 +229,17 @@ def test_cut_keys(dtype, draft):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,hk,hd", [(16, 16, 128), (32, 16, 96), (16, 16, 64), (8, 8, 32)])
+@pytest.mark.parametrize("most", [3, 200])
+def test_long_contexts_that_are_not_cut(dtype, heads, hk, hd, most):
+    """Enough requests for the GPU: a CTA takes every block of a request's keys, for one tile or two."""
+    rng = np.random.default_rng(hd + most)
+    n = 700 // hk
+    cs = make(dtype, heads, hk, hd, rng.integers(1, most, n), rng.integers(0, 2500, n), seed=most)
+    check(cs, requests=range(0, n, 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("draft", [False, True])
 def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(dtype, draft):
     import torch
