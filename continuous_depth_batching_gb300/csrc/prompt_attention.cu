@@ -23,10 +23,11 @@
 //   warp 9       issues S = Q K^T (128 x 128) and O += P V.  The next scores of a group
 //                follow its product with V in the tensor core's queue, which keeps order,
 //                so they may overwrite the weights, and their commit covers both;
-//   warps 8, 11  bf16: copy K and V pages by TMA; then warp 11 looks the blocks that some
-//                rows do not see through (below).  e4m3: copy codes and scales in units of
-//                64 keys of K or of V;
-//   warps 12-15  e4m3: widen codes to fp16 in the MMA's swizzled layout.
+//   warps 8, 11  copy K and V pages by TMA, and scales; bf16: then warp 11 looks the blocks that
+//                some rows do not see through (below);
+//   warps 12-15  e4m3: widen V's codes to fp16 in the MMA's swizzled layout.  K's codes are an
+//                operand as they are: q becomes the sum of two e4m3 numbers, exactly but for elements
+//                far below a row's largest, and the scores of both are added up.
 // A weight of 0 times an infinite or NaN value is NaN, so in blocks that not all
 // rows see, V rows with such an element are set to zero in shared memory before the
 // product, and rows that see them take a NaN weight; V rows behind the sequence's
@@ -62,22 +63,24 @@ struct Geo {
   static_assert(HD % 32 == 0 && HD <= 128, "head dim");
   static constexpr int NX = (HD + 63) / 64;       // 128-byte slices of a 16-bit row
   static constexpr int SLICE = 128 * 128;         // one slice of 128 rows
-  static constexpr int TILE = NX * SLICE;         // Q tile, K or V block
-  static constexpr int KS = NX == 2 ? 2 : 4;      // K blocks in flight
+  static constexpr int TILE = NX * SLICE;         // V block in 16 bits
+  // bf16: Q tile and K block as V.  e4m3: K as it comes, a slice of up to 128 codes a row; Q in two parts like it.
+  static constexpr int QT = Q8 ? 2 * SLICE : TILE, KB = Q8 ? SLICE : TILE;
+  static constexpr int KS = Q8 ? 3 : NX == 2 ? 2 : 4;   // K blocks in flight
   static constexpr int VS = NX == 2 ? (Q8 ? 2 : 3) : 4;
-  // e4m3: units of 64 keys of K or V, as they come: codes, then their scales.
-  static constexpr int UNIT = 64 * HD + 64 * 4;
-  static constexpr int NU = NX == 2 ? 3 : 6;
+  // e4m3: V as it comes, a unit of 32 keys for each converter warp, with the scales of K and V.
+  static constexpr int UNIT = 32 * HD + 2 * 32 * 4;
+  static constexpr int NU = NX == 2 ? 2 : 3;      // units of a warp in flight
   static constexpr int NT = 8;                    // blocks whose end is told apart: more than a ring's slots and three
   static constexpr int NSC = 4;                   // blocks whose scales are kept
   static constexpr int SCN = 3 * kKeys + 4;       // scales of K, of V, the latter's logarithms, the largest of those by quarters
-  static constexpr int OFF_K = 2 * TILE;
-  static constexpr int OFF_V = OFF_K + KS * TILE;
+  static constexpr int OFF_K = 2 * QT;
+  static constexpr int OFF_V = OFF_K + KS * KB;
   static constexpr int OFF_U = OFF_V + VS * TILE;
-  static constexpr int OFF_SC = OFF_U + (Q8 ? NU * UNIT : 0);
+  static constexpr int OFF_SC = OFF_U + (Q8 ? 4 * NU * UNIT : 0);
   static constexpr int OFF_BAD = OFF_SC + (Q8 ? NSC * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
   static constexpr int OFF_BAR = OFF_BAD + VS * (Q8 ? kKeys : 16);
-  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 6;
+  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 4 * NU;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int THREADS = Q8 ? 512 : 384;
   static constexpr int S_COL = 256;               // [2][128] scores, then weights
@@ -221,6 +224,24 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
   return found;
 }
 
+// Two times two bf16 numbers times f as e4m3 codes, and what these leave of them.
+__device__ __forceinline__ void split_e4m3(uint32_t a, uint32_t b, float f, uint32_t& one, uint32_t& two) {
+  const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xFFFF0000u) * f, __uint_as_float(b << 16) * f,
+                      __uint_as_float(b & 0xFFFF0000u) * f};
+  auto codes = [](float x0, float x1, float x2, float x3) {
+    uint32_t r;
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+        " mov.b32 %0, {l, h};\n}\n"
+        : "=r"(r)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+    return r;
+  };
+  one = codes(x[0], x[1], x[2], x[3]);
+  const uint32_t lo = widen(one), hi = widen_hi(one);
+  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo)), h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  two = codes(x[0] - l.x, x[1] - l.y, x[2] - h.x, x[3] - h.y);
+}
+
 // 32 keys from position s on that a row sees, as bits.  Prompt: positions up to
 // lim.  Draft: those before `lim`, and behind them the row's mask.
 __device__ __forceinline__ uint32_t seen(int s, int lim, const uint32_t* mask, int nodes) {
@@ -267,6 +288,37 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k,
                  "r"(q), "r"(k), "r"(upper), "r"(id)
                  : "memory");
 }
+// The same of e4m3 codes, 32 elements a step; Q is the sum of two such tiles.
+#define CDB_S8(qoff, koff, acc)                                                                    \
+  " add.u32 x, %1, " qoff ";\n mov.b64 da, {x, %3};\n add.u32 x, %2, " koff ";\n mov.b64 db, {x, %3};\n" \
+  " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %4, " acc ";\n"
+template <int STEPS>
+__device__ __forceinline__ void issue_scores_e4m3(uint32_t d, uint32_t q, uint32_t k, uint32_t upper, uint32_t id) {
+  static_assert(STEPS >= 1 && STEPS <= 4, "head dim");
+  if constexpr (STEPS == 1)
+    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("1024", "0", "t") "}\n" ::"r"(d), "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+  if constexpr (STEPS == 2)
+    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("1024", "0", "t") CDB_S8("1026", "2", "t")
+                     "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+  if constexpr (STEPS == 3)
+    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("4", "4", "t") CDB_S8("1024", "0", "t")
+                     CDB_S8("1026", "2", "t") CDB_S8("1028", "4", "t") "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+  if constexpr (STEPS == 4)
+    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("4", "4", "t") CDB_S8("6", "6", "t")
+                     CDB_S8("1024", "0", "t") CDB_S8("1026", "2", "t") CDB_S8("1028", "4", "t") CDB_S8("1030", "6", "t")
+                         "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A and B e4m3, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 // O[tmem] (+)= P[tmem] V over `steps` pages of 16 keys (all eight where FULL).
 #define CDB_TS(n, a, off, acc)                                                              \
   " setp.gt.s32 s, %5, " n ";\n and.pred s, s, q;\n add.u32 x, %1, " a ";\n add.u32 y, %2, " off ";\n mov.b64 db, {y, %3};\n" \
@@ -288,7 +340,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   using G = Geo<HD, Q8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float2* xch = reinterpret_cast<float2*>(smem + G::TILE);  // [2][kRows], with one tile: the second's place
+  float2* xch = reinterpret_cast<float2*>(smem + G::QT);  // [2][kRows], with one tile: the second's place
   uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem + G::OFF_BAD);
   uint8_t* bad_bytes = smem + G::OFF_BAD;
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);  // [2]
@@ -301,16 +353,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint64_t* o_final = p_full + 2;
   uint64_t* done = o_final + 2;
   uint64_t* k_first = done + 1;          // K of the groups' first blocks is free
-  uint64_t* u_full = k_first + 1;        // [NU <= 6]
-  uint64_t* u_empty = u_full + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + 6);
+  uint64_t* u_full = k_first + 1;        // [4][NU]
+  uint64_t* u_empty = u_full + 4 * G::NU;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + 4 * G::NU);
 
   const cdb_prompt_attention_args& a = A.a;
   const cdb_paged_cache& c = a.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kh = blockIdx.x;
   if (threadIdx.x == 0) {
-    if constexpr (!Q8) asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
     for (int g = 0; g < 2; ++g) {
       mbar_init(&q_ready[g], 4);
       mbar_init(&s_full[g], 1);
@@ -318,7 +370,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       mbar_init(&o_final[g], 1);
     }
     for (int s = 0; s < G::KS; ++s) {
-      mbar_init(&k_full[s], Q8 ? 4 : 1);
+      mbar_init(&k_full[s], 1);
     }
     for (int s = 0; s < G::VS; ++s) {
       mbar_init(&v_full[s], Q8 ? 4 : 1);
@@ -327,9 +379,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     mbar_init(done, 1);
     mbar_init(k_first, 1);
     for (int s = 0; s < G::NT; ++s) mbar_init(&taken[s], 1);
-    for (int s = 0; s < 6; ++s) {
-      mbar_init(&u_full[s], 1);
-      mbar_init(&u_empty[s], 4);
+    for (int s = 0; s < 4 * G::NU; ++s) {
+      mbar_init(&u_full[s], 2);
+      mbar_init(&u_empty[s], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -381,14 +433,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // its warp nearly as long as the tensor cores take to compute it.  So both products of a job are issued in one go, after
       // one wait for all they need (lane 1 for the weights, lane 2 for the next keys, the others for the values), and
       // there is one commit for the scores and one for a block's K and V.
-      constexpr uint32_t idS = idesc_16(!Q8, kRows, kKeys, false), idO = idesc_16(!Q8, kRows, HD, true);
+      constexpr uint32_t idS = Q8 ? idesc_e4m3(kRows, kKeys) : idesc_16(true, kRows, kKeys, false);
+      constexpr uint32_t idO = idesc_16(!Q8, kRows, HD, true);
       const uint32_t q = (uint32_t)desc_k(su32(smem), 1024), k = (uint32_t)desc_k(su32(smem + G::OFF_K), 1024);
       const uint32_t v = (uint32_t)desc_mn(su32(smem + G::OFF_V), G::SLICE, 1024);
       const uint32_t up_k = (uint32_t)(desc_k(0, 1024) >> 32), up_v = (uint32_t)(desc_mn(0, G::SLICE, 1024) >> 32);
       const int jobs = two ? 2 * nb : nb;
       auto scores = [&](int b, int g) {
-        issue_scores<HD / 16>(tmem + G::S_COL + g * kKeys, q + (two ? g : 0) * (G::TILE / 16), k + (b % G::KS) * (G::TILE / 16),
-                              up_k, idS);
+        const uint32_t d = tmem + G::S_COL + g * kKeys, qa = q + (two ? g : 0) * (G::QT / 16), ka = k + (b % G::KS) * (G::KB / 16);
+        if constexpr (Q8) issue_scores_e4m3<HD / 32>(d, qa, ka, up_k, idS);
+        else issue_scores<HD / 16>(d, qa, ka, up_k, idS);
       };
       bool ok = true;
       for (int g = 0; ok && g < 2; ++g) {
@@ -444,28 +498,43 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // Key rows before this head's page of a block (V follows n_kv_heads pages after K).
       auto row_of = [&](int blk, int v) { return ((((long long)blk * c.n_kv_slots + a.slot) * 2 + v) * c.n_kv_heads + kh) * 16; };
       if constexpr (Q8) {
-        // Units: K of a block in two halves, then V; even ones are warp 8's, odd ones warp 11's.
-        for (int u = kv; u < 4 * nb; u += 2) {
-          const int s = u % G::NU, b = u >> 2, v = (u >> 1) & 1, pg = (b_lo + b) * 8 + (u & 1) * 4;
-          const int blk = lane < 4 ? block_at(pg + lane) : -1;
-          const int n = __popc(__ballot_sync(0xffffffffu, blk >= 0));
-          if (u >= G::NU && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[s], (u / G::NU - 1) & 1)))) break;
-          const uint32_t at = su32(smem + G::OFF_U + s * G::UNIT);
-          if (elect_one()) mbar_arrive_tx(&u_full[s], (uint32_t)n * (16 * HD + 64));
+        // Warp 8: K's codes, as the bf16 ones, and the scales of K into the units; warp 11: codes and scales of V.
+        uint64_t pol;  // a sequence's keys are read again by its other tiles
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+        for (int j = 0; j < nb; ++j) {
+          const int blk = lane < 8 ? block_at((b_lo + j) * 8 + lane) : -1;
+          const uint32_t there = __ballot_sync(0xffffffffu, blk >= 0);
+          const long long r = row_of(max(blk, 0), kv);
+          const int su = j % G::NU, sk = j % G::KS;
+          if (!kv) {
+            if (j >= G::KS && !(ok = __all_sync(0xffffffffu, wait_k(j)))) break;
+            if (elect_one()) mbar_arrive_tx(&k_full[sk], (uint32_t)__popc(there) * (16 * 128));
+            __syncwarp();
+            if (blk >= 0) tma_2d(su32(smem + G::OFF_K + sk * G::KB) + lane * 2048, &tmk, &k_full[sk], 0, (int)r, pol);
+            __syncwarp();
+            issued = j + 1;
+          }
+          // Lane l has a page of unit l / 2; its converter has done with what was there.
+          if (j >= G::NU && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[(lane & 3) * G::NU + su], (j / G::NU - 1) & 1)))) break;
+          if (lane < 4)
+            mbar_arrive_tx(&u_full[lane * G::NU + su], (uint32_t)__popc((there >> (2 * lane)) & 3) * (kv ? 16 * HD + 64 : 64));
           __syncwarp();
           if (blk >= 0) {
-            const long long r = row_of(blk, v);
-            bulk_1d(at + lane * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD, &u_full[s]);
-            bulk_1d(at + 64 * HD + lane * 64, c.scales + r, 64, &u_full[s]);
+            uint64_t* full = &u_full[lane / 2 * G::NU + su];
+            const uint32_t at = su32(smem + G::OFF_U + (lane / 2 * G::NU + su) * G::UNIT);
+            if (kv) bulk_1d(at + (lane & 1) * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD, full);
+            bulk_1d(at + 32 * HD + kv * 128 + (lane & 1) * 64, c.scales + r, 64, full);
           }
           __syncwarp();
-          issued = u + 1;
+          if (kv) issued = j + 1;
         }
         if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-        // Copies in flight land before the CTA may leave.  A slot that the other warp filled again was used, and its
-        // phase has moved on: where all went well only this warp's last unit is left to wait for, and that was used too.
-        for (int u = ok ? issued - 1 : max(kv, issued - 1 - 2 * ((G::NU - 1) / 2)); u >= 0 && u < issued; u += 2)
-          mbar_wait(&u_full[u % G::NU], (u / G::NU) & 1);
+        // Copies in flight land before the CTA may leave (at once when everything was used).  Units: where all went
+        // well the converters have waited for them.
+        if (!kv)
+          for (int j = max(0, issued - G::KS); j < issued; ++j) mbar_wait(&k_full[j % G::KS], (j / G::KS) & 1);
+        if (!ok)
+          for (int j = max(0, issued - G::NU); j < issued; ++j) mbar_wait(&u_full[(lane & 3) * G::NU + j % G::NU], (j / G::NU) & 1);
       } else {
         constexpr int slots_k = G::KS, slots_v = G::VS;
         const int slots = kv ? slots_v : slots_k;
@@ -535,68 +604,64 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       }
     } else if (Q8 && warp >= 12) {
       // ---------------- code converters ----------------
-      // 16 codes to 32 bytes at a time; lanes of the upper half of a row store their second piece first, so that
-      // the stores of eight lanes meet every bank once.
-      const int tid = threadIdx.x - 384;
-      constexpr int C = HD / 16, CL = HD == 96 ? 8 : C, PIECES = 64 * CL;  // of a row: pieces, lanes
+      // V to fp16, 32 keys of a block for each warp: 16 codes to 32 bytes at a time; lanes of the upper half of a row
+      // store their second piece first, so that the stores of eight lanes meet every bank once.
+      const int w = warp - 12;
+      constexpr int C = HD / 16, CL = HD == 96 ? 8 : C;  // of a row: pieces, lanes
       bool ok = true;
-      for (int u = 0; u < 4 * nb; ++u) {
-        const int s = u % G::NU, b = u >> 2, v = (u >> 1) & 1, half = u & 1;
-        const int slots = v ? G::VS : G::KS, slot = b % slots;
-        // Lane 1 waits for the slot, the others for the codes.
-        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= slots ? v ? wait_taken(b - slots) : wait_k(b)
-                                                                    : mbar_wait(&u_full[s], (u / G::NU) & 1))))
+      for (int b = 0; b < nb; ++b) {
+        const int su = w * G::NU + b % G::NU, slot = b % G::VS;
+        // Lane 1 waits for the slot, lane 2 for the place of the scales, the others for the codes.
+        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= G::VS    ? wait_taken(b - G::VS)
+                                           : lane == 2 && b >= G::NSC ? wait_taken(b - G::NSC)
+                                                                      : mbar_wait(&u_full[su], (b / G::NU) & 1))))
           break;
-        const uint8_t* raw = smem + G::OFF_U + (size_t)s * G::UNIT;
-        uint8_t* to = smem + (v ? G::OFF_V : G::OFF_K) + slot * G::TILE;
-        const int left = end - (b_lo + b) * kKeys - half * 64;  // keys of this unit that are there
-        const bool part = v && b >= first_part;
+        const uint8_t* raw = smem + G::OFF_U + (size_t)su * G::UNIT;
+        const float* raw_scale = reinterpret_cast<const float*>(raw + 32 * HD);  // of K, of V
+        uint8_t* to = smem + G::OFF_V + slot * G::TILE;
+        const int left = end - (b_lo + b) * kKeys - w * 32;  // keys of this unit that are there
+        const bool part = b >= first_part;
         float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::NSC) * G::SCN;
-        if (!v && b >= G::NSC && !(ok = __all_sync(0xffffffffu, wait_taken(b - G::NSC)))) break;
-        const float* raw_scale = reinterpret_cast<const float*>(raw + 64 * HD);
-#pragma unroll
-        for (int i = 0; i < PIECES / 128; ++i) {
-          const int key = (i * 128 + tid) / CL, x = tid % CL, r = half * 64 + key;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (x < C && !(v && key >= left)) w = *reinterpret_cast<const uint4*>(raw + key * HD + x * 16);
+        {
+          const float f = raw_scale[32 + lane];
+          // Keys behind the end, and in blocks looked through those whose scale is not finite, take no part.
+          const float fv = lane >= left || (part && !(fabsf(f) < INFINITY)) ? 0.f : f;
+          sc[w * 32 + lane] = raw_scale[lane];
+          sc[kKeys + w * 32 + lane] = fv;
+          sc[2 * kKeys + w * 32 + lane] = __log2f(fabsf(fv));
+          const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
+          if (lane == 0) sc[3 * kKeys + w] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
+        }
+#pragma unroll 4
+        for (int i = 0; i < CL; ++i) {
+          const int key = (i * 32 + lane) / CL, x = lane % CL, r = w * 32 + key;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (x < C && key < left) v = *reinterpret_cast<const uint4*>(raw + key * HD + x * 16);
           if (part) {
             // A code of NaN has all seven lower bits.  Every element of a key that holds one, or whose scale is not
             // finite, becomes 0.
-            const uint32_t f = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                               ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            const uint32_t f = ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                               ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
             const uint32_t found = __ballot_sync(0xffffffffu, (f & 0x80808080u) != 0);
-            const bool bad = key < left && (((found >> (lane / CL * CL)) & ((1u << CL) - 1)) || !(fabsf(raw_scale[key]) < INFINITY));
-            if (bad) w = make_uint4(0, 0, 0, 0);
+            const bool bad = key < left && (((found >> (lane / CL * CL)) & ((1u << CL) - 1)) || !(fabsf(raw_scale[32 + key]) < INFINITY));
+            if (bad) v = make_uint4(0, 0, 0, 0);
             if (x == 0) bad_bytes[slot * kKeys + r] = bad;
           }
           if (x < C) {
             uint8_t* d = to + (x / 4) * G::SLICE + r * 128;
-            const uint4 lo = make_uint4(widen(w.x), widen_hi(w.x), widen(w.y), widen_hi(w.y));
-            const uint4 hi = make_uint4(widen(w.z), widen_hi(w.z), widen(w.w), widen_hi(w.w));
+            const uint4 lo = make_uint4(widen(v.x), widen_hi(v.x), widen(v.y), widen_hi(v.y));
+            const uint4 hi = make_uint4(widen(v.z), widen_hi(v.z), widen(v.w), widen_hi(v.w));
             const int c0 = (x % 4) * 2, sw = r & 7;
             const bool swap = x >= 4;
             *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ sw) << 4)) = swap ? hi : lo;
             *reinterpret_cast<uint4*>(d + (((c0 + !swap) ^ sw) << 4)) = swap ? lo : hi;
           }
         }
-        if (tid < 64) {
-          const float f = raw_scale[tid];
-          if (!v) {
-            sc[half * 64 + tid] = f;
-          } else {
-            // Keys behind the end, and in blocks looked through those whose scale is not finite, take no part.
-            const float fv = tid >= left || (part && !(fabsf(f) < INFINITY)) ? 0.f : f;
-            sc[kKeys + half * 64 + tid] = fv;
-            sc[2 * kKeys + half * 64 + tid] = __log2f(fabsf(fv));
-            const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
-            if (lane == 0) sc[3 * kKeys + half * 2 + tid / 32] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
-          }
-        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&u_empty[s]);
-          if (half) mbar_arrive(v ? &v_full[slot] : &k_full[slot]);
+          mbar_arrive(&u_empty[su]);
+          mbar_arrive(&v_full[slot]);
         }
       }
       if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
@@ -626,10 +691,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     {
       // This row of q into the tile, swizzled; with one tile the first group does it.
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + (size_t)head * HD);
-      uint8_t* dst = smem + tile * G::TILE + r * 128;
+      uint8_t* dst = smem + tile * G::QT + r * 128;
       float down = 1.f, up = 1.f;
       if constexpr (Q8) {
-        // e4m3: each row divided by a power of two, in fp16.
+        // e4m3: each row times a power of two, which takes its largest element into [128, 256), in two parts, what
+        // the first leaves in the second: four bits each, so that elements down to 2^-9 of it are exact.
         float mx = 0.f;
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
@@ -639,21 +705,28 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           for (int e = 0; e < 4; ++e) mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
         }
         const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
-        const bool norm = eb > 0x00800000u && eb < 0x7E000000u;  // else zero, tiny, infinite or NaN
-        down = norm ? __uint_as_float(0x7F000000u - eb) : 1.f;
-        up = norm ? __uint_as_float(eb) : 1.f;
+        if (eb == 0x7F800000u) {
+          down = NAN;  // the conversion would make an infinite element a finite one
+        } else if (eb >= 0x04000000u) {  // else zero or below 2^-119
+          down = __uint_as_float(0x82800000u - eb);
+          up = __uint_as_float(eb - 0x03800000u);
+        }
       }
       if (two || g == 0) {
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
           const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
-          uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
           if constexpr (Q8) {
+            uint32_t one[2], two_[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xFFFF0000u) * down);
+            for (int e = 0; e < 2; ++e) split_e4m3(v[2 * e], v[2 * e + 1], down, one[e], two_[e]);
+            const uint32_t at = su32(dst) + (((x / 2) ^ (r & 7)) << 4) + (x & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(one[0]), "r"(one[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + G::SLICE), "r"(two_[0]), "r"(two_[1]) : "memory");
+          } else {
+            st_shared_v4(su32(dst + (x / 8) * G::SLICE + (((x % 8) ^ (r & 7)) << 4)), v[0], v[1], v[2], v[3]);
           }
-          st_shared_v4(su32(dst + (x / 8) * G::SLICE + (((x % 8) ^ (r & 7)) << 4)), v[0], v[1], v[2], v[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -958,7 +1031,8 @@ cudaError_t launch(cudaStream_t s, const Args& A) {
   CUtensorMap tk = {};
   const uint64_t rows = (uint64_t)c.kv_blocks * c.n_kv_slots * 2 * c.n_kv_heads * 16;
   // A page is a box of 16 rows of 128 bytes; what a row has less is filled with zeros.
-  if (!Q8 && !tmap_u8_2d(&tk, c.pool, HD * 2, rows, HD * 2, 128, 16, 128)) return cudaErrorInvalidValue;
+  constexpr int kRow = HD * (Q8 ? 1 : 2);
+  if (!tmap_u8_2d(&tk, c.pool, kRow, rows, kRow, 128, 16, 128)) return cudaErrorInvalidValue;
   static bool set[kMaxDevices] = {};
   const int dev = current_device();
   if (!set[dev]) {
