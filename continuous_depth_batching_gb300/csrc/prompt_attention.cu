@@ -692,6 +692,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // This row of q into the tile, swizzled; with one tile the first group does it.
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * a.ldq + (size_t)head * HD);
       uint8_t* dst = smem + tile * G::QT + r * 128;
+      uint4 row_q[HD / 8];  // all on their way before the first is used
+#pragma unroll
+      for (int x = 0; x < HD / 8; ++x) row_q[x] = live && (Q8 || two || g == 0) ? src[x] : make_uint4(0, 0, 0, 0);
       float down = 1.f, up = 1.f;
       if constexpr (Q8) {
         // e4m3: each row times a power of two, which takes its largest element into [128, 256), in two parts, what
@@ -699,8 +702,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         float mx = 0.f;
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t v[4] = {row_q[x].x, row_q[x].y, row_q[x].z, row_q[x].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
         }
@@ -715,8 +717,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       if (two || g == 0) {
 #pragma unroll
         for (int x = 0; x < HD / 8; ++x) {
-          const uint4 w = live ? src[x] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t v[4] = {row_q[x].x, row_q[x].y, row_q[x].z, row_q[x].w};
           if constexpr (Q8) {
             uint32_t one[2], two_[2];
 #pragma unroll
@@ -902,11 +903,12 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     auto store = [&](int c0, float* v, float f) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] *= f;
-      if (it.chunks > 1) {
+      if (!live) {
+      } else if (it.chunks > 1) {
         float* po = A.part_o + pi * HD + c0;
 #pragma unroll
         for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(po + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-      } else if (live) {
+      } else {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
           *reinterpret_cast<uint4*>(out + c0 + e) = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),

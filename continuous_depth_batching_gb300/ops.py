@@ -543,14 +543,15 @@ class PagePlanner(_StatusOp):
         self._vec("free_blocks", free_blocks, t.int32, 1, True)
         self.max_requests, self.max_rows = int(max_requests), int(max_rows)
         self.row_start = t.empty(self.max_requests + 1, dtype=t.int32, device=dev)
-        self.rows = t.empty(2, self.max_rows, dtype=t.int32, device=dev)
+        self.seq, self.pos = (t.empty(self.max_rows, dtype=t.int32, device=dev) for _ in range(2))
         self.slot = t.empty(self.max_rows, dtype=t.int64, device=dev)
-        self._memory += [self.row_start, self.rows, self.slot]
+        self._memory += [self.row_start, self.seq, self.pos, self.slot]
+        self._out = Rows(self.row_start, self.seq, self.pos, self.slot)  # of the last number of requests
         self._keep = (block_table, free_blocks)
         self.args = PlanPagesArgs(block_table=block_table.data_ptr(), n_seqs=block_table.shape[0],
                                   max_blocks=block_table.shape[1], free_blocks=free_blocks.data_ptr(),
                                   free_slots=free_blocks.numel(), row_start=self.row_start.data_ptr(),
-                                  row_seq=self.rows[0].data_ptr(), row_pos=self.rows[1].data_ptr(),
+                                  row_seq=self.seq.data_ptr(), row_pos=self.pos.data_ptr(),
                                   row_slot=self.slot.data_ptr(), max_rows=self.max_rows, status=self.status.data_ptr())
         self._bind("cdb_plan_pages", "plan_pages")
 
@@ -572,7 +573,10 @@ class PagePlanner(_StatusOp):
                 self._vec("state", state, t.int64, 2, True)
                 self._vec("state_out", state_out, t.int64, 2, True)
             self._fail(rc)
-        return Rows(self.row_start[:n + 1], self.rows[0], self.rows[1], self.slot)
+        out = self._out
+        if out.row_start.shape[0] != n + 1:
+            out = self._out = Rows(self.row_start[:n + 1], self.seq, self.pos, self.slot)
+        return out
 
 
 class PathKeeper(_CacheOp):
