@@ -68,9 +68,11 @@ struct Geo {
   static constexpr int QT = Q8 ? 2 * SLICE : TILE, KB = Q8 ? SLICE : TILE;
   static constexpr int KS = Q8 ? 3 : NX == 2 ? 2 : 4;   // K blocks in flight
   static constexpr int VS = NX == 2 ? (Q8 ? 2 : 3) : 4;
-  // e4m3: V as it comes, a unit of 32 keys for each converter warp, with the scales of K and V.
-  static constexpr int UNIT = 32 * HD + 2 * 32 * 4;
+  // e4m3: V as it comes, a unit of 32 keys for each converter warp; with one tile, more of them where the second Q
+  // tile would be.
+  static constexpr int UNIT = 32 * HD;
   static constexpr int NU = NX == 2 ? 2 : 3;      // units of a warp in flight
+  static constexpr int MORE = QT / (4 * UNIT) > 4 ? 4 : QT / (4 * UNIT);
   static constexpr int NT = 8;                    // blocks whose end is told apart: more than a ring's slots and three
   static constexpr int NSC = 4;                   // blocks whose scales are kept
   static constexpr int SCN = 3 * kKeys + 4;       // scales of K, of V, the latter's logarithms, the largest of those by quarters
@@ -79,8 +81,11 @@ struct Geo {
   static constexpr int OFF_U = OFF_V + VS * TILE;
   static constexpr int OFF_SC = OFF_U + (Q8 ? 4 * NU * UNIT : 0);
   static constexpr int OFF_BAD = OFF_SC + (Q8 ? NSC * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
-  static constexpr int OFF_BAR = OFF_BAD + VS * (Q8 ? kKeys : 16);
-  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 4 * NU;
+  // float2 [2][kRows], with one tile; bf16: in the second's place
+  static constexpr int OFF_XCH = Q8 ? OFF_BAD + VS * kKeys : QT;
+  static constexpr int OFF_UP = OFF_BAD + VS * (Q8 ? kKeys : 16) + (Q8 ? 2 * kRows * 8 : 0);
+  static constexpr int OFF_BAR = OFF_UP + (Q8 ? 2 * kRows * 4 : 0);
+  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 4 * (NU + MORE) + NSC;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int THREADS = Q8 ? 512 : 384;
   static constexpr int S_COL = 256;               // [2][128] scores, then weights
@@ -224,22 +229,24 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
   return found;
 }
 
-// Two times two bf16 numbers times f as e4m3 codes, and what these leave of them.
-__device__ __forceinline__ void split_e4m3(uint32_t a, uint32_t b, float f, uint32_t& one, uint32_t& two) {
-  const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xFFFF0000u) * f, __uint_as_float(b << 16) * f,
-                      __uint_as_float(b & 0xFFFF0000u) * f};
-  auto codes = [](float x0, float x1, float x2, float x3) {
-    uint32_t r;
-    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
-        " mov.b32 %0, {l, h};\n}\n"
-        : "=r"(r)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
-    return r;
-  };
-  one = codes(x[0], x[1], x[2], x[3]);
-  const uint32_t lo = widen(one), hi = widen_hi(one);
-  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo)), h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  two = codes(x[0] - l.x, x[1] - l.y, x[2] - h.x, x[3] - h.y);
+// Two times two bf16 numbers times f as e4m3 codes, and what these leave of them (exactly: eight bits in all).
+__device__ __forceinline__ void split_e4m3(uint32_t a, uint32_t b, float f, uint32_t& one, uint32_t& rest) {
+  asm("{\n .reg .b16 l, h;\n .reg .b32 x, y, u, v;\n .reg .f32 e, f;\n"
+      " shl.b32 u, %2, 16;\n and.b32 v, %2, 0xFFFF0000;\n mul.f32 e, u, %4;\n mul.f32 f, v, %4;\n cvt.rn.f16x2.f32 x, f, e;\n"
+      " shl.b32 u, %3, 16;\n and.b32 v, %3, 0xFFFF0000;\n mul.f32 e, u, %4;\n mul.f32 f, v, %4;\n cvt.rn.f16x2.f32 y, f, e;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n cvt.rn.satfinite.e4m3x2.f16x2 h, y;\n mov.b32 %0, {l, h};\n"
+      " cvt.rn.f16x2.e4m3x2 u, l;\n cvt.rn.f16x2.e4m3x2 v, h;\n sub.rn.f16x2 x, x, u;\n sub.rn.f16x2 y, y, v;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n cvt.rn.satfinite.e4m3x2.f16x2 h, y;\n mov.b32 %1, {l, h};\n}\n"
+      : "=&r"(one), "=r"(rest)
+      : "r"(a), "r"(b), "f"(f));
+}
+// The largest magnitude of eight bf16 numbers, as bits (NaN: above infinity).
+__device__ __forceinline__ uint32_t largest_bf16(uint4 w) {
+  uint32_t m = 0;
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m = max(m, max(v[e] << 16 & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+  return m >> 16;
 }
 
 // 32 keys from position s on that a row sees, as bits.  Prompt: positions up to
@@ -340,9 +347,10 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   using G = Geo<HD, Q8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float2* xch = reinterpret_cast<float2*>(smem + G::QT);  // [2][kRows], with one tile: the second's place
+  float2* xch = reinterpret_cast<float2*>(smem + G::OFF_XCH);
   uint32_t* bad_keys = reinterpret_cast<uint32_t*>(smem + G::OFF_BAD);
   uint8_t* bad_bytes = smem + G::OFF_BAD;
+  float* q_up = reinterpret_cast<float*>(smem + G::OFF_UP);  // e4m3: what a row of q was divided by
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);  // [2]
   uint64_t* k_full = q_ready + 2;
   uint64_t* v_full = k_full + G::KS;
@@ -353,9 +361,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint64_t* o_final = p_full + 2;
   uint64_t* done = o_final + 2;
   uint64_t* k_first = done + 1;          // K of the groups' first blocks is free
-  uint64_t* u_full = k_first + 1;        // [4][NU]
-  uint64_t* u_empty = u_full + 4 * G::NU;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + 4 * G::NU);
+  constexpr int kUnits = 4 * (G::NU + G::MORE);
+  uint64_t* u_full = k_first + 1;        // [slots][4]
+  uint64_t* u_empty = u_full + kUnits;
+  uint64_t* sc_full = u_empty + kUnits;  // [NSC]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + G::NSC);
 
   const cdb_prompt_attention_args& a = A.a;
   const cdb_paged_cache& c = a.cache;
@@ -364,9 +374,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&q_ready[g], 4);
       mbar_init(&s_full[g], 1);
-      mbar_init(&p_full[g], 4);
       mbar_init(&o_final[g], 1);
     }
     for (int s = 0; s < G::KS; ++s) {
@@ -379,12 +387,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     mbar_init(done, 1);
     mbar_init(k_first, 1);
     for (int s = 0; s < G::NT; ++s) mbar_init(&taken[s], 1);
-    for (int s = 0; s < 4 * G::NU; ++s) {
-      mbar_init(&u_full[s], 2);
+    for (int s = 0; s < G::NSC; ++s) mbar_init(&sc_full[s], 4);
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(&u_full[s], 1);
       mbar_init(&u_empty[s], 1);
     }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   pdl_wait();
   pdl_trigger();
@@ -393,6 +400,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   const int tt = A.tokens;
   const int n_tok = min(2 * tt, it.count - it.t0);      // tokens of this item
   const bool two = n_tok > tt;
+  // Warps of a group that have rows; the others' lanes of the products hold what they may.
+  auto live_warps = [&](int g) { return div_up(min(tt, two && g ? n_tok - tt : n_tok) * A.group, 32); };
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&q_ready[g], live_warps(g));
+      mbar_init(&p_full[g], live_warps(g));
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -420,6 +437,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   auto wait_k = [&](int j) {
     const int gone = j - G::KS - (two ? 1 : 2);
     return gone < 0 ? mbar_wait(k_first, 0) : wait_taken(gone);
+  };
+
+  const int units = G::NU + (two ? 0 : G::MORE);  // e4m3: units of a converter warp in flight
+  auto unit_at = [&](int s, int w) {
+    return s < G::NU ? smem + G::OFF_U + (s * 4 + w) * G::UNIT : smem + G::QT + ((s - G::NU) * 4 + w) * G::UNIT;
   };
 
   static_assert(!Q8 || 256 * 176 + 256 * 80 <= 512 * 128, "registers of the launch");
@@ -509,43 +531,40 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // Key rows before this head's page of a block (V follows n_kv_heads pages after K).
       auto row_of = [&](int blk, int v) { return ((((long long)blk * c.n_kv_slots + a.slot) * 2 + v) * c.n_kv_heads + kh) * 16; };
       if constexpr (Q8) {
-        // Warp 8: K's codes, as the bf16 ones, and the scales of K into the units; warp 11: codes and scales of V.
+        // Warp 8: K's codes, as the bf16 ones; warp 11: V's codes.  Lane l has a page of a block.
         uint64_t pol;  // a sequence's keys are read again by its other tiles
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+        auto mine = [&](int j) { return lane < 8 && j < nb ? block_at((b_lo + j) * 8 + lane) : -1; };
+        int blk = mine(0), s = 0, turn = 0;
         for (int j = 0; j < nb; ++j) {
-          const int blk = lane < 8 ? block_at((b_lo + j) * 8 + lane) : -1;
+          const int blk_next = mine(j + 1);  // on its way during this one
           const uint32_t there = __ballot_sync(0xffffffffu, blk >= 0);
           const long long r = row_of(max(blk, 0), kv);
-          const int su = j % G::NU, sk = j % G::KS;
           if (!kv) {
             if (j >= G::KS && !(ok = __all_sync(0xffffffffu, wait_k(j)))) break;
-            if (elect_one()) mbar_arrive_tx(&k_full[sk], (uint32_t)__popc(there) * (16 * 128));
+            if (elect_one()) mbar_arrive_tx(&k_full[s], (uint32_t)__popc(there) * (16 * 128));
             __syncwarp();
-            if (blk >= 0) tma_2d(su32(smem + G::OFF_K + sk * G::KB) + lane * 2048, &tmk, &k_full[sk], 0, (int)r, pol);
+            if (blk >= 0) tma_2d(su32(smem + G::OFF_K + s * G::KB) + lane * 2048, &tmk, &k_full[s], 0, (int)r, pol);
+            if (++s == G::KS) s = 0;
+          } else {
+            // The converters of the units have done with what was there.
+            if (j >= units && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[s * 4 + (lane & 3)], turn ^ 1)))) break;
+            if (lane < 4) mbar_arrive_tx(&u_full[s * 4 + lane], (uint32_t)__popc((there >> (2 * lane)) & 3) * (16 * HD));
             __syncwarp();
-            issued = j + 1;
-          }
-          // Lane l has a page of unit l / 2; its converter has done with what was there.
-          if (j >= G::NU && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[(lane & 3) * G::NU + su], (j / G::NU - 1) & 1)))) break;
-          if (lane < 4)
-            mbar_arrive_tx(&u_full[lane * G::NU + su], (uint32_t)__popc((there >> (2 * lane)) & 3) * (kv ? 16 * HD + 64 : 64));
-          __syncwarp();
-          if (blk >= 0) {
-            uint64_t* full = &u_full[lane / 2 * G::NU + su];
-            const uint32_t at = su32(smem + G::OFF_U + (lane / 2 * G::NU + su) * G::UNIT);
-            if (kv) bulk_1d(at + (lane & 1) * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD, full);
-            bulk_1d(at + 32 * HD + kv * 128 + (lane & 1) * 64, c.scales + r, 64, full);
+            if (blk >= 0)
+              bulk_1d(su32(unit_at(s, lane / 2)) + (lane & 1) * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD,
+                      &u_full[s * 4 + lane / 2]);
+            if (++s == units) s = 0, turn ^= 1;
           }
           __syncwarp();
-          if (kv) issued = j + 1;
+          issued = j + 1;
+          blk = blk_next;
         }
         if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
-        // Copies in flight land before the CTA may leave (at once when everything was used).  Units: where all went
-        // well the converters have waited for them.
-        if (!kv)
-          for (int j = max(0, issued - G::KS); j < issued; ++j) mbar_wait(&k_full[j % G::KS], (j / G::KS) & 1);
-        if (!ok)
-          for (int j = max(0, issued - G::NU); j < issued; ++j) mbar_wait(&u_full[(lane & 3) * G::NU + j % G::NU], (j / G::NU) & 1);
+        // Copies in flight land before the CTA may leave (at once when everything was used).
+        const int slots = kv ? units : G::KS;
+        for (int j = max(0, issued - slots); j < issued; ++j)
+          mbar_wait(kv ? &u_full[j % slots * 4 + (lane & 3)] : &k_full[j % slots], (j / slots) & 1);
       } else {
         constexpr int slots_k = G::KS, slots_v = G::VS;
         const int slots = kv ? slots_v : slots_k;
@@ -619,61 +638,106 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // store their second piece first, so that the stores of eight lanes meet every bank once.
       const int w = warp - 12;
       constexpr int C = HD / 16, CL = HD == 96 ? 8 : C;  // of a row: pieces, lanes
+      constexpr int B = CL < 4 ? CL : 4;                 // passes whose loads are on their way together
+      // The scales of this lane's key go ahead of the codes, two blocks, so that scores need not wait for V; they are
+      // on their way for a block before that.
+      const int* bt = c.block_table + (size_t)it.seq * c.max_blocks;
+      const int npg = div_up(end, 16);
+      auto pool_block = [&](int b) {
+        const int pg = (b_lo + b) * 8 + w * 2 + lane / 16, blk = b < nb && pg < npg ? bt[pg] : -1;
+        return blk < c.kv_blocks ? blk : -1;  // reported by the producers
+      };
+      float k_scale = 0.f, v_scale = 0.f;
+      auto fetch = [&](int blk) {
+        const long long at = (((long long)max(blk, 0) * c.n_kv_slots + a.slot) * 2 * c.n_kv_heads + kh) * 16 + lane % 16;
+        k_scale = blk >= 0 ? c.scales[at] : 0.f;
+        v_scale = blk >= 0 ? c.scales[at + c.n_kv_heads * 16] : 0.f;
+      };
+      uint32_t bad_scales[3] = {0, 0, 0};  // keys of blocks b, b + 1 and b + 2 whose value scale is not finite
+      auto put = [&](int b) {
+        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::NSC) * G::SCN;
+        const bool bad = b >= first_part && !(fabsf(v_scale) < INFINITY);
+        // Keys behind the end, and in blocks looked through those whose scale is not finite, take no part.
+        const float fv = bad || lane >= end - (b_lo + b) * kKeys - w * 32 ? 0.f : v_scale;
+        sc[w * 32 + lane] = k_scale;
+        sc[kKeys + w * 32 + lane] = fv;
+        sc[2 * kKeys + w * 32 + lane] = __log2f(fabsf(fv));
+        const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
+        if (lane == 0) sc[3 * kKeys + w] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[b % G::NSC]);
+        return __ballot_sync(0xffffffffu, bad);
+      };
+      const int first_ids = pool_block(0), second_ids = pool_block(1), third_ids = pool_block(2);
+      fetch(first_ids);
+      bad_scales[0] = put(0);
+      fetch(second_ids);
+      if (nb > 1) bad_scales[1] = put(1);
+      fetch(third_ids);
+      int ahead = pool_block(3), s = 0, turn = 0;
       bool ok = true;
       for (int b = 0; b < nb; ++b) {
-        const int su = w * G::NU + b % G::NU, slot = b % G::VS;
-        // Lane 1 waits for the slot, lane 2 for the place of the scales, the others for the codes.
-        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= G::VS    ? wait_taken(b - G::VS)
-                                           : lane == 2 && b >= G::NSC ? wait_taken(b - G::NSC)
-                                                                      : mbar_wait(&u_full[su], (b / G::NU) & 1))))
+        const int slot = b % G::VS;
+        // Lane 1 waits for the slot, lane 2 for the place of the scales two blocks on, the others for the codes.
+        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= G::VS        ? wait_taken(b - G::VS)
+                                           : lane == 2 && b + 2 >= G::NSC ? wait_taken(b + 2 - G::NSC)
+                                                                          : mbar_wait(&u_full[s * 4 + w], turn))))
           break;
-        const uint8_t* raw = smem + G::OFF_U + (size_t)su * G::UNIT;
-        const float* raw_scale = reinterpret_cast<const float*>(raw + 32 * HD);  // of K, of V
+        if (b + 2 < nb) {
+          bad_scales[2] = put(b + 2);
+          fetch(ahead);
+          ahead = pool_block(b + 4);
+        }
+        const uint8_t* raw = unit_at(s, w);
         uint8_t* to = smem + G::OFF_V + slot * G::TILE;
         const int left = end - (b_lo + b) * kKeys - w * 32;  // keys of this unit that are there
         const bool part = b >= first_part;
-        float* sc = reinterpret_cast<float*>(smem + G::OFF_SC) + (b % G::NSC) * G::SCN;
-        {
-          const float f = raw_scale[32 + lane];
-          // Keys behind the end, and in blocks looked through those whose scale is not finite, take no part.
-          const float fv = lane >= left || (part && !(fabsf(f) < INFINITY)) ? 0.f : f;
-          sc[w * 32 + lane] = raw_scale[lane];
-          sc[kKeys + w * 32 + lane] = fv;
-          sc[2 * kKeys + w * 32 + lane] = __log2f(fabsf(fv));
-          const uint32_t fm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
-          if (lane == 0) sc[3 * kKeys + w] = fmaxf(__log2f(__uint_as_float(fm)), -82.f);
-        }
-#pragma unroll 4
-        for (int i = 0; i < CL; ++i) {
-          const int key = (i * 32 + lane) / CL, x = lane % CL, r = w * 32 + key;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (x < C && key < left) v = *reinterpret_cast<const uint4*>(raw + key * HD + x * 16);
-          if (part) {
-            // A code of NaN has all seven lower bits.  Every element of a key that holds one, or whose scale is not
-            // finite, becomes 0.
-            const uint32_t f = ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                               ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
-            const uint32_t found = __ballot_sync(0xffffffffu, (f & 0x80808080u) != 0);
-            const bool bad = key < left && (((found >> (lane / CL * CL)) & ((1u << CL) - 1)) || !(fabsf(raw_scale[32 + key]) < INFINITY));
-            if (bad) v = make_uint4(0, 0, 0, 0);
-            if (x == 0) bad_bytes[slot * kKeys + r] = bad;
+        const int x = lane % CL;
+#pragma unroll 1
+        for (int i0 = 0; i0 < CL; i0 += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int key = (i0 + i) * (32 / CL) + lane / CL;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (x < C && key < left) v[i] = *reinterpret_cast<const uint4*>(raw + key * HD + x * 16);
           }
-          if (x < C) {
-            uint8_t* d = to + (x / 4) * G::SLICE + r * 128;
-            const uint4 lo = make_uint4(widen(v.x), widen_hi(v.x), widen(v.y), widen_hi(v.y));
-            const uint4 hi = make_uint4(widen(v.z), widen_hi(v.z), widen(v.w), widen_hi(v.w));
-            const int c0 = (x % 4) * 2, sw = r & 7;
-            const bool swap = x >= 4;
-            *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ sw) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(d + (((c0 + !swap) ^ sw) << 4)) = swap ? lo : hi;
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+              // A code of NaN has all seven lower bits.  Every element of a key that holds one, or whose scale is not
+              // finite, becomes 0.
+              const int key = (i0 + i) * (32 / CL) + lane / CL;
+              const uint32_t f = ((v[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((v[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                 ((v[i].z & 0x7F7F7F7Fu) + 0x01010101u) | ((v[i].w & 0x7F7F7F7Fu) + 0x01010101u);
+              const uint32_t found = __ballot_sync(0xffffffffu, (f & 0x80808080u) != 0);
+              const bool bad = key < left && (((found >> (lane / CL * CL)) & ((1u << CL) - 1)) || ((bad_scales[0] >> key) & 1));
+              if (bad) v[i] = make_uint4(0, 0, 0, 0);
+              if (x == 0) bad_bytes[slot * kKeys + w * 32 + key] = bad;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            if (x < C) {
+              const int r = w * 32 + (i0 + i) * (32 / CL) + lane / CL;
+              uint8_t* d = to + (x / 4) * G::SLICE + r * 128;
+              const uint4 lo = make_uint4(widen(v[i].x), widen_hi(v[i].x), widen(v[i].y), widen_hi(v[i].y));
+              const uint4 hi = make_uint4(widen(v[i].z), widen_hi(v[i].z), widen(v[i].w), widen_hi(v[i].w));
+              const int c0 = (x % 4) * 2, sw = r & 7;
+              const bool swap = x >= 4;
+              *reinterpret_cast<uint4*>(d + (((c0 + swap) ^ sw) << 4)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(d + (((c0 + !swap) ^ sw) << 4)) = swap ? lo : hi;
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&u_empty[su]);
+          mbar_arrive(&u_empty[s * 4 + w]);
           mbar_arrive(&v_full[slot]);
         }
+        if (++s == units) s = 0, turn ^= 1;
+        bad_scales[0] = bad_scales[1], bad_scales[1] = bad_scales[2];
       }
       if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     }
@@ -682,6 +746,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax groups ----------------
     const int q4 = warp & 3, g = warp >> 2;
+    const bool works = q4 < live_warps(g);
     const int r = q4 * 32 + lane;
     const int tile = two ? g : 0;
     const int tk = it.t0 + tile * tt + r / A.group;  // token of this row
@@ -704,64 +769,86 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // another take pieces of 16 bytes that do, P of a row (a thread for a row: 1.5 us more for each item).
       constexpr int P = HD / 8, L = HD == 96 ? 16 : P, R = 32 / L;  // pieces, lanes of a row, rows at a time
       uint8_t* dst = smem + tile * G::QT;
-      const int x = lane % L;
-      float up = 1.f;
-      uint4 piece[L];
-      {
+      const int x = lane % L, rows_here = min(tt * A.group, (it.count - it.t0 - tile * tt) * A.group) - q4 * 32;
+      if (works && (two || g == 0)) {
+        // Token and head of this lane's row, R rows further in each pass.
+        const int step_t = R / A.group, step_h = R - step_t * A.group;
+        int rr = lane / L, t = (q4 * 32 + rr) / A.group, h = q4 * 32 + rr - t * A.group, loaded = rr;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (long long)(it.row0 + it.t0 + tile * tt) * a.ldq +
+                                   (size_t)kh * A.group * HD + x * 8;
+        auto load_q = [&] {
+          const uint4 v = x < P && loaded < rows_here ? *reinterpret_cast<const uint4*>(src + (long long)t * a.ldq + (size_t)h * HD)
+                                                      : make_uint4(0, 0, 0, 0);
+          t += step_t, h += step_h, loaded += R;
+          if (h >= A.group) h -= A.group, ++t;
+          return v;
+        };
+        if constexpr (!Q8) {
+          uint4 piece[L];
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int rr = q4 * 32 + i * R + lane / L, t = it.t0 + tile * tt + rr / A.group;
-          const bool there = x < P && rr < tt * A.group && t < it.count;
-          piece[i] = there ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (long long)(it.row0 + t) * a.ldq +
-                                                             (size_t)(kh * A.group + rr % A.group) * HD + x * 8)
-                           : make_uint4(0, 0, 0, 0);
-        }
+          for (int i = 0; i < L; ++i) piece[i] = load_q();
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int rr = q4 * 32 + i * R + lane / L;
-          const uint32_t v[4] = {piece[i].x, piece[i].y, piece[i].z, piece[i].w};
-          if constexpr (Q8) {
-            // e4m3: each row times a power of two, which takes its largest element into [128, 256), in two parts, what
-            // the first leaves in the second: four bits each, so that elements down to 2^-9 of it are exact.
-            float mx = 0.f;
+          for (int i = 0; i < L; ++i) {
+            const int row_t = q4 * 32 + rr + i * R;  // of the tile
+            if (x < P)
+              st_shared_v4(su32(dst + (x / 8) * G::SLICE + row_t * 128 + (((x % 8) ^ (row_t & 7)) << 4)), piece[i].x, piece[i].y,
+                           piece[i].z, piece[i].w);
+          }
+        } else {
+          // e4m3: each row times a power of two, which takes its largest element into [128, 256), in two parts, what
+          // the first leaves in the second: four bits each, so that elements down to 2^-9 of it are exact.  A short loop:
+          // its instructions are fetched once for every item (unrolled: 5 us more).
+          constexpr int B = L < 4 ? L : 4;
+          uint4 piece[B];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max3(mx, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+          for (int i = 0; i < B; ++i) piece[i] = load_q();
+#pragma unroll 1
+          for (int i0 = 0; i0 * R < rows_here && i0 < L; i0 += B) {
+            uint4 later[B];
 #pragma unroll
-            for (int o = 1; o < L; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            float down = 1.f, its_up = 1.f;
-            const uint32_t eb = __float_as_uint(mx) & 0x7F800000u;
-            if (eb == 0x7F800000u) {
-              down = NAN;  // the conversion would make an infinite element a finite one
-            } else if (eb >= 0x04000000u) {  // else zero or below 2^-119
-              down = __uint_as_float(0x82800000u - eb);
-              its_up = __uint_as_float(eb - 0x03800000u);
-            }
-            // Thread r of the warp wants row r's.
-            const float u = __shfl_sync(0xffffffffu, its_up, (lane % R) * L);
-            if (lane / R == i) up = u;
-            if ((two || g == 0) && x < P) {
+            for (int i = 0; i < B; ++i) later[i] = load_q();
+#pragma unroll
+            for (int i = 0; i < B; ++i, rr += R) {
+              const int row_t = q4 * 32 + rr;
+              uint32_t top = largest_bf16(piece[i]);
+#pragma unroll
+              for (int o = 1; o < L; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const uint32_t eb = (top & 0x7F80u) << 16;
+              float down = 1.f, its_up = 1.f;
+              if (eb == 0x7F800000u) {
+                down = NAN;  // infinite or NaN; the conversion would make an infinite element a finite one
+              } else if (eb >= 0x04000000u) {  // else zero or below 2^-119
+                down = __uint_as_float(0x82800000u - eb);
+                its_up = __uint_as_float(eb - 0x03800000u);
+              }
+              if (x == 0) q_up[tile * kRows + row_t] = its_up;
               uint32_t one[2], rest[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) split_e4m3(v[2 * e], v[2 * e + 1], down, one[e], rest[e]);
-              const uint32_t at = su32(dst + rr * 128) + (((x / 2) ^ (rr & 7)) << 4) + (x & 1) * 8;
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(one[0]), "r"(one[1]) : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + G::SLICE), "r"(rest[0]), "r"(rest[1]) : "memory");
+              split_e4m3(piece[i].x, piece[i].y, down, one[0], rest[0]);
+              split_e4m3(piece[i].z, piece[i].w, down, one[1], rest[1]);
+              if (x < P) {
+                const uint32_t at = su32(dst + row_t * 128) + (((x / 2) ^ (row_t & 7)) << 4) + (x & 1) * 8;
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(one[0]), "r"(one[1]) : "memory");
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + G::SLICE), "r"(rest[0]), "r"(rest[1]) : "memory");
+              }
             }
-          } else if ((two || g == 0) && x < P) {
-            st_shared_v4(su32(dst + (x / 8) * G::SLICE + rr * 128 + (((x % 8) ^ (rr & 7)) << 4)), v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int i = 0; i < B; ++i) piece[i] = later[i];
           }
         }
-      }
-      if (two || g == 0) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_ready[tile]);
+      }
+      float up = 1.f;
+      if (Q8 && works) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_ready[tile], 0));  // the first group's
+        if (live) up = q_up[tile * kRows + r];
       }
       scale = fmaxf(scale * up, 1e-37f);  // not 0: a masked score stays -inf
     }
     int n = 0;  // jobs of this group so far
     const int n_jobs = two ? (g ? nb : nb0) : (nb + 1 - g) / 2;
-    for (; ok && n < n_jobs; ++n) {
+    for (; works && ok && n < n_jobs; ++n) {
       const int b = two ? n : 2 * n + g;
       const int k0 = (b_lo + b) * kKeys;
       float sv[128];
@@ -781,7 +868,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // Scores that the row does not see become -inf; those of keys whose value is not finite NaN.
       auto mask_out = [&] {
         if (b < first_part) return true;
-        if (!Q8 && !(ok = __all_sync(0xffffffffu, mbar_wait(&v_clean[b % G::VS], ((b - first_part) / G::VS) & 1)))) return false;
+        const bool there = Q8 ? mbar_wait(&v_full[b % G::VS], (b / G::VS) & 1)
+                              : mbar_wait(&v_clean[b % G::VS], ((b - first_part) / G::VS) & 1);
+        if (!(ok = __all_sync(0xffffffffu, there))) return false;
         // Four keys of a lane are looked at at once; hardly ever is one bad.
         const bool some = Q8 && __any_sync(0xffffffffu, bad_keys[(b % G::VS) * (kKeys / 4) + lane] != 0);
 #pragma unroll
@@ -827,7 +916,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       };
       if constexpr (Q8) {
         const uint32_t scales = su32(smem + G::OFF_SC + (b % G::NSC) * G::SCN * 4);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[b % G::VS], (b / G::VS) & 1)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[b % G::NSC], (b / G::NSC) & 1)))) break;
         load();
         if (!ok) break;
 #pragma unroll
@@ -920,7 +1009,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       if (lane == 0) mbar_arrive(&p_full[g]);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_final[g], 0));
-    if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
+    if (!works) ok = false;
+    if (works && !ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
     fence_after();
     const size_t pi = (((size_t)blockIdx.y * c.n_kv_heads + kh) * 256) + tile * kRows + r;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + (size_t)head * HD;
