@@ -66,8 +66,8 @@ struct Geo {
   static constexpr int TILE = NX * SLICE;         // V block in 16 bits
   // bf16: Q tile and K block as V.  e4m3: K as it comes, a slice of up to 128 codes a row; Q in two parts like it.
   static constexpr int QT = Q8 ? 2 * SLICE : TILE, KB = Q8 ? SLICE : TILE;
-  static constexpr int KS = Q8 ? 3 : NX == 2 ? 2 : 4;   // K blocks in flight
-  static constexpr int VS = NX == 2 ? (Q8 ? 2 : 3) : 4;
+  static constexpr int KS = NX == 2 || Q8 ? 3 : 4;   // K blocks in flight (bf16: of drafts over long caches 549 us with 2, 494 with 3)
+  static constexpr int VS = NX == 2 ? 2 : 4;
   // e4m3: V as it comes, a unit of 32 keys for each converter warp; with one tile, more of them where the second Q
   // tile would be.
   static constexpr int UNIT = 32 * HD;
@@ -127,9 +127,10 @@ __device__ __forceinline__ bool look(const Args& A, int i, Item& it, bool tell) 
 
 // Which item this CTA takes, found by all its threads: requests in order, of each
 // request its cut ranges of keys, of those its double tiles, the last (most keys) first.
-// A request's keys are cut into ranges of `cb` blocks, the same for the whole call, such
-// that all of it makes about kItems items.
-// Up to 32 requests: every warp by itself, without a barrier.
+// A request's keys are cut into equal ranges of at most `cb` blocks, such that kItems items would
+// hold all of the call's.
+// Up to 32 requests: every warp by itself, without a barrier; where keys are cut, requests of
+// longer ranges come first, so that the last CTAs to run are short.
 __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
   const cdb_prompt_attention_args& a = A.a;
   const int lane = threadIdx.x & 31, step = 2 * A.tokens;
@@ -142,15 +143,26 @@ __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
     const int work = __reduce_add_sync(0xffffffffu, on ? nt * blocks : 0);  // cutting calls have few tiles
     cb = max(kMinBlocks, div_up(work, A.cut));
   }
-  const int nc = on ? div_up(blocks, cb) : 0;
+  const int nc = on ? div_up(blocks, cb) : 0, range = nc ? div_up(blocks, nc) : 0;
   int xi = nt * nc, xt = nt;
+  int tiles = 0;
+  if (A.cut) {
+    xi = xt = 0;
+#pragma unroll 4
+    for (int j = 0; j < min(32, a.requests); ++j) {
+      const int r = __shfl_sync(0xffffffffu, range, j), t = __shfl_sync(0xffffffffu, nt, j), n = __shfl_sync(0xffffffffu, nc, j);
+      if (r > range || (r == range && j < lane)) xi += t * n;
+      if (j < lane) xt += t;
+      tiles += t;
+    }
+  } else {
 #pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
-    if (lane >= o) xi += p, xt += q;
+    for (int o = 1; o < 32; o *= 2) {
+      const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
+      if (lane >= o) xi += p, xt += q;
+    }
+    xi -= nt * nc, xt -= nt;
   }
-  const int tiles = __shfl_sync(0xffffffffu, xt, 31);
-  xi -= nt * nc, xt -= nt;
   const uint32_t mine = __ballot_sync(0xffffffffu, on && y >= xi && y < xi + nt * nc);
   if (A.cut && tell) {  // for the join
     if (on)
@@ -160,7 +172,7 @@ __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
   const int from = mine ? __ffs(mine) - 1 : 0;
   const int k = y - xi, tile = nt ? nt - 1 - k % nt : 0;
   it.t0 = tile * step;
-  it.chunk = nt ? k / nt : 0, it.chunks = nc, it.cb = cb;
+  it.chunk = nt ? k / nt : 0, it.chunks = nc, it.cb = A.cut ? range : cb;
   it.tile = xt + tile;
   int* f = reinterpret_cast<int*>(&it);
 #pragma unroll
@@ -215,7 +227,7 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
     if (on && y >= xi && y < xi + nt * nc) {
       const int k = y - xi, tile = nt - 1 - k % nt;
       it.t0 = tile * step;
-      it.chunk = k / nt, it.chunks = nc, it.cb = cb;
+      it.chunk = k / nt, it.chunks = nc, it.cb = A.cut ? max(1, div_up(div_up(it.len, kKeys), nc)) : cb;
       it.tile = xt + tile;
       found = it;
     }
