@@ -54,7 +54,7 @@ using namespace tc;
 constexpr int kRows = 128;   // query rows of a tile
 constexpr int kKeys = 128;   // keys of a block: eight pages
 constexpr int kSms = 152;
-constexpr int kItems = 3 * kSms;  // items (times KV heads) that cutting keys aims at
+constexpr int kItems = kSms;      // items (times KV heads) that cutting keys aims at
 constexpr int kMinBlocks = 2;     // blocks of a cut item, at least
 constexpr int kCutBelow = 4 * kSms;  // items without cutting, above which no call cuts
 
@@ -67,12 +67,12 @@ struct Geo {
   // bf16: Q tile and K block as V.  e4m3: K as it comes, a slice of up to 128 codes a row; Q in two parts like it.
   static constexpr int QT = Q8 ? 2 * SLICE : TILE, KB = Q8 ? SLICE : TILE;
   static constexpr int KS = NX == 2 || Q8 ? 3 : 4;   // K blocks in flight (bf16: of drafts over long caches 549 us with 2, 494 with 3)
-  static constexpr int VS = NX == 2 ? 2 : 4;
-  // e4m3: V as it comes, a unit of 32 keys for each converter warp; with one tile, more of them where the second Q
-  // tile would be.
+  // V blocks in flight; with one tile, one more where the second Q tile would be (32 drafts behind 16000 tokens of 32/8
+  // heads, bf16: 466 us without, 440 with).
+  static constexpr int VS = NX == 2 ? 2 : 4, VX = NX == 2 ? 1 : 0;
+  // e4m3: V as it comes, a unit of 32 keys for each converter warp.
   static constexpr int UNIT = 32 * HD;
   static constexpr int NU = NX == 2 ? 2 : 3;      // units of a warp in flight
-  static constexpr int MORE = QT / (4 * UNIT) > 4 ? 4 : QT / (4 * UNIT);
   static constexpr int NT = 8;                    // blocks whose end is told apart: more than a ring's slots and three
   static constexpr int NSC = 4;                   // blocks whose scales are kept
   static constexpr int SCN = 3 * kKeys + 4;       // scales of K, of V, the latter's logarithms, the largest of those by quarters
@@ -81,11 +81,11 @@ struct Geo {
   static constexpr int OFF_U = OFF_V + VS * TILE;
   static constexpr int OFF_SC = OFF_U + (Q8 ? 4 * NU * UNIT : 0);
   static constexpr int OFF_BAD = OFF_SC + (Q8 ? NSC * SCN * 4 : 0);  // [VS] keys whose value is not finite: bits (bf16), bytes (e4m3)
-  // float2 [2][kRows], with one tile; bf16: in the second's place
-  static constexpr int OFF_XCH = Q8 ? OFF_BAD + VS * kKeys : QT;
-  static constexpr int OFF_UP = OFF_BAD + VS * (Q8 ? kKeys : 16) + (Q8 ? 2 * kRows * 8 : 0);
+  // float2 [2][kRows], with one tile: the last K slot, which is not in use when a group has finished, or has nothing to do
+  static constexpr int OFF_XCH = OFF_K + (KS - 1) * KB;
+  static constexpr int OFF_UP = OFF_BAD + (VS + VX) * (Q8 ? kKeys : 16);
   static constexpr int OFF_BAR = OFF_UP + (Q8 ? 2 * kRows * 4 : 0);
-  static constexpr int NBAR = 2 + KS + 2 * VS + NT + 2 + 2 + 2 + 2 + 2 * 4 * (NU + MORE) + NSC;
+  static constexpr int NBAR = 2 + KS + 2 * (VS + VX) + NT + 2 + 2 + 2 + 2 + 2 * 4 * NU + NSC;
   static constexpr size_t SMEM = 1024 + OFF_BAR + NBAR * 8 + 16;
   static constexpr int THREADS = Q8 ? 512 : 384;
   static constexpr int S_COL = 256;               // [2][128] scores, then weights
@@ -366,14 +366,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + G::OFF_BAR);  // [2]
   uint64_t* k_full = q_ready + 2;
   uint64_t* v_full = k_full + G::KS;
-  uint64_t* v_clean = v_full + G::VS;    // blocks that were looked through
-  uint64_t* taken = v_clean + G::VS;     // V of this block, and K of the next, are free
+  uint64_t* v_clean = v_full + G::VS + G::VX;    // blocks that were looked through
+  uint64_t* taken = v_clean + G::VS + G::VX;     // V of this block, and K of the next, are free
   uint64_t* s_full = taken + G::NT;      // [2] by group
   uint64_t* p_full = s_full + 2;
   uint64_t* o_final = p_full + 2;
   uint64_t* done = o_final + 2;
   uint64_t* k_first = done + 1;          // K of the groups' first blocks is free
-  constexpr int kUnits = 4 * (G::NU + G::MORE);
+  constexpr int kUnits = 4 * G::NU;
   uint64_t* u_full = k_first + 1;        // [slots][4]
   uint64_t* u_empty = u_full + kUnits;
   uint64_t* sc_full = u_empty + kUnits;  // [NSC]
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     for (int s = 0; s < G::KS; ++s) {
       mbar_init(&k_full[s], 1);
     }
-    for (int s = 0; s < G::VS; ++s) {
+    for (int s = 0; s < G::VS + G::VX; ++s) {
       mbar_init(&v_full[s], Q8 ? 4 : 1);
       mbar_init(&v_clean[s], 1);
     }
@@ -451,10 +451,12 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     return gone < 0 ? mbar_wait(k_first, 0) : wait_taken(gone);
   };
 
-  const int units = G::NU + (two ? 0 : G::MORE);  // e4m3: units of a converter warp in flight
-  auto unit_at = [&](int s, int w) {
-    return s < G::NU ? smem + G::OFF_U + (s * 4 + w) * G::UNIT : smem + G::QT + ((s - G::NU) * 4 + w) * G::UNIT;
-  };
+  auto unit_at = [&](int s, int w) { return smem + G::OFF_U + (s * 4 + w) * G::UNIT; };
+  // V's ring: slots, a block's slot and turn, and where a slot is.
+  const int slots_v = two ? G::VS : G::VS + G::VX;
+  auto v_slot = [&](int b) { return two || !G::VX ? b % G::VS : b % (G::VS + G::VX); };
+  auto v_turn = [&](int b) { return (two || !G::VX ? b / G::VS : b / (G::VS + G::VX)) & 1; };
+  auto v_at = [&](int s) { return s < G::VS ? G::OFF_V + s * G::TILE : G::QT; };
 
   static_assert(!Q8 || 256 * 176 + 256 * 80 <= 512 * 128, "registers of the launch");
   static_assert(Q8 || 256 * 208 + 128 * 72 <= 384 * 168, "registers of the launch");
@@ -502,17 +504,17 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           const int b = two ? n : 2 * n + g, last = two && g == 0 ? nb0 : nb;  // blocks of this group end at `last`
           if (!ok || b >= last) continue;
           const bool more = b + far < last;
-          const int sv = b % G::VS, sk = (b + far) % G::KS;
+          const int sv = v_slot(b), sk = (b + far) % G::KS;
           uint32_t bar = bar_at(v_full, sv);
-          int phase = b / G::VS;
+          int phase = v_turn(b);
           // v_clean completes a phase for each block looked through that came to this slot.
-          if (!Q8 && b >= first_part) bar = bar_at(v_clean, sv), phase = (b - first_part) / G::VS;
+          if (!Q8 && b >= first_part) bar = bar_at(v_clean, sv), phase = v_turn(b - first_part);
           if (lane == 1) bar = bar_at(p_full, g), phase = n;
           if (lane == 2 && more) bar = bar_at(k_full, sk), phase = (b + far) / G::KS;
           ok = __all_sync(0xffffffffu, wait_at(bar, phase & 1));
           if (!ok) continue;
           fence_after();
-          const uint32_t vb = v + sv * (G::TILE / 16);
+          const uint32_t vb = v + (uint32_t)((v_at(sv) - G::OFF_V) / 16);
           const uint32_t d = tmem + G::O_COL + g * kRows, p = tmem + G::S_COL + g * kKeys;
           const int pages = b == nb - 1 ? tail : 8;
           issue_values(d, p, vb, up_v, idO, pages, n > 0);
@@ -560,13 +562,13 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
             if (++s == G::KS) s = 0;
           } else {
             // The converters of the units have done with what was there.
-            if (j >= units && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[s * 4 + (lane & 3)], turn ^ 1)))) break;
+            if (j >= G::NU && !(ok = __all_sync(0xffffffffu, mbar_wait(&u_empty[s * 4 + (lane & 3)], turn ^ 1)))) break;
             if (lane < 4) mbar_arrive_tx(&u_full[s * 4 + lane], (uint32_t)__popc((there >> (2 * lane)) & 3) * (16 * HD));
             __syncwarp();
             if (blk >= 0)
               bulk_1d(su32(unit_at(s, lane / 2)) + (lane & 1) * 16 * HD, static_cast<const uint8_t*>(c.pool) + r * HD, 16 * HD,
                       &u_full[s * 4 + lane / 2]);
-            if (++s == units) s = 0, turn ^= 1;
+            if (++s == G::NU) s = 0, turn ^= 1;
           }
           __syncwarp();
           issued = j + 1;
@@ -574,22 +576,20 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         }
         if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
         // Copies in flight land before the CTA may leave (at once when everything was used).
-        const int slots = kv ? units : G::KS;
+        const int slots = kv ? G::NU : G::KS;
         for (int j = max(0, issued - slots); j < issued; ++j)
           mbar_wait(kv ? &u_full[j % slots * 4 + (lane & 3)] : &k_full[j % slots], (j / slots) & 1);
       } else {
-        constexpr int slots_k = G::KS, slots_v = G::VS;
-        const int slots = kv ? slots_v : slots_k;
+        const int slots = kv ? slots_v : G::KS;
         uint64_t* full = kv ? v_full : k_full;
-        const uint32_t ring = su32(smem + (kv ? G::OFF_V : G::OFF_K));
         uint64_t pol;  // a sequence's keys are read again by its other tiles
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
         // The blocks that some rows do not see: rows behind the end and rows with a value that is not finite
         // become zeros; the latter are noted.
         auto clean = [&](int b) {
-          const int s = b % slots, left = min(kKeys, end - (b_lo + b) * kKeys);
-          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[s], (b / slots) & 1))) return false;
-          uint8_t* v = smem + G::OFF_V + s * G::TILE;
+          const int s = v_slot(b), left = min(kKeys, end - (b_lo + b) * kKeys);
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[s], v_turn(b)))) return false;
+          uint8_t* v = smem + v_at(s);
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int r = i * 32 + lane;
@@ -620,6 +620,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
         int cleaned = kv ? first_part : nb;
         for (int j = 0; j < nb; ++j) {
           const int s = j % slots;
+          const uint32_t to = su32(smem + (kv ? v_at(s) : G::OFF_K + s * G::TILE));
           const int blk = lane < 8 ? block_at((b_lo + j) * 8 + lane) : -1;
           const uint32_t there = __ballot_sync(0xffffffffu, blk >= 0);
           // A slot to be filled again may hold a block that waits to be looked through.
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
               const int y = (int)row_of(bi, kv);
 #pragma unroll
               for (int x = 0; x < G::NX; ++x)
-                tma_2d(ring + s * G::TILE + x * G::SLICE + i * 2048, &tmk, &full[s], x * 128, y, pol);
+                tma_2d(to + x * G::SLICE + i * 2048, &tmk, &full[s], x * 128, y, pol);
             }
             __syncwarp();
           }
@@ -689,9 +690,9 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       int ahead = pool_block(3), s = 0, turn = 0;
       bool ok = true;
       for (int b = 0; b < nb; ++b) {
-        const int slot = b % G::VS;
+        const int slot = v_slot(b);
         // Lane 1 waits for the slot, lane 2 for the place of the scales two blocks on, the others for the codes.
-        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= G::VS        ? wait_taken(b - G::VS)
+        if (!(ok = __all_sync(0xffffffffu, lane == 1 && b >= slots_v      ? wait_taken(b - slots_v)
                                            : lane == 2 && b + 2 >= G::NSC ? wait_taken(b + 2 - G::NSC)
                                                                           : mbar_wait(&u_full[s * 4 + w], turn))))
           break;
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           ahead = pool_block(b + 4);
         }
         const uint8_t* raw = unit_at(s, w);
-        uint8_t* to = smem + G::OFF_V + slot * G::TILE;
+        uint8_t* to = smem + v_at(slot);
         const int left = end - (b_lo + b) * kKeys - w * 32;  // keys of this unit that are there
         const bool part = b >= first_part;
         const int x = lane % CL;
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           mbar_arrive(&u_empty[s * 4 + w]);
           mbar_arrive(&v_full[slot]);
         }
-        if (++s == units) s = 0, turn ^= 1;
+        if (++s == G::NU) s = 0, turn ^= 1;
         bad_scales[0] = bad_scales[1], bad_scales[1] = bad_scales[2];
       }
       if (!ok && lane == 0) report(a.status, CDB_OPS_TIMEOUT);
@@ -880,16 +881,16 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // Scores that the row does not see become -inf; those of keys whose value is not finite NaN.
       auto mask_out = [&] {
         if (b < first_part) return true;
-        const bool there = Q8 ? mbar_wait(&v_full[b % G::VS], (b / G::VS) & 1)
-                              : mbar_wait(&v_clean[b % G::VS], ((b - first_part) / G::VS) & 1);
+        const int slot = v_slot(b);
+        const bool there = Q8 ? mbar_wait(&v_full[slot], v_turn(b)) : mbar_wait(&v_clean[slot], v_turn(b - first_part));
         if (!(ok = __all_sync(0xffffffffu, there))) return false;
         // Four keys of a lane are looked at at once; hardly ever is one bad.
-        const bool some = Q8 && __any_sync(0xffffffffu, bad_keys[(b % G::VS) * (kKeys / 4) + lane] != 0);
+        const bool some = Q8 && __any_sync(0xffffffffu, bad_keys[slot * (kKeys / 4) + lane] != 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w = seen(k0 + i * 32, lim, mask, nodes);
-          const uint32_t bits = !Q8 ? bad_keys[(b % G::VS) * 4 + i]
-                                : some ? __ballot_sync(0xffffffffu, bad_bytes[(b % G::VS) * kKeys + i * 32 + lane] != 0) : 0u;
+          const uint32_t bits = !Q8 ? bad_keys[slot * 4 + i]
+                                : some ? __ballot_sync(0xffffffffu, bad_bytes[slot * kKeys + i * 32 + lane] != 0) : 0u;
           const uint32_t bad = bits & w;
           if (!__all_sync(0xffffffffu, w == ~0u)) {
 #pragma unroll
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
     } else {
       // The groups' halves: each has waited for its own accumulator's last product, and reads the other's too, which
       // these fences order behind the other group's wait.
-      xch[g * kRows + r] = make_float2(m, l);
+      if (works) xch[g * kRows + r] = make_float2(m, l);
       fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       fence_after();
