@@ -261,15 +261,15 @@ int cdb_rotate(const cdb_rotate_args *a, void *stream);
  * they were.  Softmax statistics and sums are fp32; weights enter the products
  * as 16-bit numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache,
  * one, weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
- * With an e4m3 cache a query's elements are exact down to 2^-17 of the head's largest
- * one, smaller ones within 2^-25 of that.
+ * With an e4m3 cache a query's elements are exact down to 2^-8 of the head's largest
+ * one, smaller ones within 2^-17 of that; a head with an infinite element counts as NaN.
  * Keys and values that no row sees may hold anything.  Inside the stretch that
  * some rows of a request see and others do not, a value with an infinite or NaN
  * element makes the rows that see it NaN in all elements of the head, and does not
  * touch the others.
- * Where a call has less work than the GPU has room for, keys are cut among CTAs
- * and joined, by the lengths of all its requests: this changes roundings, never
- * from one run to the next.
+ * Where a call has few rows for the GPU, keys are cut among CTAs and joined, by the
+ * lengths of all its requests: this changes roundings, never from one run to the
+ * next.  max_ctx costs nothing but that a call within 256 tokens is never cut.
  * workspace: cdb_prompt_attention_workspace() bytes, 256-byte aligned, any
  * contents; used by one call at a time. */
 #define CDB_DRAFT_MAX 256

@@ -6,7 +6,8 @@ are not a request's hold a sentinel.
 Tolerances.  A score is a sum of head_dim exact products, accumulated in fp32 with at most 2^-23 per step of
 S = |scale| * sum |q k|; a weight e^s is then off by that (as an exponent) plus 2^-20 for the exponential and its
 16-bit form: two numbers within 2^-17 (bf16 cache), or one of weight times value scale within 2^-11 of it or 2^-33
-of the largest (e4m3 cache, whose queries lose 2^-25 of their largest element); weights enter twice (numerator, sum).
+of the largest (e4m3 cache); weights enter twice (numerator, sum).  With an e4m3 cache an element of a query below
+2^-8 of the head's largest one may be off by 2^-17 of that.
 The weighted sum adds 2^-23 of max |v| per accumulation step (16 keys each) and per joined range.  A bf16 output
 adds 2^-8 of its value.
 """
@@ -118,7 +119,9 @@ def expected(cs, i, scale):
     steps = 16 + length / 16 + length / 64
     w = 2.0 ** -17
     if cs["dtype"] == "e4m3":
-        w = 2.0 ** -11 + length * 2.0 ** -33 + 2.0 ** -25 * hd * S
+        top = q.abs().amax(-1, keepdim=True)
+        small = torch.einsum("tkgd,lkd->tkgl", (q.abs() < 2.0 ** -8 * top).double() * top, big).amax() * abs(scale)
+        w = 2.0 ** -11 + length * 2.0 ** -33 + 2.0 ** -17 * small
     tol = 2.0 ** -8 * o.abs() + vm[:, :, None, None] * (2 * (hd * 2.0 ** -23 * S + 2.0 ** -20 + w) + steps * 2.0 ** -23) + 1e-30
     return o.reshape(c, heads, hd), tol.reshape(c, heads, hd)
 
