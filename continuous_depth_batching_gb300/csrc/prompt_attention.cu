@@ -67,9 +67,9 @@ struct Geo {
   // bf16: Q tile and K block as V.  e4m3: K as it comes, a slice of up to 128 codes a row; Q in two parts like it.
   static constexpr int QT = Q8 ? 2 * SLICE : TILE, KB = Q8 ? SLICE : TILE;
   static constexpr int KS = NX == 2 || Q8 ? 3 : 4;   // K blocks in flight (bf16: of drafts over long caches 549 us with 2, 494 with 3)
-  // V blocks in flight; with one tile, one more where the second Q tile would be (32 drafts behind 16000 tokens of 32/8
-  // heads, bf16: 466 us without, 440 with).
-  static constexpr int VS = NX == 2 ? 2 : 4, VX = NX == 2 ? 1 : 0;
+  // V blocks in flight; bf16, with one tile: one more where the second Q tile would be (32 drafts behind 16000 tokens of 32/8
+  // heads: 466 us without, 440 with; e4m3: no change, 1% less for prompts).
+  static constexpr int VS = NX == 2 ? 2 : 4, VX = NX == 2 && !Q8 ? 1 : 0;
   // e4m3: V as it comes, a unit of 32 keys for each converter warp.
   static constexpr int UNIT = 32 * HD;
   static constexpr int NU = NX == 2 ? 2 : 3;      // units of a warp in flight
@@ -144,24 +144,23 @@ __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
     cb = max(kMinBlocks, div_up(work, A.cut));
   }
   const int nc = on ? div_up(blocks, cb) : 0, range = nc ? div_up(blocks, nc) : 0;
-  int xi = nt * nc, xt = nt;
-  int tiles = 0;
-  if (A.cut) {
-    xi = xt = 0;
-#pragma unroll 4
-    for (int j = 0; j < min(32, a.requests); ++j) {
-      const int r = __shfl_sync(0xffffffffu, range, j), t = __shfl_sync(0xffffffffu, nt, j), n = __shfl_sync(0xffffffffu, nc, j);
-      if (r > range || (r == range && j < lane)) xi += t * n;
-      if (j < lane) xt += t;
-      tiles += t;
-    }
-  } else {
+  const int own = nt * nc;
+  int xi = own, xt = nt;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
-      if (lane >= o) xi += p, xt += q;
+  for (int o = 1; o < 32; o *= 2) {
+    const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, xt, o);
+    if (lane >= o) xi += p, xt += q;
+  }
+  const int tiles = __shfl_sync(0xffffffffu, xt, 31);
+  xi -= own, xt -= nt;
+  if (A.cut && a.requests > 1) {
+    const int key = range * 32 + 31 - lane;  // by range, then by request
+    xi = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int other = __shfl_sync(0xffffffffu, key, j), n = __shfl_sync(0xffffffffu, own, j);
+      xi += other > key ? n : 0;
     }
-    xi -= nt * nc, xt -= nt;
   }
   const uint32_t mine = __ballot_sync(0xffffffffu, on && y >= xi && y < xi + nt * nc);
   if (A.cut && tell) {  // for the join
