@@ -32,8 +32,12 @@
 // rows see, V rows with such an element are set to zero in shared memory before the
 // product, and rows that see them take a NaN weight; V rows behind the sequence's
 // end, which may hold anything, are set to zero too.
-// What bounds it: two products (three with two-part weights) of 512 cycles and 128 x 128
-// exponentials of 512 or more a job, for a long prompt; HBM for drafts over long caches.
+// What bounds it.  A long bf16 prompt: the tensor cores, which compute three products of 512 cycles for a job (one
+// for the scores, two for weights in two parts), together with the waits and commits of the warp that feeds them
+// (8192 tokens of 32/8 heads: 550 us, 1.0 PFLOP/s of causal products; the products alone 470, softmax alone 445; pipe
+// 63% active).  Drafts over long bf16 caches: HBM (32 drafts of 16 tokens behind 16000: 5.3 of 6.8 TB/s).  e4m3: the
+// chain from scores to weights to the next scores, in which a key's scales are read from shared memory by every thread
+// (the same drafts: 2.2 TB/s).  Short calls: setup, one chain of loads and the join.
 // Every mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT,
 // lets its copies and MMAs finish (bounded), frees TMEM and returns.
 #include <algorithm>
@@ -1094,8 +1098,11 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
   }
 }
 
-// Adds up the ranges of keys of the requests that were cut.  A warp takes a token's row of one head; x: double tile
-// and its rows, 8 warps each.  Latency bounds it.
+// Adds up the ranges of keys of the requests that were cut.  A warp takes a token's row of one head at a time; a double
+// tile and KV head has kJoin CTAs of 8 warps.  Latency bounds it, and CTAs without anything to add up (whole call, a
+// batch of drafts / chunks behind cached tokens: 161 / 155 us with 32 CTAs, a row for each warp, 156 / 148 with 16, 169 /
+// 144 with 8).
+constexpr int kJoin = 16;
 template <int HD>
 __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ Args A) {
   pdl_wait();
@@ -1104,30 +1111,33 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ Arg
   const int chunks = info.w & 0xFFFF, nt = info.w >> 16;
   if (chunks < 2) return;
   const cdb_prompt_attention_args& a = A.a;
-  const int lane = threadIdx.x & 31, w = blockIdx.z * 8 + (threadIdx.x >> 5), kh = blockIdx.y;
-  const int tile = w / kRows, r = w % kRows, tk = info.y + tile * A.tokens + r / A.group;
+  const int lane = threadIdx.x & 31, kh = blockIdx.y;
   const int row0 = a.row_start[info.x], count = a.row_start[info.x + 1] - row0;
-  if (r >= A.tokens * A.group || tk >= count) return;
   constexpr int E = HD / 32;
-  const size_t p0 = ((size_t)info.z * a.cache.n_kv_heads + kh) * 256 + w, step = (size_t)nt * a.cache.n_kv_heads * 256;
-  float mj = -INFINITY;
-  for (int k = lane; k < chunks; k += 32) mj = fmaxf(mj, A.part_ml[p0 + k * step].x);
+  const size_t step = (size_t)nt * a.cache.n_kv_heads * 256;
+  for (int w = blockIdx.z * 8 + (threadIdx.x >> 5); w < 2 * kRows; w += 8 * kJoin) {
+    const int tile = w / kRows, r = w % kRows, tk = info.y + tile * A.tokens + r / A.group;
+    if (r >= A.tokens * A.group || tk >= count) continue;
+    const size_t p0 = ((size_t)info.z * a.cache.n_kv_heads + kh) * 256 + w;
+    float mj = -INFINITY;
+    for (int k = lane; k < chunks; k += 32) mj = fmaxf(mj, A.part_ml[p0 + k * step].x);
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, o));
-  float l = 0.f, v[E] = {};
+    for (int o = 16; o > 0; o /= 2) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, o));
+    float l = 0.f, v[E] = {};
 #pragma unroll 4
-  for (int k = 0; k < chunks; ++k) {
-    const float2 ml = A.part_ml[p0 + k * step];
-    const float f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - mj);
-    const float* po = A.part_o + (p0 + k * step) * HD + lane * E;
-    l = fmaf(ml.y, f, l);
+    for (int k = 0; k < chunks; ++k) {
+      const float2 ml = A.part_ml[p0 + k * step];
+      const float f = ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - mj);
+      const float* po = A.part_o + (p0 + k * step) * HD + lane * E;
+      l = fmaf(ml.y, f, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(po[e], f, v[e]);
+      for (int e = 0; e < E; ++e) v[e] = fmaf(po[e], f, v[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)(row0 + tk) * a.ldo + (size_t)(kh * A.group + r % A.group) * HD + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(v[e] * inv);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)(row0 + tk) * a.ldo + (size_t)(kh * A.group + r % A.group) * HD + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(v[e] * inv);
 }
 
 struct Plan {
@@ -1172,7 +1182,7 @@ cudaError_t launch(cudaStream_t s, const Args& A) {
   cudaError_t e = launch_pdl(k_prompt<HD, Q8>, dim3(c.n_kv_heads, A.tiles + A.cut), dim3(G::THREADS), G::SMEM, s, tk, A);
   if (e != cudaSuccess || !A.cut) return e;
   count_launch();
-  return launch_pdl(k_prompt_join<HD>, dim3(A.tiles, c.n_kv_heads, 32), dim3(256), 0, s, A);
+  return launch_pdl(k_prompt_join<HD>, dim3(A.tiles, c.n_kv_heads, kJoin), dim3(256), 0, s, A);
 }
 
 }  // namespace pa
