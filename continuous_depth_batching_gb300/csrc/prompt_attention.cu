@@ -34,10 +34,10 @@
 // end, which may hold anything, are set to zero too.
 // What bounds it.  A long bf16 prompt: the tensor cores, which compute three products of 512 cycles for a job (one
 // for the scores, two for weights in two parts), together with the waits and commits of the warp that feeds them
-// (8192 tokens of 32/8 heads: 550 us, 1.0 PFLOP/s of causal products; the products alone 470, softmax alone 445; pipe
-// 63% active).  Drafts over long bf16 caches: HBM (32 drafts of 16 tokens behind 16000: 5.3 of 6.8 TB/s).  e4m3: the
+// (8192 tokens of 32/8 heads: 555 us, 1.0 PFLOP/s of causal products; of 547 before, the products alone took 472 and
+// softmax alone 444; pipe 63% active).  Drafts over long bf16 caches: HBM (32 drafts of 16 tokens behind 16000: 5.3 of 6.8 TB/s).  e4m3: the
 // chain from scores to weights to the next scores, in which a key's scales are read from shared memory by every thread
-// (the same drafts: 2.2 TB/s).  Short calls: setup, one chain of loads and the join.
+// (the same drafts: 2.4 TB/s).  Short calls: setup, one chain of loads and the join.
 // Every mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT,
 // lets its copies and MMAs finish (bounded), frees TMEM and returns.
 #include <algorithm>
@@ -58,9 +58,14 @@ using namespace tc;
 constexpr int kRows = 128;   // query rows of a tile
 constexpr int kKeys = 128;   // keys of a block: eight pages
 constexpr int kSms = 152;
-constexpr int kItems = kSms;      // items (times KV heads) that cutting keys aims at
-constexpr int kMinBlocks = 2;     // blocks of a cut item, at least
-constexpr int kCutBelow = 4 * kSms;  // items without cutting, above which no call cuts
+// Items (times KV heads) that cutting keys aims at.  One for each SM: setup, q and the end of an item do not overlap
+// with another (32 drafts over 500 to 8000 e4m3 keys 162 us, chunks behind cached tokens 154; three for each SM 195 and
+// 183, one and a half or two 177 to 180 for the drafts).
+constexpr int kItems = kSms;
+constexpr int kMinBlocks = 2;  // blocks of a cut item, at least (8 nodes behind 1000 tokens: 15.9 us, with four 20.8)
+// Items without cutting, from which on no call cuts: SMs are busy then.  Half as many: 2500 tokens of 32/8 heads 84 us for
+// 88, 4096 tokens 171 for 176, chunks behind cached tokens 150 for 147; twice as many: 6000 tokens 334 for 323.
+constexpr int kCutBelow = 4 * kSms;
 
 template <int HD, bool Q8>
 struct Geo {
@@ -281,8 +286,7 @@ __device__ __forceinline__ uint32_t seen(int s, int lim, const uint32_t* mask, i
 }
 
 // The products of one job, each issued as one piece: one lane is elected inside, and descriptors
-// are made from 32-bit words by additions of constants.  (A call for every 128 x 128 x 16 product
-// took its warp 65 cycles to issue, as long as it takes to compute.)
+// are made from 32-bit words by additions of constants.
 #define CDB_SS(off, acc)                                                                         \
   " add.u32 x, %1, " off ";\n mov.b64 da, {x, %3};\n add.u32 x, %2, " off ";\n mov.b64 db, {x, %3};\n" \
   " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " acc ";\n"
