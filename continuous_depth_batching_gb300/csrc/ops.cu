@@ -159,9 +159,10 @@ int cdb_plan_pages(const cdb_plan_pages_args* a, void* stream) {
   CDB_ENTRY_BEGIN
   if (!a) return refuse("no arguments");
   if (a->requests < 0 || a->requests > CDB_PLAN_MAX_REQUESTS) return refuse("requests must be in 0..8192");
-  if (a->max_rows < 0) return refuse("max_rows out of range");
+  // The kernel's 32-bit indices run up to one pass (4 rows of 4096 threads) behind max_rows and behind 4 free_slots.
+  if (a->max_rows < 0 || a->max_rows > (1 << 30)) return refuse("max_rows must be in 0..2^30");
   if (a->n_seqs < 1 || a->max_blocks < 1 || a->max_blocks > INT_MAX / 16) return refuse("n_seqs or max_blocks out of range");
-  if (a->free_slots < 1) return refuse("free_slots must be >= 1");
+  if (a->free_slots < 1 || a->free_slots > (1 << 28)) return refuse("free_slots must be in 1..2^28");
   if (!a->block_table || !a->free_blocks) return refuse("block_table and free_blocks are needed");
   if (!a->state || !a->state_out || !a->row_start) return refuse("state, state_out and row_start are needed");
   if (!aligned(a->state, 8) || !aligned(a->state_out, 8) || !aligned(a->row_slot, 8))

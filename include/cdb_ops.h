@@ -204,14 +204,14 @@ typedef struct {
   int32_t *block_table;         /* [n_seqs][max_blocks] */
   int n_seqs, max_blocks;
   int32_t *free_blocks;         /* [free_slots] */
-  int free_slots;
+  int free_slots;               /* <= 2^28 */
   const int64_t *state;         /* [2]: blocks taken and given so far */
   int64_t *state_out;           /* [2] */
   int32_t *lens_out;            /* [requests] */
   int32_t *row_start;           /* [requests + 1] */
   int32_t *row_seq, *row_pos;   /* [max_rows] */
   int64_t *row_slot;            /* [max_rows], or NULL */
-  int max_rows;
+  int max_rows;                 /* <= 2^30 */
   int32_t *status;
 } cdb_plan_pages_args;
 int cdb_plan_pages(const cdb_plan_pages_args *a, void *stream);

@@ -54,6 +54,12 @@ def test_plan_pages_refuses(L, bad):
     refused(L.cdb_plan_pages, pages_args(**bad))
 
 
+@pytest.mark.parametrize("bad", [dict(max_rows=2**30 + 1), dict(max_rows=2**31 - 1), dict(free_slots=2**28 + 1),
+                                 dict(free_slots=2**31 - 1)])
+def test_plan_pages_refuses_what_32_bit_indices_do_not_hold(L, bad):
+    refused(L.cdb_plan_pages, pages_args(**bad))
+
+
 def rotate_args(**kw):
     return filled(ops.RotateArgs(rows=3, n_heads=8, n_kv_heads=4, head_dim=64, x=P, dtype=0, ldx=768, pos=P, steps=P, rot_dim=64,
                                  factor=1.0, q_gain=P, k_gain=P, eps=1e-6, out=P, ldo=768), kw)
