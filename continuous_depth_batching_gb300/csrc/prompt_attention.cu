@@ -122,11 +122,13 @@ struct Item {
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
-// The request's double tiles, its blocks of keys; false: it is not there.
+// The request's double tiles, its blocks of keys; false: it is not there.  count < 0: row_start descends.  Where it does
+// not, requests that are there have rows of their own, hence A.tiles double tiles at most, all of them together.
 __device__ __forceinline__ bool look(const Args& A, int i, Item& it, bool tell) {
   const cdb_prompt_attention_args& a = A.a;
   const int r0 = a.row_start[i], r1 = a.row_start[i + 1], len = a.lens[i], seq = a.seq ? a.seq[i] : i;
-  it.request = i, it.seq = seq, it.row0 = r0, it.count = r1 - r0, it.len = len;
+  it.request = i, it.seq = seq, it.row0 = r0, it.count = r1 < r0 ? -1 : r1 - r0, it.len = len;
+  if (r1 < r0 && tell) report(a.status, CDB_OPS_BAD_ROW);
   if (seq < 0 || r1 == r0) return false;
   const bool ok = seq < a.cache.n_seqs && r0 >= 0 && r1 > r0 && r1 <= a.rows && len >= 0 && len <= a.max_ctx &&
                   (!a.visible || r1 - r0 <= 64 * a.mask_words);
@@ -145,7 +147,8 @@ __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
   const int lane = threadIdx.x & 31, step = 2 * A.tokens;
   const bool tell = blockIdx.x == 0 && y == 0 && threadIdx.x < 32;
   Item it = {};
-  const bool on = lane < a.requests && look(A, lane, it, tell);
+  const bool there = lane < a.requests && look(A, lane, it, tell);
+  const bool on = !__any_sync(0xffffffffu, it.count < 0) && there;
   const int nt = on ? div_up(it.count, step) : 0, blocks = max(1, div_up(it.len, kKeys));
   int cb = INT_MAX / kKeys;
   if (A.cut) {
@@ -199,15 +202,17 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, step = 2 * A.tokens;
   const bool tell = blockIdx.x == 0 && y == 0;
   Item it;
-  int cb = INT_MAX / kKeys;
+  int cb = INT_MAX / kKeys, falls = 0;
   if (A.cut) {
     long long work = 0;  // blocks of keys, once for each double tile
-    for (int i = tid; i < a.requests; i += THREADS)
+    for (int i = tid; i < a.requests; i += THREADS) {
       if (look(A, i, it, false)) work += (long long)div_up(it.count, step) * max(1, div_up(it.len, kKeys));
+      falls |= it.count < 0;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) work += __shfl_xor_sync(0xffffffffu, work, o);
     if (lane == 0) work_s[warp] = work;
-    __syncthreads();
+    falls = __syncthreads_or(falls);  // nothing is cut, or noted for the join, that may not fit the workspace
     work = 0;
     for (int w = 0; w < THREADS / 32; ++w) work += work_s[w];
     cb = (int)max((long long)kMinBlocks, (work + A.cut - 1) / A.cut);
@@ -216,7 +221,7 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
   int items = 0, tiles = 0;  // of the requests before this round
   for (int i0 = 0; i0 < a.requests; i0 += THREADS) {
     const int i = i0 + tid;
-    const bool on = i < a.requests && look(A, i, it, tell);
+    const bool on = i < a.requests && look(A, i, it, tell) && !falls;
     const int nt = on ? div_up(it.count, step) : 0, nc = on ? max(1, div_up(div_up(it.len, kKeys), cb)) : 0;
     int xi = nt * nc, xt = nt;
 #pragma unroll

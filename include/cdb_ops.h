@@ -258,7 +258,8 @@ int cdb_rotate(const cdb_rotate_args *a, void *stream);
  *                         nodes: its ancestors and itself).  Bits of rows that the
  *                         request does not have are ignored.
  * A row that sees nothing gives zeros.  Rows behind row_start[requests] are left as
- * they were.  Softmax statistics and sums are fp32; weights enter the products
+ * they were.  Where row_start descends anywhere, CDB_OPS_BAD_ROW is set and `out` is
+ * undefined.  Softmax statistics and sums are fp32; weights enter the products
  * as 16-bit numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache,
  * one, weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
  * With an e4m3 cache a query's elements are exact down to 2^-8 of the head's largest
