@@ -371,7 +371,7 @@ constexpr int kThreads = 256;
 // several entries may run ahead of their stores.  HBM bounds it (half of its rate: 16 paths of
 // 96 slots 14 us), or the latency of one load and one store (one path of 4 slots: 1.7 us).
 __global__ void __launch_bounds__(kThreads) k_keep_path(const __grid_constant__ cdb_keep_path_args a) {
-  __shared__ int from[CDB_DRAFT_MAX], to[CDB_DRAFT_MAX];  // 16 * block + offset
+  __shared__ long long from[CDB_DRAFT_MAX], to[CDB_DRAFT_MAX];  // 16 * block + offset, past 32 bits in large pools
   __shared__ int moves;
   const cdb_paged_cache& c = a.cache;
   const int i = blockIdx.y, tid = threadIdx.x;
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kThreads) k_keep_path(const __grid_constant__ 
       const int32_t* t = c.block_table + (size_t)seq * c.max_blocks;
       const int bs = t[src / 16], bd = t[dst / 16];
       if (bs < 0 || bs >= c.kv_blocks || bd < 0 || bd >= c.kv_blocks) bad = CDB_OPS_BAD_BLOCK;
-      from[tid] = bs * 16 + (int)(src % 16);
-      to[tid] = bd * 16 + (int)(dst % 16);
+      from[tid] = bs * 16ll + src % 16;
+      to[tid] = bd * 16ll + dst % 16;
       atomicMin(&moves, tid - CDB_DRAFT_MAX);  // entries before the first that moves are in place
     }
   }
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) k_keep_path(const __grid_constant__ 
     if (p < pieces) {
       const long long h = p / vec;
       const int piece = (int)(p - h * vec);
-      auto at = [&](int cell) { return (((long long)(cell / 16) * heads + h) * 16 + cell % 16) * vec + piece; };
+      auto at = [&](long long cell) { return (((cell >> 4) * heads + h) * 16 + (cell & 15)) * vec + piece; };
       for (int k = k0; k < n; k += B) {
         uint4 v[B];
 #pragma unroll
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) k_keep_path(const __grid_constant__ 
       }
     } else {
       const long long h = p - pieces;
-      auto at = [&](int cell) { return ((long long)(cell / 16) * heads + h) * 16 + cell % 16; };
+      auto at = [&](long long cell) { return ((cell >> 4) * heads + h) * 16 + (cell & 15); };
       for (int k = k0; k < n; k += B) {
         float v[B];
 #pragma unroll
