@@ -26,7 +26,7 @@
 //   warps 8, 11  copy K and V pages by TMA, and scales; bf16: then warp 11 looks the blocks that
 //                some rows do not see through (below);
 //   warps 12-15  e4m3: widen V's codes to fp16 in the MMA's swizzled layout.  K's codes are an
-//                operand as they are: q becomes the sum of two e4m3 numbers, exactly but for elements
+//                operand as they are: q becomes the sum of an e4m3 and an e5m2 number, exactly but for elements
 //                far below a row's largest, and the scores of both are added up.
 // A weight of 0 times an infinite or NaN value is NaN, so in blocks that not all
 // rows see, V rows with such an element are set to zero in shared memory before the
@@ -254,14 +254,17 @@ __device__ __forceinline__ Item find_item(const Args& A, int y) {
   return found;
 }
 
-// Two times two bf16 numbers times f as e4m3 codes, and what these leave of them (exactly: eight bits in all).
-__device__ __forceinline__ void split_e4m3(uint32_t a, uint32_t b, float f, uint32_t& one, uint32_t& rest) {
+// Two times two bf16 numbers times f as e4m3 codes, and what these leave of them as e5m2 codes.  Of the eight bits of a
+// number the first takes four, which leaves at most half of its last step: 0 to 8 sixteenths of it, exact in e5m2's three
+// bits.  e5m2, because its steps go down to 2^-16 where e4m3's end at 2^-9: with the rest in e4m3 too, one channel of q
+// 1000 times as loud as the others made outputs twice as far off as their bf16 rounding.
+__device__ __forceinline__ void split_q(uint32_t a, uint32_t b, float f, uint32_t& one, uint32_t& rest) {
   asm("{\n .reg .b16 l, h;\n .reg .b32 x, y, u, v;\n .reg .f32 e, f;\n"
       " shl.b32 u, %2, 16;\n and.b32 v, %2, 0xFFFF0000;\n mul.f32 e, u, %4;\n mul.f32 f, v, %4;\n cvt.rn.f16x2.f32 x, f, e;\n"
       " shl.b32 u, %3, 16;\n and.b32 v, %3, 0xFFFF0000;\n mul.f32 e, u, %4;\n mul.f32 f, v, %4;\n cvt.rn.f16x2.f32 y, f, e;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n cvt.rn.satfinite.e4m3x2.f16x2 h, y;\n mov.b32 %0, {l, h};\n"
       " cvt.rn.f16x2.e4m3x2 u, l;\n cvt.rn.f16x2.e4m3x2 v, h;\n sub.rn.f16x2 x, x, u;\n sub.rn.f16x2 y, y, v;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n cvt.rn.satfinite.e4m3x2.f16x2 h, y;\n mov.b32 %1, {l, h};\n}\n"
+      " cvt.rn.satfinite.e5m2x2.f16x2 l, x;\n cvt.rn.satfinite.e5m2x2.f16x2 h, y;\n mov.b32 %1, {l, h};\n}\n"
       : "=&r"(one), "=r"(rest)
       : "r"(a), "r"(b), "f"(f));
 }
@@ -319,36 +322,39 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k,
                  "r"(q), "r"(k), "r"(upper), "r"(id)
                  : "memory");
 }
-// The same of e4m3 codes, 32 elements a step; Q is the sum of two such tiles.
-#define CDB_S8(qoff, koff, acc)                                                                    \
+// The same of codes, 32 elements a step; Q is the sum of two tiles, of e4m3 (id) and of e5m2 (id5) codes.
+#define CDB_S8(qoff, koff, id, acc)                                                                \
   " add.u32 x, %1, " qoff ";\n mov.b64 da, {x, %3};\n add.u32 x, %2, " koff ";\n mov.b64 db, {x, %3};\n" \
-  " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %4, " acc ";\n"
+  " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, " id ", " acc ";\n"
+#define CDB_S8_ONE(off, acc) CDB_S8(off, off, "%4", acc)
+#define CDB_S8_REST(qoff, koff) CDB_S8(qoff, koff, "%5", "t")
 template <int STEPS>
-__device__ __forceinline__ void issue_scores_e4m3(uint32_t d, uint32_t q, uint32_t k, uint32_t upper, uint32_t id) {
+__device__ __forceinline__ void issue_scores_8(uint32_t d, uint32_t q, uint32_t k, uint32_t upper, uint32_t id, uint32_t id5) {
   static_assert(STEPS >= 1 && STEPS <= 4, "head dim");
   if constexpr (STEPS == 1)
-    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("1024", "0", "t") "}\n" ::"r"(d), "r"(q), "r"(k), "r"(upper), "r"(id)
+    asm volatile(CDB_SS_BEGIN CDB_S8_ONE("0", "f") CDB_S8_REST("1024", "0") "}\n" ::"r"(d), "r"(q), "r"(k), "r"(upper), "r"(id),
+                 "r"(id5)
                  : "memory");
   if constexpr (STEPS == 2)
-    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("1024", "0", "t") CDB_S8("1026", "2", "t")
+    asm volatile(CDB_SS_BEGIN CDB_S8_ONE("0", "f") CDB_S8_ONE("2", "t") CDB_S8_REST("1024", "0") CDB_S8_REST("1026", "2")
                      "}\n" ::"r"(d),
-                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 "r"(q), "r"(k), "r"(upper), "r"(id), "r"(id5)
                  : "memory");
   if constexpr (STEPS == 3)
-    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("4", "4", "t") CDB_S8("1024", "0", "t")
-                     CDB_S8("1026", "2", "t") CDB_S8("1028", "4", "t") "}\n" ::"r"(d),
-                 "r"(q), "r"(k), "r"(upper), "r"(id)
+    asm volatile(CDB_SS_BEGIN CDB_S8_ONE("0", "f") CDB_S8_ONE("2", "t") CDB_S8_ONE("4", "t") CDB_S8_REST("1024", "0")
+                     CDB_S8_REST("1026", "2") CDB_S8_REST("1028", "4") "}\n" ::"r"(d),
+                 "r"(q), "r"(k), "r"(upper), "r"(id), "r"(id5)
                  : "memory");
   if constexpr (STEPS == 4)
-    asm volatile(CDB_SS_BEGIN CDB_S8("0", "0", "f") CDB_S8("2", "2", "t") CDB_S8("4", "4", "t") CDB_S8("6", "6", "t")
-                     CDB_S8("1024", "0", "t") CDB_S8("1026", "2", "t") CDB_S8("1028", "4", "t") CDB_S8("1030", "6", "t")
+    asm volatile(CDB_SS_BEGIN CDB_S8_ONE("0", "f") CDB_S8_ONE("2", "t") CDB_S8_ONE("4", "t") CDB_S8_ONE("6", "t")
+                     CDB_S8_REST("1024", "0") CDB_S8_REST("1026", "2") CDB_S8_REST("1028", "4") CDB_S8_REST("1030", "6")
                          "}\n" ::"r"(d),
-                 "r"(q), "r"(k), "r"(upper), "r"(id)
+                 "r"(q), "r"(k), "r"(upper), "r"(id), "r"(id5)
                  : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A and B e4m3, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A e4m3 or e5m2, B e4m3, both K-major.
+__host__ __device__ constexpr uint32_t idesc_8(bool a_e5m2, int M, int N) {
+  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // O[tmem] (+)= P[tmem] V over up to eight pages of 16 keys.
 #define CDB_TS(n, a, off, acc)                                                              \
@@ -481,14 +487,14 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
       // of a job take its warp beyond that, they stand still.  So a job has one wait (lane 1 for the weights, lane 2 for
       // the next keys, the others for the values), one commit for the scores and one for a block's K and V, and few sums.
       // (A product with V that starts on the first 64 weights: 565 us for 552, 8192 tokens of 32/8 heads.)
-      constexpr uint32_t idS = Q8 ? idesc_e4m3(kRows, kKeys) : idesc_16(true, kRows, kKeys, false);
+      constexpr uint32_t idS = Q8 ? idesc_8(false, kRows, kKeys) : idesc_16(true, kRows, kKeys, false);
       constexpr uint32_t idO = idesc_16(!Q8, kRows, HD, true);
       const uint32_t q = (uint32_t)desc_k(su32(smem), 1024), k = (uint32_t)desc_k(su32(smem + G::OFF_K), 1024);
       const uint32_t v = (uint32_t)desc_mn(su32(smem + G::OFF_V), G::SLICE, 1024);
       const uint32_t up_k = (uint32_t)(desc_k(0, 1024) >> 32), up_v = (uint32_t)(desc_mn(0, G::SLICE, 1024) >> 32);
       auto scores = [&](int slot, int g) {
         const uint32_t d = tmem + G::S_COL + g * kKeys, qa = q + (two ? g : 0) * (G::QT / 16), ka = k + slot * (G::KB / 16);
-        if constexpr (Q8) issue_scores_e4m3<HD / 32>(d, qa, ka, up_k, idS);
+        if constexpr (Q8) issue_scores_8<HD / 32>(d, qa, ka, up_k, idS, idesc_8(true, kRows, kKeys));
         else issue_scores<HD / 16>(d, qa, ka, up_k, idS);
       };
       bool ok = true;
@@ -821,7 +827,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
           }
         } else {
           // e4m3: each row times a power of two, which takes its largest element into [128, 256), in two parts, what
-          // the first leaves in the second: four bits each, so that elements down to 2^-9 of it are exact.  A short loop:
+          // the first leaves in the second.  Elements from 2^-6 on, 2^-14 of the largest, are exact; of smaller ones the
+          // first part leaves up to 2^-10, and of that the second up to 2^-14, 2^-21 of the largest.  A short loop:
           // its instructions are fetched once for every item (unrolled: 5 us more).
           constexpr int B = L < 4 ? L : 4;
           uint4 piece[B];
@@ -848,8 +855,8 @@ __global__ void __launch_bounds__(Geo<HD, Q8>::THREADS, 1)
               }
               if (x == 0) q_up[tile * kRows + row_t] = its_up;
               uint32_t one[2], rest[2];
-              split_e4m3(piece[i].x, piece[i].y, down, one[0], rest[0]);
-              split_e4m3(piece[i].z, piece[i].w, down, one[1], rest[1]);
+              split_q(piece[i].x, piece[i].y, down, one[0], rest[0]);
+              split_q(piece[i].z, piece[i].w, down, one[1], rest[1]);
               if (x < P) {
                 const uint32_t at = su32(dst + row_t * 128) + (((x / 2) ^ (row_t & 7)) << 4) + (x & 1) * 8;
                 asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(one[0]), "r"(one[1]) : "memory");

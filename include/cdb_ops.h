@@ -262,8 +262,8 @@ int cdb_rotate(const cdb_rotate_args *a, void *stream);
  * undefined.  Softmax statistics and sums are fp32; weights enter the products
  * as 16-bit numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache,
  * one, weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
- * With an e4m3 cache a query's elements are exact down to 2^-8 of the head's largest
- * one, smaller ones within 2^-17 of that; a head with an infinite element counts as NaN.
+ * With an e4m3 cache a query's elements are exact down to 2^-14 of the head's largest
+ * one, smaller ones within 2^-21 of that; a head with an infinite element counts as NaN.
  * Keys and values that no row sees may hold anything.  Inside the stretch that
  * some rows of a request see and others do not, a value with an infinite or NaN
  * element makes the rows that see it NaN in all elements of the head, and does not
