@@ -275,8 +275,13 @@ __global__ void __launch_bounds__(128) k_rotate(const __grid_constant__ cdb_rota
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint64_t phase = a.steps[8 * u + j] * (uint64_t)(uint32_t)pos;
-      sincospif(__ll2float_rn((long long)phase) * 0x1p-63f, &s[j], &c[j]);
-      s[j] *= a.factor, c[j] *= a.factor;
+      // Whole quarters of a turn are taken off first: what is left, at most 1/4 half turn either way, rounds to fp32 by
+      // 2^-27 half turns at most (of a whole half turn 2^-25).
+      const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+      float sr, cr;
+      sincospif(__ll2float_rn((long long)(phase - ((uint64_t)quarter << 62))) * 0x1p-63f, &sr, &cr);
+      const float sq = quarter & 1 ? cr : sr, cq = quarter & 1 ? sr : cr;
+      s[j] = (quarter & 2 ? -sq : sq) * a.factor, c[j] = ((quarter + 1) & 2 ? -cq : cq) * a.factor;
     }
   }
   float gq[16], gk[16];

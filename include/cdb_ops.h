@@ -225,7 +225,8 @@ int cdb_plan_pages(const cdb_plan_pages_args *a, void *stream);
  * 2 is turned by the angle of 2 pi * (pos * steps[j] mod 2^64) / 2^64 and
  * multiplied by `factor`; elements behind rot_dim are left as they are.  A pair
  * is (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved.  Angles are exact sums of
- * a 64-bit fraction of a turn, whatever the position.
+ * a 64-bit fraction of a turn, whatever the position; sine and cosine are taken of
+ * its distance from the nearest quarter of a turn, rounded to fp32 (2.4e-8 at most).
  * out may be x itself; otherwise they do not overlap.  A row with pos < 0 is
  * padding: nothing of it is read or written. */
 typedef struct {
