@@ -258,17 +258,19 @@ int cdb_rotate(const cdb_rotate_args *a, void *stream);
  *                         visible[row][u / 64] for row u of the request (a tree's
  *                         nodes: its ancestors and itself).  Bits of rows that the
  *                         request does not have are ignored.
- * A row that sees nothing gives zeros.  Rows behind row_start[requests] are left as
- * they were.  Where row_start descends anywhere, CDB_OPS_BAD_ROW is set and `out` is
- * undefined.  Softmax statistics and sums are fp32; weights enter the products
- * as 16-bit numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache,
- * one, weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
+ * A row that sees nothing, or nothing with a score above -inf, gives zeros.  Rows
+ * behind row_start[requests] are left as they were.  Where row_start descends
+ * anywhere, CDB_OPS_BAD_ROW is set and `out` is undefined.
+ * Softmax statistics and sums are fp32; weights enter the products as 16-bit
+ * numbers: bf16 cache, two of them, within 2^-17 of the weight; e4m3 cache, one,
+ * weight times value scale, within 2^-11 of it or 2^-33 of the row's largest.
  * With an e4m3 cache a query's elements are exact down to 2^-14 of the head's largest
  * one, smaller ones within 2^-21 of that; a head with an infinite element counts as NaN.
- * Keys and values that no row sees may hold anything.  Inside the stretch that
- * some rows of a request see and others do not, a value with an infinite or NaN
- * element makes the rows that see it NaN in all elements of the head, and does not
- * touch the others.
+ * Keys and values that no row sees may hold anything.  A value with an infinite or
+ * NaN element makes that element infinite or NaN in the rows that see it, and may make
+ * the head's other elements NaN there (it does where its block of 128 keys is not
+ * seen whole by all rows of a tile); a value scale that is not finite does so to all
+ * elements of the head.  Rows that do not see it keep their bits.
  * Where a call has few rows for the GPU, keys are cut among CTAs and joined, by the
  * lengths of all its requests: this changes roundings, never from one run to the
  * next.  max_ctx costs nothing but that a call within 256 tokens is never cut.
