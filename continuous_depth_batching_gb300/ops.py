@@ -2,16 +2,19 @@
 
 For programs that drive the model themselves instead of through
 ``binding.Engine``.  Each class checks its arguments, keeps the argument
-structure and the output buffers of its operator, and enqueues one call on the
-current CUDA stream; nothing synchronizes, and every call can be captured into
-a CUDA graph.  An object's default outputs and its workspace are overwritten by
-its next call, so one object serves one stream at a time.  It may be called on
-other streams than the one it was made on, and dropped while a call is in
-flight: its own memory (default outputs, status, workspace) waits for every
-stream that called it.  A graph that captured its calls needs the object for as
-long as it is replayed.  Tensors that the caller gives are the caller's to
-order and to keep.  An object works on the device that was current when it was
-made; no gradients are recorded.
+structure of its operator, its workspace and what it returns (the tokens of
+Sampler, the rows of PagePlanner), and enqueues one call on the current CUDA
+stream; nothing synchronizes, and every call can be captured into a CUDA graph.
+What an object keeps is overwritten by its next call, so one object serves one
+stream at a time.  CacheWriter and the attentions keep no output: without q_out
+or out they allocate a new tensor of zeros in every call, which costs a pass
+over it (8192 rows of 32 heads of 128: 67 MB), so give one where time counts.
+An object may be called on other streams than the one it was made on, and
+dropped while a call is in flight: its own memory (what it returns, status,
+workspace) waits for every stream that called it.  A graph that captured its
+calls needs the object for as long as it is replayed.  Tensors that the caller
+gives are the caller's to order and to keep.  An object works on the device
+that was current when it was made; no gradients are recorded.
 """
 
 from __future__ import annotations
@@ -629,7 +632,7 @@ def rope_steps(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained=None,
     further than a model was trained: "linear": positions divided by factor; "base": theta times
     factor^(rot_dim / (rot_dim - 2)), so that the slowest pair turns factor times slower; "parts": a pair that
     turns fewer than `low` times over `trained` positions turns factor times slower, one of more than `high` as before,
-    a linear ramp between them, and cos and sin are multiplied by 0.1 ln(factor) + 1, the factor returned (else 1)."""
+    a linear ramp between them in the number of turns (not in j, as some checkpoints have it), and cos and sin are multiplied by 0.1 ln(factor) + 1, the factor returned (else 1)."""
     import torch
     if rot_dim < 2 or rot_dim % 2 or theta <= 0 or factor < 1 or scaling not in ("none", "linear", "base", "parts"):
         raise ValueError(f"rot_dim {rot_dim}, theta {theta}, scaling {scaling!r}, factor {factor}")
