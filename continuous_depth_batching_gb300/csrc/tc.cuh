@@ -24,9 +24,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
 }
-// Wait for the phase of the given parity; false after ~2 s of global time.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = su32(bar);
+// Wait for the phase of the given parity of the barrier at a shared-memory address; false after ~2 s of global time.
+__device__ __forceinline__ bool wait_at(uint32_t a, uint32_t parity) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
     uint32_t ok;
@@ -44,25 +43,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
   }
 }
-// The same by shared-memory address.
-__device__ __forceinline__ bool wait_at(uint32_t a, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((it & 63) == 63) {
-      uint64_t t;
-      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-      if (t0 == 0) t0 = t;
-      else if (t - t0 > 2000000000ull) return false;
-    }
-  }
-}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) { return wait_at(su32(bar), parity); }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
                                        uint64_t pol) {
   asm volatile(
