@@ -38,9 +38,10 @@
 // What bounds it.  A long bf16 prompt: the tensor cores, which compute three products of 512 cycles for a job (one
 // for the scores, two for weights in two parts), together with the waits and commits of the warp that feeds them
 // (8192 tokens of 32/8 heads: 555 us, 1.0 PFLOP/s of causal products; of 547 before, the products alone took 472 and
-// softmax alone 444; pipe 63% active).  Drafts over long bf16 caches: HBM (32 drafts of 16 tokens behind 16000: 5.3 of 6.8 TB/s).  e4m3: the
-// chain from scores to weights to the next scores, in which a key's scales are read from shared memory by every thread
-// (the same drafts: 2.4 TB/s).  Short calls: setup, one chain of loads and the join.
+// softmax alone 444; pipe 63% active).  Drafts over long bf16 caches: HBM (32 drafts of 16 tokens
+// behind 16000: 4.8 of 6.7 TB/s for the call, 5.3 over the growth from 4000 tokens).  e4m3: the chain from scores to
+// weights to the next scores, in which a key's scales are read from shared memory by every thread (the same drafts: 2.2
+// TB/s, 2.4 over the growth).  Short calls: setup, one chain of loads and the join.
 // Every mbarrier wait is bounded; on expiry the kernel reports CDB_OPS_TIMEOUT,
 // lets its copies and MMAs finish (bounded), frees TMEM and returns.
 #include <algorithm>
@@ -66,8 +67,10 @@ constexpr int kSms = 152;
 // 183, one and a half or two 177 to 180 for the drafts).
 constexpr int kItems = kSms;
 constexpr int kMinBlocks = 2;  // blocks of a cut item, at least (8 nodes behind 1000 tokens: 15.9 us, with four 20.8)
-// Items without cutting, from which on no call cuts: SMs are busy then.  Half as many: 2500 tokens of 32/8 heads 84 us for
-// 88, 4096 tokens 171 for 176, chunks behind cached tokens 150 for 147; twice as many: 6000 tokens 334 for 323.
+// Items without cutting, from which on no call cuts: SMs are busy then.  It depends on the lengths: equal ones prefer
+// half as many (of 32/8 heads: 2500 tokens 85 us for 89, 3300 122 for 131, 4096 173 for 177, five chunks of 600 behind 1500
+// 143 for 151), uneven ones do not (five chunks of 100 to 1100 behind up to 3000, bf16 133 for 121, e4m3 151 for 147; 44
+// e4m3 drafts 278 for 263), and of twice as many 20 uneven chunks take 202 for 225, but 6000 tokens 336 for 325.
 constexpr int kCutBelow = 4 * kSms;
 
 template <int HD, bool Q8>
@@ -144,7 +147,8 @@ __device__ __forceinline__ bool look(const Args& A, int i, Item& it, bool tell) 
 // A request's keys are cut into equal ranges of at most `cb` blocks, such that kItems items would
 // hold all of the call's.
 // Up to 32 requests: every warp by itself, without a barrier; where keys are cut, requests of
-// longer ranges come first, so that the last CTAs to run are short.
+// longer ranges come first, so that the last CTAs to run are short.  Beyond: all warps, in the caller's order (drafts over
+// 500 to 8000 e4m3 keys: 32 requests 152 us, 33 214).
 __device__ __forceinline__ Item find_item_warp(const Args& A, int y) {
   const cdb_prompt_attention_args& a = A.a;
   const int lane = threadIdx.x & 31, step = 2 * A.tokens;

@@ -64,7 +64,7 @@ __device__ __forceinline__ void find(const int* (&start)[N], int (&x)[N], int n,
 // part of the rows and pages, found by bisection in shared memory.  Nothing is
 // written before every CTA has read lens and state, which outputs may be.
 // Latency bounds it: the chain of loads, sums, barrier, lookups and stores (64 requests
-// 4.3 us, 1000 with 18000 rows 9.5; those in clusters of four CTAs 16).
+// 4.1 us, 1000 with 21702 rows 9.7; those in clusters of four CTAs 16).
 template <int B>  // rows of a thread at a time
 __global__ void __launch_bounds__(kThreads) k_plan_pages(const __grid_constant__ cdb_plan_pages_args a, int ctas) {
   extern __shared__ int dyn[];
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) k_plan_pages(const __grid_constant__
                  tail_at = (unsigned)((unsigned long long)tail % slots);
   auto ring = [&](unsigned from, unsigned k) { return from + k < slots ? from + k : from + k - slots; };  // k < slots
   // Rows, blocks taken and blocks given go by side by side: their lookups and loads do not wait for one another (1000
-  // requests with 18000 rows: 11.5 us one after the other, 9.6 four rows at a time).
+  // requests with 21702 rows: 11.5 us one after the other, 9.6 four rows at a time).
   const int taken = ok ? (int)total[1] : 0, given = ok ? (int)total[2] : 0, most = max(a.max_rows, max(B * taken, B * given));
   for (int k = 0; k < most; k += B * step) {
     int i[B], seq[B], pos[B], block[B];
@@ -248,9 +248,9 @@ __device__ __forceinline__ void store16(T* p, int second, const float* v) {
 // each.  A lane's eight angles are the same for every head, so their sines and
 // cosines are computed once: pos * step wraps around at whole turns, which
 // leaves the exact fraction, whatever the position.  A row's angles, the
-// norm's sums and loads come one after the other in a warp, which with HBM bounds it (8192
-// rows of 40 heads of 128, bf16, with norm: 40 us, 4.2 of 6.8 TB/s; four heads of a lane on
-// their way 38 us, but 500 such rows without norm 5.8 for 5.1).
+// norm's sums and loads come one after the other in a warp, of which 16 fit an SM (120 registers); that
+// bounds it (8192 rows of 40 heads of 128 with norm, bf16 40 us, 4.2 of 6.7 TB/s, fp32 56, 6.0; four heads of
+// a lane on their way 38 us in bf16, but 500 such rows without norm 5.8 for 5.1).
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_rotate(const __grid_constant__ cdb_rotate_args a, int heads_per_warp, int parts) {
   constexpr int G = HD == 96 ? 8 : HD / 16;  // lanes of a head; of 96 elements, six lanes work
@@ -373,8 +373,9 @@ constexpr int kThreads = 256;
 // A thread owns 16 bytes of a (slot, K or V, head) row, or a scale, and takes
 // them along the path.  The path ascends, so what is overwritten was read before
 // (entry k goes to k <= path[k], and no later entry comes from there): loads of
-// several entries may run ahead of their stores.  HBM bounds it (half of its rate: 16 paths of
-// 96 slots 14 us), or the latency of one load and one store (one path of 4 slots: 1.7 us).
+// several entries may run ahead of their stores.  16 paths of 96 slots from HBM: 14.3 us, half of
+// the copy rate (64 registers: four CTAs of an SM at a time, each with a chain of lookups before its first load);
+// one path of 4 slots: 1.6 us, the latency of those, one load and one store.
 __global__ void __launch_bounds__(kThreads) k_keep_path(const __grid_constant__ cdb_keep_path_args a) {
   __shared__ long long from[CDB_DRAFT_MAX], to[CDB_DRAFT_MAX];  // 16 * block + offset, past 32 bits in large pools
   __shared__ int moves;
@@ -450,7 +451,7 @@ cudaError_t launch_keep_path(cudaStream_t s, const cdb_keep_path_args& a) {
   const cdb_paged_cache& c = a.cache;
   const long long heads = (long long)c.n_kv_slots * 2 * c.n_kv_heads;
   const long long pieces = heads * (c.head_dim * (c.dtype == CDB_BF16 ? 2 : 1) / 16 + (c.dtype == CDB_E4M3));
-  // Eight CTAs for each SM: a CTA's look at the path is shared by several pieces of its threads (16 paths of 96 slots,
+  // Eight CTAs for each SM, of which four fit at a time: a CTA's look at the path is shared by several pieces of its threads (16 paths of 96 slots,
   // from HBM: 18.5 us with a CTA for every 256 pieces, 14.3 so).
   const unsigned x = (unsigned)std::min((pieces + keep::kThreads - 1) / keep::kThreads, std::max(1ll, 152ll * 8 / a.requests));
   count_launch();

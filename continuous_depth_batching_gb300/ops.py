@@ -632,7 +632,8 @@ def rope_steps(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained=None,
     further than a model was trained: "linear": positions divided by factor; "base": theta times
     factor^(rot_dim / (rot_dim - 2)), so that the slowest pair turns factor times slower; "parts": a pair that
     turns fewer than `low` times over `trained` positions turns factor times slower, one of more than `high` as before,
-    a linear ramp between them in the number of turns (not in j, as some checkpoints have it), and cos and sin are multiplied by 0.1 ln(factor) + 1, the factor returned (else 1)."""
+    a linear ramp between them in the number of turns (not in j, as some checkpoints have it), and cos and sin are
+    multiplied by 0.1 ln(factor) + 1, the factor returned (else 1)."""
     import torch
     if rot_dim < 2 or rot_dim % 2 or theta <= 0 or factor < 1 or scaling not in ("none", "linear", "base", "parts"):
         raise ValueError(f"rot_dim {rot_dim}, theta {theta}, scaling {scaling!r}, factor {factor}")

@@ -191,7 +191,8 @@ size_t cdb_attention_workspace(int rows, int n_heads, int n_kv_heads, int head_d
  * lens_out[i] is the new length and state_out the new counters; they may be lens
  * and state themselves.  Rows from row_start[requests] to max_rows - 1 are padding:
  * row_seq, row_pos and row_slot -1.  Table entries behind a sequence's last page
- * are left as they were.  A sequence is named by one request at most.
+ * are left as they were.  A sequence is named by one request at most, but for
+ * requests with lens and new_tokens 0, which do nothing (padding).
  * A call that cannot be served in full changes nothing: it sets a status bit
  * (CDB_OPS_NO_BLOCKS; CDB_OPS_NO_ROWS; CDB_OPS_BAD_ROW: a sequence, length or
  * counter out of range, or pages past max_blocks), lens_out and state_out are as
